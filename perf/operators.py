@@ -258,7 +258,7 @@ def _run_own(s):
             got["dlogits"] = nv.nvfp4_route_bwd(s["logits"], p, s["dweight"], mode)
         return got
     p = s["plan"]
-    xe = nv.nvfp4_dispatch(s["x"], p["source"], case["top"])
+    xe = nv.nvfp4_dispatch(s["x"], p["row"], p["source"])
     y = nv.nvfp4_combine(s["out"], p["row"], p["weight"])
     dout, dweight = nv.nvfp4_combine_bwd(s["dy"], s["out"], p["row"], p["source"], p["weight"])
     dx = nv.nvfp4_combine(s["dxe"], p["row"])
