@@ -192,7 +192,8 @@ def prepare(case, seed):
         s["w_pre"] = 1 + 0.2 * torch.randn(d, generator=g, device="cuda")
         s["gate"] = None
         if case["gate"] != "none":
-            s["gate"] = torch.rand(d if case["gate"] == "channel" else t, generator=g, device="cuda")
+            shape = (d,) if case["gate"] == "channel" else (t, 1)
+            s["gate"] = torch.rand(*shape, generator=g, device="cuda")
         if case["back"]:
             s["dy"] = torch.randn(t, d, generator=g, device="cuda").to(kind)
             s["dh"] = torch.randn(t, d, generator=g, device="cuda").bfloat16()
@@ -304,14 +305,9 @@ def _plain_wgrad(s):
     return s["d"].add_(d) if s["case"]["fold"] else d.bfloat16()
 
 
-def _gate(s):
-    if s["gate"] is None:
-        return 1.0
-    return s["gate"] if s["case"]["gate"] == "channel" else s["gate"].unsqueeze(1)
-
-
 def _plain_norm(s):
-    x, z, g = s["x"].float(), s["z"].float(), _gate(s)
+    x, z = s["x"].float(), s["z"].float()
+    g = 1.0 if s["gate"] is None else s["gate"]
     rz = torch.rsqrt(z.square().mean(1, keepdim=True) + EPS)
     zn = z * rz
     y = x + 0.5 * (g * (zn * s["w_post"]))
@@ -326,7 +322,8 @@ def _plain_norm(s):
     q = 0.5 * dy
     dgate = None
     if s["gate"] is not None:
-        dgate = (q * zn * s["w_post"]).sum(0 if s["case"]["gate"] == "channel" else 1)
+        dgate = q * zn * s["w_post"]
+        dgate = dgate.sum(0) if s["case"]["gate"] == "channel" else dgate.sum(1, keepdim=True)
     dn = q * g
     dw_post = (dn * zn).sum(0)
     v = dn * s["w_post"]
@@ -447,8 +444,6 @@ def _exact_norm(s):
     leaf = {k: s[k].double().requires_grad_(back) for k in ("x", "z", "w_post", "w_pre", "gate")
             if s[k] is not None}
     gate = leaf.get("gate", torch.ones((), dtype=torch.float64, device="cuda"))
-    if s["case"]["gate"] == "row":
-        gate = gate[:, None]
     norm = lambda v, w: v / torch.sqrt((v * v).mean(-1, keepdim=True) + EPS) * w  # noqa: E731
     y = leaf["x"] + 0.5 * gate * norm(leaf["z"], leaf["w_post"])
     h = norm(y, leaf["w_pre"])
