@@ -501,6 +501,167 @@ enum { NVFP4_ZERO_GRAD = 16u };
 nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t flags, float* amax,
                             void* workspace, size_t workspace_bytes, nvfp4_stream stream);
 
+/* ---------------------------------------------------------------------- */
+/* Mixture of experts: routing, grouped products, norms                     */
+/* ---------------------------------------------------------------------- */
+/* The pages describe a dense MLP; these calls build the mixture-of-experts
+ * form of it from the same quantisers and NVFP4 operands.  A block is
+ *   nvfp4_residual_norm_fwd -> nvfp4_route_fwd -> nvfp4_dispatch ->
+ *   quantise, nvfp4_group_gemm (gate, up), nvfp4_swiglu_fwd, quantise,
+ *   nvfp4_group_gemm (down) -> nvfp4_combine -> nvfp4_residual_norm_fwd.
+ *
+ * Groups: expert e owns rows offsets[e] .. offsets[e] + sizes[e] - 1 of a
+ * [rows, .] tensor.  The offsets are multiples of 128 (the rows of a scale
+ * atom), rows is a multiple of 128, and the rows of a group's last block of
+ * 128 past its size, and those from offsets[groups] on, are padding, which
+ * every producer here writes as zero.  sizes [groups] and offsets
+ * [groups + 1] are device int32 arrays: nothing of a plan is known to the
+ * host, so a whole block can be captured into a graph. */
+
+/* How the weights of the chosen experts are normalised. */
+enum {
+  NVFP4_ROUTE_ALL = 0,   /* softmax over all experts, the chosen ones' entries kept */
+  NVFP4_ROUTE_CHOSEN = 1 /* softmax over the chosen experts                         */
+};
+
+/* *rows = the rows of a plan's tensors, a multiple of 128 that holds every
+ * assignment of `tokens` tokens to `top` of `experts` experts:
+ * floor((n + 127 min(experts, n)) / 128) 128 with n = tokens top; source has
+ * as many entries.  *workspace_bytes = what nvfp4_route_fwd needs.  Either may
+ * be NULL.  NVFP4_ERR_SHAPE unless tokens >= 1, 1 <= experts <= 512,
+ * 1 <= top <= min(16, experts) and *rows <= INT32_MAX. */
+nvfp4_status nvfp4_route_sizes(int64_t tokens, int64_t experts, int32_t top, int64_t* rows,
+                               size_t* workspace_bytes);
+
+/* Routes each token to `top` experts by its logits [tokens, experts] (bf16 or
+ * FP32, leading dimension ld elements): the largest logits, the largest first,
+ * the lowest index among equals.  A logit of -inf or NaN is never chosen;
+ * +inf counts as the largest finite value.  Outputs (device, caller-owned):
+ *   expert [tokens, top] int32  the chosen experts; -1 in the slots of a token
+ *                               with fewer than `top` logits to choose from
+ *   weight [tokens, top] float  their weights (mode NVFP4_ROUTE_*), 0 for -1
+ *   sizes [experts], offsets [experts + 1] int32   the groups
+ *   row [tokens, top] int32     the row of each slot among the groups, -1 for -1
+ *   source [rows] int32         the slot (token top + j) of each row, -1: padding
+ * A group's rows are in the order of the slots.  The result is the same on
+ * every call.  workspace: device, 4-byte aligned, >= nvfp4_route_sizes gives.
+ * One launch up to 128 tokens, else two.  Returns NVFP4_ERR_INVALID_ARG,
+ * _SHAPE, _ALIGN, _WORKSPACE, _ARCH, _CUDA. */
+nvfp4_status nvfp4_route_fwd(const void* logits, int32_t in_dtype, int64_t tokens,
+                             int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                             int32_t* expert, float* weight, int32_t* sizes, int32_t* offsets,
+                             int32_t* row, int32_t* source, void* workspace,
+                             size_t workspace_bytes, nvfp4_stream stream);
+
+/* dlogits [tokens, experts] (contiguous, the logits' type) from dweight
+ * [tokens, top]: w_i sum_j w_j (dw_i - dw_j) over a token's slots, with
+ * NVFP4_ROUTE_ALL also the unchosen experts' share; exact zeros where an
+ * expert could not be chosen.  expert, weight: as nvfp4_route_fwd wrote them
+ * for the same logits and mode.  One launch. */
+nvfp4_status nvfp4_route_bwd(const void* logits, int32_t in_dtype, int64_t tokens,
+                             int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                             const int32_t* expert, const float* weight, const float* dweight,
+                             void* dlogits, nvfp4_stream stream);
+
+/* xe [rows, cols] bf16: row row[t, j] is x[t], x bf16 [tokens, cols]; rows whose
+ * source is -1 are zero.  cols % 8 == 0, all tensors contiguous and 16-byte
+ * aligned.  Entries of `row` outside [0, rows) are skipped.  The gradient is
+ * nvfp4_combine without weights.  One launch. */
+nvfp4_status nvfp4_dispatch(const void* x, const int32_t* row, const int32_t* source,
+                            int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* xe,
+                            nvfp4_stream stream);
+
+/* y[t] = sum_j weight[t, j] o[row[t, j]] (weight NULL: all ones) in FP32,
+ * rounded once to bf16; a token without rows gets zeros.  Shapes as
+ * nvfp4_dispatch. */
+nvfp4_status nvfp4_combine(const void* o, const int32_t* row, const float* weight,
+                           int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* y,
+                           nvfp4_stream stream);
+
+/* The gradients of nvfp4_combine from dy bf16 [tokens, cols]: d_o [rows, cols]
+ * bf16, row row[t, j] is weight[t, j] dy[t] and padding rows are zero;
+ * dweight[t, j] = sum_c dy[t, c] o[row[t, j], c] (0 for a slot without a row).
+ * d_o may not be o.  One launch. */
+nvfp4_status nvfp4_combine_bwd(const void* dy, const void* o, const int32_t* row,
+                               const int32_t* source, const float* weight, int64_t tokens,
+                               int64_t cols, int32_t top, int64_t rows, void* d_o,
+                               float* dweight, nvfp4_stream stream);
+
+/* Products grouped by expert: D[r, :] = alpha A[r, :] . B_e^T for the rows r of
+ * group e, alpha = *A->s_dec * *B->s_dec.  A [rows, K] is a row-wise operand.
+ *   b_view 0: B [groups * N, K], expert e's weights in rows e N .. (FPROP)
+ *   b_view 1: B [groups * K, N] quantised 16x16 with NVFP4_EMIT_T, expert e in
+ *             rows e K ..; codes_t / scales_t are read (DGRAD)
+ * d_mode NVFP4_D_BF16 or NVFP4_D_BF16_ADD_C (adds C bf16 [rows, N] in FP32
+ * before the rounding).  D bf16 [rows, N]: padding rows are written as zero
+ * whatever A (or C) holds there.  Shapes: rows % 128 == 0, N % 128 == 0,
+ * K % 64 == 0, 1 <= groups <= 512.  A group that does not lie in [0, rows) or
+ * does not start on a multiple of 128 counts as empty.  One launch.  Returns
+ * NVFP4_ERR_INVALID_ARG, _SHAPE, _ALIGN, _ARCH, _CUDA. */
+nvfp4_status nvfp4_group_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
+                              const int32_t* sizes, const int32_t* offsets, int32_t groups,
+                              void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
+                              int64_t K, nvfp4_stream stream);
+
+/* Weight gradients grouped by expert: D_e [M, N] = alpha A[:, rows of e] .
+ * B[:, rows of e]^T for A [M, rows], B [N, rows] column-wise operands
+ * (NVFP4_COL_1X16 of the [rows, M] and [rows, N] tensors, with the RHT on both
+ * or on neither); the padding rows of those tensors must have been zero.
+ *   NVFP4_D_BF16       D bf16 [groups, M, N], zeros for an empty group
+ *   NVFP4_D_F32_ACCUM  D fp32 [groups, M, N] += the FP32 product, not rounded
+ *                      to bf16 in between (an empty group's D stays as it is)
+ * Shapes: rows, M, N multiples of 128, 1 <= groups <= 512.  One launch. */
+nvfp4_status nvfp4_group_wgrad(const nvfp4_tensor* A, const nvfp4_tensor* B,
+                               const int32_t* sizes, const int32_t* offsets, int32_t groups,
+                               void* D, int32_t d_mode, int64_t M, int64_t N, int64_t rows,
+                               nvfp4_stream stream);
+
+/* The gate of a block's output in nvfp4_residual_norm_*. */
+enum {
+  NVFP4_GATE_NONE = 0,
+  NVFP4_GATE_CHANNEL = 1, /* gate [cols] */
+  NVFP4_GATE_ROW = 2      /* gate [rows] */
+};
+typedef struct nvfp4_norm_params {
+  int64_t rows, cols;
+  int32_t stream_dtype; /* nvfp4_in_dtype of x, y, dy, dx                */
+  int32_t gate_mode;    /* NVFP4_GATE_*                                  */
+  float eps;            /* > 0                                           */
+  float x_scale;        /* a, of the residual stream                     */
+  float z_scale;        /* b, of the block's output                      */
+} nvfp4_norm_params;
+
+/* The norms after a block and before the next one in one pass:
+ *   y = a x + b g (.) (z r_z w_post),   h = y r_y w_pre,
+ *   r_v = (mean over the row of v^2 + eps)^(-1/2),
+ * x the residual stream [rows, cols], z (bf16) the block's output, h (bf16)
+ * the next block's input; w_post, w_pre, gate FP32.  y is rounded once when
+ * stored, h comes from y before that rounding.  y may be x.
+ * z NULL (with w_post NULL): y = a x, the first block's norm, y may be NULL
+ * then; w_pre NULL (with h NULL): no norm follows.
+ * cols % 8 == 0, cols <= 65536; all tensors contiguous and 16-byte aligned (a
+ * row gate: 4-byte).  One launch.  Returns NVFP4_ERR_INVALID_ARG, _SHAPE,
+ * _ALIGN, _ARCH, _CUDA. */
+nvfp4_status nvfp4_residual_norm_fwd(const nvfp4_norm_params* p, const void* x, const void* z,
+                                     const float* w_post, const float* gate, const float* w_pre,
+                                     void* y, void* h, nvfp4_stream stream);
+
+/* Its gradients from dy (NULL: zero) and dh (NULL exactly when w_pre is):
+ * dx (the stream's type), dz bf16, and FP32 dw_post [cols], dgate (the gate's
+ * shape), dw_pre [cols], written, not accumulated; an output is NULL exactly
+ * when its input is.  Everything is recomputed from x and z: nothing of the
+ * forward is kept.  dx may be dy, dz may be dh or z.  workspace: device,
+ * 16-byte aligned, at least nvfp4_residual_norm_bwd_sizes gives.  Two
+ * launches; sums are taken in a fixed order.  Statuses as the forward and
+ * _WORKSPACE. */
+nvfp4_status nvfp4_residual_norm_bwd_sizes(int64_t rows, int64_t cols, size_t* workspace_bytes);
+nvfp4_status nvfp4_residual_norm_bwd(const nvfp4_norm_params* p, const void* dy, const void* dh,
+                                     const void* x, const void* z, const float* w_post,
+                                     const float* gate, const float* w_pre, void* dx, void* dz,
+                                     float* dw_post, float* dgate, float* dw_pre,
+                                     void* workspace, size_t workspace_bytes,
+                                     nvfp4_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -7,6 +7,7 @@ built, importing this module raises -- there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 from dataclasses import dataclass, field
 
@@ -41,6 +42,13 @@ class Tensor(C.Structure):
                 ("scales_t", C.c_void_p), ("amax", C.c_void_p), ("s_dec", C.c_void_p),
                 ("rows", C.c_int64), ("cols", C.c_int64), ("mode", C.c_int32),
                 ("flags", C.c_uint32)]
+
+
+class NormParams(C.Structure):
+    """Mirror of ``nvfp4_norm_params``."""
+    _fields_ = [("rows", C.c_int64), ("cols", C.c_int64), ("stream_dtype", C.c_int32),
+                ("gate_mode", C.c_int32), ("eps", C.c_float), ("x_scale", C.c_float),
+                ("z_scale", C.c_float)]
 
 
 class MlpParams(C.Structure):
@@ -88,6 +96,21 @@ def _load():
         "nvfp4_mlp_tensor": ([i64, i64, i64, vp, vp, i32, P(vp), P(i64), P(i64)], C.c_int),
         "nvfp4_mlp_operand": ([i64, i64, i64, vp, vp, i32, P(Tensor)], C.c_int),
         "nvfp4_sgd_step": ([vp, vp, i64, C.c_float, u32, vp, vp, sz, vp], C.c_int),
+        "nvfp4_route_sizes": ([i64, i64, i32, P(i64), P(sz)], C.c_int),
+        "nvfp4_route_fwd": ([vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                            C.c_int),
+        "nvfp4_route_bwd": ([vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp], C.c_int),
+        "nvfp4_dispatch": ([vp, vp, vp, i64, i64, i32, i64, vp, vp], C.c_int),
+        "nvfp4_combine": ([vp, vp, vp, i64, i64, i32, i64, vp, vp], C.c_int),
+        "nvfp4_combine_bwd": ([vp, vp, vp, vp, vp, i64, i64, i32, i64, vp, vp, vp], C.c_int),
+        "nvfp4_group_gemm": ([P(Tensor), P(Tensor), i32, vp, vp, i32, vp, i32, vp, i64, i64, i64,
+                              vp], C.c_int),
+        "nvfp4_group_wgrad": ([P(Tensor), P(Tensor), vp, vp, i32, vp, i32, i64, i64, i64, vp],
+                              C.c_int),
+        "nvfp4_residual_norm_fwd": ([P(NormParams), vp, vp, vp, vp, vp, vp, vp, vp], C.c_int),
+        "nvfp4_residual_norm_bwd_sizes": ([i64, i64, P(sz)], C.c_int),
+        "nvfp4_residual_norm_bwd": ([P(NormParams), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                     vp, sz, vp], C.c_int),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(L, name)
@@ -482,6 +505,339 @@ def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool 
                               workspace.numel() if workspace is not None else 0,
                               _stream(stream)), "nvfp4_sgd_step")
     return W
+
+
+# ---- mixture of experts ------------------------------------------------------
+ROUTE_ALL, ROUTE_CHOSEN = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_ROW = 0, 1, 2
+_DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
+
+
+def _want(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _cuda(t, dtype, name, shape=None):
+    """A contiguous CUDA tensor of one type (and shape)."""
+    _want(t.is_cuda and t.dtype == dtype and t.is_contiguous(),
+          f"{name} must be a contiguous {dtype} CUDA tensor")
+    if shape is not None:
+        _want(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
+
+
+def operand(codes: torch.Tensor, scales: torch.Tensor, s_dec: torch.Tensor, rows: int,
+            cols: int) -> QTensor:
+    """A QTensor over buffers that hold a K-major operand [rows, cols] already:
+    codes and scales (MMA layout) as uint8, s_dec one float32."""
+    cb, sb, _, _ = quantize_sizes(rows, cols, ROW_1X16)
+    _cuda(codes, torch.uint8, "codes")
+    _cuda(scales, torch.uint8, "scales")
+    _cuda(s_dec, torch.float32, "s_dec")
+    _want(codes.numel() >= cb and scales.numel() >= sb and s_dec.numel() >= 1,
+          "buffers smaller than the operand")
+    q = QTensor(codes=codes, scales=scales, amax=None, s_dec=s_dec)
+    q.desc = Tensor(codes.data_ptr(), scales.data_ptr(), None, None, None, s_dec.data_ptr(), rows,
+                    cols, ROW_1X16, 0)
+    return q
+
+
+def operand_t(codes_t: torch.Tensor, scales_t: torch.Tensor, s_dec: torch.Tensor, rows: int,
+              cols: int) -> QTensor:
+    """A QTensor over the transposed view alone (codes_t / scales_t hold the
+    K-major operand [cols, rows]) of a 16x16 quantisation of [rows, cols]: what
+    b_view 1 of the products reads."""
+    q = operand(codes_t, scales_t, s_dec, cols, rows)
+    q.codes_t, q.scales_t, q.codes, q.scales = codes_t, scales_t, None, None
+    q.desc = Tensor(None, None, codes_t.data_ptr(), scales_t.data_ptr(), None, s_dec.data_ptr(),
+                    rows, cols, BLOCK_16X16, EMIT_T)
+    return q
+
+
+def route_sizes(tokens, experts, top):
+    """(rows of a plan, workspace bytes of nvfp4_route_fwd)."""
+    r, w = C.c_int64(), C.c_size_t()
+    _check(lib.nvfp4_route_sizes(tokens, experts, top, C.byref(r), C.byref(w)),
+           "nvfp4_route_sizes")
+    return r.value, w.value
+
+
+@dataclass
+class RoutePlan:
+    """The outputs of nvfp4_route_fwd (see nvfp4.h)."""
+    expert: torch.Tensor   # int32 [tokens, top]
+    weight: torch.Tensor   # float32 [tokens, top]
+    sizes: torch.Tensor    # int32 [experts]
+    offsets: torch.Tensor  # int32 [experts + 1]
+    row: torch.Tensor      # int32 [tokens, top]
+    source: torch.Tensor   # int32 [rows]
+
+    @property
+    def rows(self):
+        return self.source.numel()
+
+
+def alloc_plan(tokens, experts, top, device="cuda") -> RoutePlan:
+    rows, _ = route_sizes(tokens, experts, top)
+    i = dict(dtype=torch.int32, device=device)
+    return RoutePlan(expert=torch.empty(tokens, top, **i),
+                     weight=torch.empty(tokens, top, dtype=torch.float32, device=device),
+                     sizes=torch.empty(experts, **i), offsets=torch.empty(experts + 1, **i),
+                     row=torch.empty(tokens, top, **i), source=torch.empty(rows, **i))
+
+
+def _on_stream(call):
+    """Runs a call with its `stream` as the current one, so that what it
+    allocates (outputs, a workspace) belongs to the stream that uses it."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return run
+
+
+def _logits(logits):
+    _want(logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1,
+          "logits must be a 2-D CUDA tensor with unit column stride")
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"logits must be bf16 or fp32, got {logits.dtype}")
+    tokens, experts = logits.shape
+    return tokens, experts, logits.stride(0) if tokens > 1 else experts
+
+
+@_on_stream
+def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
+                    plan: RoutePlan | None = None, workspace: torch.Tensor | None = None) -> RoutePlan:
+    """Choose each token's `top` experts and order the rows by expert (see
+    nvfp4_route_fwd in nvfp4.h)."""
+    tokens, experts, ld = _logits(logits)
+    rows, wsb = route_sizes(tokens, experts, top)
+    if plan is None:
+        plan = alloc_plan(tokens, experts, top, logits.device)
+    else:
+        for name, shape in (("expert", (tokens, top)), ("row", (tokens, top)),
+                            ("sizes", (experts,)), ("offsets", (experts + 1,)),
+                            ("source", (rows,))):
+            _cuda(getattr(plan, name), torch.int32, name, shape)
+        _cuda(plan.weight, torch.float32, "weight", (tokens, top))
+    if workspace is None:
+        workspace = _workspace(wsb, logits.device)
+    _check(lib.nvfp4_route_fwd(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, ld, top,
+                               mode, plan.expert.data_ptr(), plan.weight.data_ptr(),
+                               plan.sizes.data_ptr(), plan.offsets.data_ptr(),
+                               plan.row.data_ptr(), plan.source.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), _stream(None)), "nvfp4_route_fwd")
+    return plan
+
+
+@_on_stream
+def nvfp4_route_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor,
+                    mode: int = ROUTE_CHOSEN, dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient from that of the plan's weights."""
+    tokens, experts, ld = _logits(logits)
+    top = plan.expert.shape[1]
+    _cuda(plan.expert, torch.int32, "expert", (tokens, top))
+    _cuda(plan.weight, torch.float32, "weight", (tokens, top))
+    _cuda(dweight, torch.float32, "dweight", (tokens, top))
+    if dlogits is None:
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    else:
+        _cuda(dlogits, logits.dtype, "dlogits", (tokens, experts))
+    _check(lib.nvfp4_route_bwd(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, ld, top,
+                               mode, plan.expert.data_ptr(), plan.weight.data_ptr(),
+                               dweight.data_ptr(), dlogits.data_ptr(), _stream(None)),
+           "nvfp4_route_bwd")
+    return dlogits
+
+
+@_on_stream
+def nvfp4_dispatch(x: torch.Tensor, row: torch.Tensor, source: torch.Tensor,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """x's rows in the order of a plan's groups (`row`, `source` of a
+    RoutePlan), padding rows zero (see nvfp4_dispatch in nvfp4.h)."""
+    tokens, top = row.shape
+    rows = source.numel()
+    _cuda(x, torch.bfloat16, "x")
+    _want(x.dim() == 2 and x.shape[0] == tokens, "x must have one row per token")
+    _cuda(row, torch.int32, "row")
+    _cuda(source, torch.int32, "source")
+    if out is None:
+        out = torch.empty((rows, x.shape[1]), dtype=torch.bfloat16, device=x.device)
+    else:
+        _cuda(out, torch.bfloat16, "out", (rows, x.shape[1]))
+    _check(lib.nvfp4_dispatch(x.data_ptr(), row.data_ptr(), source.data_ptr(), tokens, x.shape[1],
+                              top, rows, out.data_ptr(), _stream(None)), "nvfp4_dispatch")
+    return out
+
+
+@_on_stream
+def nvfp4_combine(o: torch.Tensor, row: torch.Tensor, weight: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Each token's weighted sum of its rows of `o`; without weights, the
+    gradient of nvfp4_dispatch (see nvfp4_combine in nvfp4.h)."""
+    tokens, top = row.shape
+    _cuda(o, torch.bfloat16, "o")
+    _want(o.dim() == 2, "o must be 2-D")
+    _cuda(row, torch.int32, "row")
+    if weight is not None:
+        _cuda(weight, torch.float32, "weight", (tokens, top))
+    if out is None:
+        out = torch.empty((tokens, o.shape[1]), dtype=torch.bfloat16, device=o.device)
+    else:
+        _cuda(out, torch.bfloat16, "out", (tokens, o.shape[1]))
+    _check(lib.nvfp4_combine(o.data_ptr(), row.data_ptr(), _ptr(weight), tokens, o.shape[1], top,
+                             o.shape[0], out.data_ptr(), _stream(None)), "nvfp4_combine")
+    return out
+
+
+@_on_stream
+def nvfp4_combine_bwd(dy: torch.Tensor, o: torch.Tensor, row: torch.Tensor, source: torch.Tensor,
+                      weight: torch.Tensor, d_o: torch.Tensor | None = None,
+                      dweight: torch.Tensor | None = None):
+    """(d_o, dweight) of nvfp4_combine (see nvfp4_combine_bwd in nvfp4.h)."""
+    tokens, top = row.shape
+    _cuda(o, torch.bfloat16, "o")
+    _want(o.dim() == 2, "o must be 2-D")
+    rows, cols = o.shape
+    _cuda(dy, torch.bfloat16, "dy", (tokens, cols))
+    _cuda(row, torch.int32, "row")
+    _cuda(source, torch.int32, "source", (rows,))
+    _cuda(weight, torch.float32, "weight", (tokens, top))
+    if d_o is None:
+        d_o = torch.empty_like(o)
+    else:
+        _cuda(d_o, torch.bfloat16, "d_o", (rows, cols))
+    if dweight is None:
+        dweight = torch.empty_like(weight)
+    else:
+        _cuda(dweight, torch.float32, "dweight", (tokens, top))
+    _check(lib.nvfp4_combine_bwd(dy.data_ptr(), o.data_ptr(), row.data_ptr(), source.data_ptr(),
+                                 weight.data_ptr(), tokens, cols, top, rows, d_o.data_ptr(),
+                                 dweight.data_ptr(), _stream(None)), "nvfp4_combine_bwd")
+    return d_o, dweight
+
+
+def _groups(sizes, offsets):
+    groups = sizes.numel()
+    _cuda(sizes, torch.int32, "sizes")
+    _cuda(offsets, torch.int32, "offsets")
+    _want(offsets.numel() == groups + 1, "offsets must have one entry more than sizes")
+    return groups
+
+
+@_on_stream
+def nvfp4_group_gemm(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch.Tensor,
+                     b_view: int = 0, out: torch.Tensor | None = None, d_mode: int = D_BF16,
+                     C_add: torch.Tensor | None = None) -> torch.Tensor:
+    """D[r] = alpha A[r] . B_e^T for the rows r of each group e (see
+    nvfp4_group_gemm in nvfp4.h); returns D bf16 [rows, N]."""
+    groups = _groups(sizes, offsets)
+    rows, K = A.desc.rows, A.desc.cols
+    N = B.desc.cols if b_view else B.desc.rows // groups
+    if out is None:
+        out = torch.empty((rows, N), dtype=torch.bfloat16, device=A.s_dec.device)
+    else:
+        _cuda(out, torch.bfloat16, "out", (rows, N))
+    if C_add is not None:
+        _cuda(C_add, torch.bfloat16, "C_add", (rows, N))
+    _check(lib.nvfp4_group_gemm(A.desc, B.desc, b_view, sizes.data_ptr(), offsets.data_ptr(),
+                                groups, out.data_ptr(), d_mode, _ptr(C_add), rows, N, K,
+                                _stream(None)), "nvfp4_group_gemm")
+    return out
+
+
+@_on_stream
+def nvfp4_group_wgrad(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch.Tensor,
+                      out: torch.Tensor | None = None, d_mode: int = D_BF16) -> torch.Tensor:
+    """D_e = alpha A[:, rows of e] . B[:, rows of e]^T (see nvfp4_group_wgrad in
+    nvfp4.h); returns D [groups, M, N], bf16 or (D_F32_ACCUM: folded into) fp32."""
+    groups = _groups(sizes, offsets)
+    M, rows, N = A.desc.rows, A.desc.cols, B.desc.rows
+    dtype = torch.float32 if d_mode == D_F32_ACCUM else torch.bfloat16
+    if out is None:
+        out = (torch.zeros if d_mode == D_F32_ACCUM else torch.empty)(
+            (groups, M, N), dtype=dtype, device=A.s_dec.device)
+    else:
+        _cuda(out, dtype, "out", (groups, M, N))
+    _check(lib.nvfp4_group_wgrad(A.desc, B.desc, sizes.data_ptr(), offsets.data_ptr(), groups,
+                                 out.data_ptr(), d_mode, M, N, rows, _stream(None)),
+           "nvfp4_group_wgrad")
+    return out
+
+
+def _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale):
+    _want(x.is_cuda and x.dim() == 2 and x.is_contiguous(), "x must be a contiguous 2-D CUDA tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
+    rows, cols = x.shape
+    if z is not None:
+        _cuda(z, torch.bfloat16, "z", (rows, cols))
+    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _cuda(t, torch.float32, name, (cols,))
+    mode = GATE_NONE
+    if gate is not None:
+        mode = GATE_CHANNEL if gate.dim() == 1 else GATE_ROW
+        _want(tuple(gate.shape) == ((cols,) if mode == GATE_CHANNEL else (rows, 1)),
+              f"gate must have shape {(cols,)} or {(rows, 1)}")
+        _cuda(gate, torch.float32, "gate")
+    return NormParams(rows, cols, _DTYPES[x.dtype], mode, eps, x_scale, z_scale)
+
+
+@_on_stream
+def nvfp4_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor | None = None,
+                            w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                            w_pre: torch.Tensor | None = None, eps: float = 1e-5,
+                            x_scale: float = 1.0, z_scale: float = 1.0,
+                            y: torch.Tensor | None = None, h: torch.Tensor | None = None):
+    """y = x_scale x + z_scale gate (.) norm(z) w_post and h = norm(y) w_pre in
+    one pass (see nvfp4_residual_norm_fwd in nvfp4.h); returns (y, h).  Without
+    z, y is only written when given or x_scale is not 1 (and is x otherwise);
+    without w_pre, h is None.  A gate [rows, 1] is per row, one of [cols] per
+    channel."""
+    p = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
+    if y is None:
+        y = torch.empty_like(x) if z is not None or x_scale != 1.0 else None
+    else:
+        _cuda(y, x.dtype, "y", x.shape)
+    if h is None:
+        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if w_pre is not None else None
+    else:
+        _cuda(h, torch.bfloat16, "h", x.shape)
+    _check(lib.nvfp4_residual_norm_fwd(p, x.data_ptr(), _ptr(z), _ptr(w_post), _ptr(gate),
+                                       _ptr(w_pre), _ptr(y), _ptr(h), _stream(None)),
+           "nvfp4_residual_norm_fwd")
+    return (x if y is None else y), h
+
+
+@_on_stream
+def nvfp4_residual_norm_bwd(dy: torch.Tensor | None, dh: torch.Tensor | None, x: torch.Tensor,
+                            z: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, w_pre: torch.Tensor | None = None,
+                            eps: float = 1e-5, x_scale: float = 1.0, z_scale: float = 1.0,
+                            workspace: torch.Tensor | None = None):
+    """(dx, dz, dw_post, dgate, dw_pre) of nvfp4_residual_norm_fwd from the
+    gradients of y and h (None: zero); an entry is None where its input is."""
+    p = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
+    if dy is not None:
+        _cuda(dy, x.dtype, "dy", x.shape)
+    if dh is not None:
+        _cuda(dh, torch.bfloat16, "dh", x.shape)
+    if workspace is None:
+        n = C.c_size_t()
+        _check(lib.nvfp4_residual_norm_bwd_sizes(p.rows, p.cols, C.byref(n)),
+               "nvfp4_residual_norm_bwd_sizes")
+        workspace = _workspace(n.value, x.device)
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    dx, dz, dw_post, dgate, dw_pre = like(x), like(z), like(w_post), like(gate), like(w_pre)
+    _check(lib.nvfp4_residual_norm_bwd(p, _ptr(dy), _ptr(dh), x.data_ptr(), _ptr(z), _ptr(w_post),
+                                       _ptr(gate), _ptr(w_pre), dx.data_ptr(), _ptr(dz),
+                                       _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
+                                       workspace.data_ptr(), workspace.numel(), _stream(None)),
+           "nvfp4_residual_norm_bwd")
+    return dx, dz, dw_post, dgate, dw_pre
 
 
 STALL_QUANTIZE, STALL_GEMM = 1, 2

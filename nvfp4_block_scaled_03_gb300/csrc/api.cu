@@ -63,12 +63,14 @@ nvfp4_status nvfp4_device_check(int device) {
 nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  unsigned int gcode = 0, qcode = 0;
+  unsigned int gcode = 0, qcode = 0, ecode = 0;
   nvfp4_status st = gemm_read_error(&gcode);
+  if (st != NVFP4_OK) return st;
+  st = group_read_error(&ecode);
   if (st != NVFP4_OK) return st;
   st = quant_read_error(&qcode);
   if (st != NVFP4_OK) return st;
-  return (gcode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
+  return (gcode || ecode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
 }
 
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
@@ -77,6 +79,8 @@ nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
   const unsigned long long ns = wait_limit_ns ? wait_limit_ns : 2000000000ull;
   if (cudaDeviceSynchronize() != cudaSuccess) return NVFP4_ERR_CUDA;
   nvfp4_status st = quant_set_injection((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u, ns);
+  if (st != NVFP4_OK) return st;
+  st = group_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
   if (st != NVFP4_OK) return st;
   return gemm_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
 }
@@ -178,6 +182,87 @@ nvfp4_status nvfp4_gemm_ex(const nvfp4_tensor* A, int32_t a_view, const nvfp4_te
                            int64_t N, int64_t K, int32_t tile, nvfp4_stream stream) {
   return gemm_impl(A, a_view, B, b_view, D, d_mode, C, M, N, K, tile,
                    static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_route_sizes(int64_t tokens, int64_t experts, int32_t top, int64_t* rows,
+                               size_t* workspace_bytes) {
+  return route_sizes_impl(tokens, experts, top, rows, workspace_bytes);
+}
+
+nvfp4_status nvfp4_route_fwd(const void* logits, int32_t in_dtype, int64_t tokens,
+                             int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                             int32_t* expert, float* weight, int32_t* sizes, int32_t* offsets,
+                             int32_t* row, int32_t* source, void* workspace,
+                             size_t workspace_bytes, nvfp4_stream stream) {
+  return route_fwd_impl(logits, in_dtype, tokens, experts, ld, top, mode, expert, weight, sizes,
+                        offsets, row, source, workspace, workspace_bytes,
+                        static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_route_bwd(const void* logits, int32_t in_dtype, int64_t tokens,
+                             int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                             const int32_t* expert, const float* weight, const float* dweight,
+                             void* dlogits, nvfp4_stream stream) {
+  return route_bwd_impl(logits, in_dtype, tokens, experts, ld, top, mode, expert, weight, dweight,
+                        dlogits, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_dispatch(const void* x, const int32_t* row, const int32_t* source,
+                            int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* xe,
+                            nvfp4_stream stream) {
+  return dispatch_impl(x, row, source, tokens, cols, top, rows, xe,
+                       static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_combine(const void* o, const int32_t* row, const float* weight,
+                           int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* y,
+                           nvfp4_stream stream) {
+  return combine_impl(o, row, weight, tokens, cols, top, rows, y,
+                      static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_combine_bwd(const void* dy, const void* o, const int32_t* row,
+                               const int32_t* source, const float* weight, int64_t tokens,
+                               int64_t cols, int32_t top, int64_t rows, void* d_o,
+                               float* dweight, nvfp4_stream stream) {
+  return combine_bwd_impl(dy, o, row, source, weight, tokens, cols, top, rows, d_o, dweight,
+                          static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_group_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
+                              const int32_t* sizes, const int32_t* offsets, int32_t groups,
+                              void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
+                              int64_t K, nvfp4_stream stream) {
+  return group_gemm_impl(A, B, b_view, sizes, offsets, groups, D, d_mode, C, rows, N, K,
+                         static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_group_wgrad(const nvfp4_tensor* A, const nvfp4_tensor* B,
+                               const int32_t* sizes, const int32_t* offsets, int32_t groups,
+                               void* D, int32_t d_mode, int64_t M, int64_t N, int64_t rows,
+                               nvfp4_stream stream) {
+  return group_wgrad_impl(A, B, sizes, offsets, groups, D, d_mode, M, N, rows,
+                          static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_residual_norm_fwd(const nvfp4_norm_params* p, const void* x, const void* z,
+                                     const float* w_post, const float* gate, const float* w_pre,
+                                     void* y, void* h, nvfp4_stream stream) {
+  return norm_fwd_impl(p, x, z, w_post, gate, w_pre, y, h, static_cast<cudaStream_t>(stream));
+}
+
+nvfp4_status nvfp4_residual_norm_bwd_sizes(int64_t rows, int64_t cols, size_t* workspace_bytes) {
+  return norm_bwd_sizes_impl(rows, cols, workspace_bytes);
+}
+
+nvfp4_status nvfp4_residual_norm_bwd(const nvfp4_norm_params* p, const void* dy, const void* dh,
+                                     const void* x, const void* z, const float* w_post,
+                                     const float* gate, const float* w_pre, void* dx, void* dz,
+                                     float* dw_post, float* dgate, float* dw_pre,
+                                     void* workspace, size_t workspace_bytes,
+                                     nvfp4_stream stream) {
+  return norm_bwd_impl(p, dy, dh, x, z, w_post, gate, w_pre, dx, dz, dw_post, dgate, dw_pre,
+                       workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

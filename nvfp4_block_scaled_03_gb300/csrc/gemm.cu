@@ -24,24 +24,15 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "gemm_common.cuh"
 #include "internal.h"
 
 namespace nvfp4 {
 
-static __device__ unsigned int g_gemm_error;
-// Failure injection for tests of the bounded waits (nvfp4_debug_inject):
-// while g_gemm_stall is set the producers of every GEMM kernel issue no
-// loads, and the pipeline waits give up after g_gemm_wait_ns.
-static __device__ unsigned int g_gemm_stall;
-static __device__ unsigned long long g_gemm_wait_ns = 2000000000ull;
-
 namespace {
 
-constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 constexpr int kThreads = 320;      // producer, MMA, 8 epilogue warps
 constexpr int kBM = 128;            // rows of A per tile (one MMA, cta_group::1)
-constexpr int kBKBytes = 128;       // K bytes per stage (256 FP4 elements)
-constexpr uint32_t kTmemCols = 512;
 
 struct GemmArgs {
   const uint8_t* sfa;
@@ -80,53 +71,6 @@ struct Smem {
   static_assert(kSfCol0 + STAGES * kSfColsPerStage <= kTmemCols, "tensor memory overflow");
   static_assert(kAlloc <= 232448, "shared memory overflow");
 };
-
-// K-major operand descriptor for a stage row width of BKB bytes (128-byte or
-// 64-byte swizzle; 8-row swizzle atoms stacked 8*BKB bytes apart).
-template <int BKB>
-NVFP4_DEV uint64_t smem_desc_kmajor(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)((8 * BKB) >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)(BKB == 128 ? 2 : 4) << 61;  // SWIZZLE_128B or SWIZZLE_64B
-  return d;
-}
-
-
-// Drain wait used after an abort: bounded, ignores the abort flag.
-NVFP4_DEV void wait_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
-      atomicCAS(&g_gemm_error, 0u, 0xDEu);
-      return;
-    }
-  }
-}
-
-// Bounded wait of the single-SM kernel: on expiry it raises the CTA's abort
-// flag and records `code` in the error word.
-NVFP4_DEV bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                            unsigned int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_gemm_wait_ns);
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > limit) {
-      *abort_flag = 1;
-      atomicCAS(&g_gemm_error, 0u, code);
-      return false;
-    }
-  }
-}
-
-NVFP4_DEV uint32_t pack_bf16x2(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 template <int DMODE>
 NVFP4_DEV void store_row_chunk(const GemmArgs& a, int64_t row, int64_t col0, const uint32_t (&r)[32],
@@ -182,42 +126,6 @@ NVFP4_DEV void store_row_chunk(const GemmArgs& a, int64_t row, int64_t col0, con
         *reinterpret_cast<float4*>(D + (g0 + g) * 4) = d[g];
       }
     }
-  }
-}
-
-// Pulls the part of D that a row of a later tile's epilogue reads (128-byte
-// lines from col0 on, `bytes` of them) into L2 while the tile's MMAs run.
-NVFP4_DEV void prefetch_l2_row(const void* p, int bytes) {
-  const char* c = static_cast<const char*>(p);
-  for (int o = 0; o < bytes; o += 128)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<uint64_t>(c + o)));
-}
-
-// Epilogue helper: one warp's 32 rows x 32 bf16 columns (lane = row, 16
-// packed pairs) into its staging box, then one tensor store at (x, y).  The
-// box is rewritten only after the previous store has read it; the 16-byte
-// pieces are rotated so a warp's writes hit distinct banks.
-NVFP4_DEV void store_box_bf16(uint8_t* box, int lane, const uint32_t (&pk)[16],
-                              const CUtensorMap* tmD, int32_t x, int32_t y) {
-  if (lane == 0) bulk_wait_group_read<0>();
-  __syncwarp();
-#pragma unroll
-  for (int pc = 0; pc < 4; ++pc) {
-    const int piece = (pc + (lane >> 1)) & 3;
-    uint4 v;
-    switch (piece) {
-      case 0: v = make_uint4(pk[0], pk[1], pk[2], pk[3]); break;
-      case 1: v = make_uint4(pk[4], pk[5], pk[6], pk[7]); break;
-      case 2: v = make_uint4(pk[8], pk[9], pk[10], pk[11]); break;
-      default: v = make_uint4(pk[12], pk[13], pk[14], pk[15]); break;
-    }
-    *reinterpret_cast<uint4*>(box + lane * 64 + piece * 16) = v;
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_2d(tmD, smem_u32(box), x, y);
-    bulk_commit_group();
   }
 }
 
@@ -557,24 +465,6 @@ struct PairSmem {
   static_assert(kSfCol0 + STAGES * kSfColsPerStage <= kTmemCols, "tensor memory overflow");
   static_assert(kAlloc <= 232448, "shared memory overflow");
 };
-
-// Bounded wait for the pair: a timeout also raises the peer CTA's abort flag.
-NVFP4_DEV bool wait_bounded_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                 uint32_t peer_abort_addr, unsigned int code) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_gemm_wait_ns);
-  while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > limit) {
-      *abort_flag = 1;
-      st_cluster_u32(peer_abort_addr, 1u);
-      atomicCAS(&g_gemm_error, 0u, code);
-      return false;
-    }
-  }
-}
 
 template <int STAGES, int DMODE, int FMT, bool IMG>
 __global__ void __cluster_dims__(2, 1, 1)
@@ -1244,40 +1134,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
 }
 
 // ---- host side -----------------------------------------------------------------
-EncodeTiledFn encode_fn() { return tensor_map_encoder(); }
-
-// 2-D map over a K-major code matrix [rows, kbytes] with a box of box_bytes
-// (128: 128-byte swizzle, 64: 64-byte swizzle) x box_rows.
-bool make_code_map(CUtensorMap* map, const void* base, int64_t rows, int64_t kbytes,
-                   int box_rows, int box_bytes = kBKBytes) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)kbytes, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kbytes};
-  const cuuint32_t box[2] = {(cuuint32_t)box_bytes, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D map over a scale tensor viewed as rows of 128 bytes (4 rows per atom),
-// box of 16 rows (the 4 atoms of one stage).
-bool make_sf_map(CUtensorMap* map, const void* base, size_t bytes, int box_rows = 16) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {128, (cuuint64_t)(bytes / 128)};
-  const cuuint64_t strides[1] = {128};
-  const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 5-D map over a scale tensor (atoms of 4 rows x 128 bytes, kg per 128-row
 // block) that reads each atom four times: dimensions (byte, atom row, copy
 // [stride 0], row block, atom along K); a box of (128, 4, 4, 2, atoms) brings
@@ -1295,72 +1151,6 @@ bool make_sf_image_map(CUtensorMap* map, const void* base, int kg, int64_t row_b
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// 2-D map over a bf16 output [rows, cols] with 32 x 32 boxes (no swizzle);
-// tensor stores skip the part of a box outside the matrix.
-bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)(cols * 2)};
-  const cuuint32_t box[2] = {32, 32};
-  const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Per-device, once-per-kernel launch set-up of a GEMM kernel, under a lock:
-// its dynamic shared memory attribute, for a kernel that splits registers
-// with setmaxnreg the check that the compiled count covers the split
-// (setmaxnreg.inc waits until the registers it asks for are free in the
-// block's launch allotment, so a split above it would wait forever), and
-// for a CTA-pair kernel how many pairs are resident at once (cluster
-// placement can leave SMs of a GPC unpaired).  Returns the resident pairs
-// (1 for a single-SM kernel), 0 when the set-up failed.
-struct GemmLaunchState {
-  std::mutex mu;
-  int resident[64] = {};  // per device: 0 not yet set up, -1 refused for good
-};
-
-template <typename K>
-int gemm_setup(GemmLaunchState& ls, K kern, uint32_t smem, int threads, int split_regs,
-               bool pair, int sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::lock_guard<std::mutex> lock(ls.mu);
-  if (ls.resident[dev] == 0) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-        cudaSuccess)
-      return 0;
-    if (split_regs > 0) {
-      cudaFuncAttributes fa;
-      if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return 0;
-      if (fa.numRegs * threads < split_regs) {
-        ls.resident[dev] = -1;  // the compiled kernel can never run
-        return 0;
-      }
-    }
-    int n = 1;
-    if (pair) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * (sms / 2));
-      cfg.blockDim = dim3(threads);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = 2;
-      attr.val.clusterDim.y = 1;
-      attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sms / 2;
-      n = std::min(n, sms / 2);
-    }
-    ls.resident[dev] = n;
-  }
-  return ls.resident[dev] > 0 ? ls.resident[dev] : 0;
 }
 
 template <int STAGES, int DMODE, int FMT, bool IMG>
@@ -1443,8 +1233,6 @@ nvfp4_status launch_pair_mode(int d_mode, const CUtensorMap& ma, const CUtensorM
                                                                       s);
   }
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 

@@ -110,6 +110,54 @@ nvfp4_status mx_quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int
                               int64_t ld, int32_t mode, int32_t fmt, void* codes, void* scales,
                               void* scales_sw, cudaStream_t stream);
 
+// Grouped products (group_gemm.cu), with their own error word and injection.
+nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
+                             const int32_t* sizes, const int32_t* offsets, int32_t groups,
+                             void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
+                             int64_t K, cudaStream_t stream);
+nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, const int32_t* sizes,
+                              const int32_t* offsets, int32_t groups, void* D, int32_t d_mode,
+                              int64_t M, int64_t N, int64_t rows, cudaStream_t stream);
+nvfp4_status group_read_error(unsigned int* code);
+nvfp4_status group_set_injection(unsigned int stall, unsigned long long wait_ns);
+
+// The most SMs that workspaces sized without a device allow for.
+constexpr int kMaxSms = 160;
+
+// Norms around a residual block (norm.cu).
+nvfp4_status norm_fwd_impl(const nvfp4_norm_params* q, const void* x, const void* z,
+                           const float* w_post, const float* gate, const float* w_pre, void* y,
+                           void* h, cudaStream_t stream);
+nvfp4_status norm_bwd_sizes_impl(int64_t rows, int64_t cols, size_t* workspace_bytes);
+nvfp4_status norm_bwd_impl(const nvfp4_norm_params* q, const void* dy, const void* dh,
+                           const void* x, const void* z, const float* w_post, const float* gate,
+                           const float* w_pre, void* dx, void* dz, float* dw_post, float* dgate,
+                           float* dw_pre, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+// Expert routing (route.cu).
+int64_t route_rows(int64_t tokens, int64_t experts, int32_t top);
+nvfp4_status route_sizes_impl(int64_t tokens, int64_t experts, int32_t top, int64_t* rows,
+                              size_t* workspace_bytes);
+nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
+                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                            int32_t* expert, float* weight, int32_t* sizes, int32_t* offsets,
+                            int32_t* row, int32_t* source, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+nvfp4_status route_bwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
+                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                            const int32_t* expert, const float* weight, const float* dweight,
+                            void* dlogits, cudaStream_t stream);
+nvfp4_status dispatch_impl(const void* x, const int32_t* row, const int32_t* source,
+                           int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* xe,
+                           cudaStream_t stream);
+nvfp4_status combine_impl(const void* o, const int32_t* row, const float* weight, int64_t tokens,
+                          int64_t cols, int32_t top, int64_t rows, void* y, cudaStream_t stream);
+nvfp4_status combine_bwd_impl(const void* dy, const void* o, const int32_t* row,
+                              const int32_t* source, const float* weight, int64_t tokens,
+                              int64_t cols, int32_t top, int64_t rows, void* d_o, float* dweight,
+                              cudaStream_t stream);
+
 inline nvfp4_status cuda_status(cudaError_t e) {
   return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
