@@ -104,8 +104,8 @@ def _load():
         "nvfp4_combine": ([vp, vp, vp, i64, i64, i32, i64, vp, vp], C.c_int),
         "nvfp4_combine_bwd": ([vp, vp, vp, vp, vp, i64, i64, i32, i64, vp, vp, vp], C.c_int),
         "nvfp4_group_gemm": ([P(Tensor), P(Tensor), i32, vp, vp, i32, vp, i32, vp, i64, i64, i64,
-                              vp], C.c_int),
-        "nvfp4_group_wgrad": ([P(Tensor), P(Tensor), vp, vp, i32, vp, i32, i64, i64, i64, vp],
+                              i32, vp], C.c_int),
+        "nvfp4_group_wgrad": ([P(Tensor), P(Tensor), vp, vp, i32, vp, i32, i64, i64, i64, i32, vp],
                               C.c_int),
         "nvfp4_residual_norm_fwd": ([P(NormParams), vp, vp, vp, vp, vp, vp, vp, vp], C.c_int),
         "nvfp4_residual_norm_bwd_sizes": ([i64, i64, P(sz)], C.c_int),
@@ -730,7 +730,7 @@ def _groups(sizes, offsets):
 @_on_stream
 def nvfp4_group_gemm(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch.Tensor,
                      b_view: int = 0, out: torch.Tensor | None = None, d_mode: int = D_BF16,
-                     C_add: torch.Tensor | None = None) -> torch.Tensor:
+                     C_add: torch.Tensor | None = None, tile: int = TILE_AUTO) -> torch.Tensor:
     """D[r] = alpha A[r] . B_e^T for the rows r of each group e (see
     nvfp4_group_gemm in nvfp4.h); returns D bf16 [rows, N]."""
     groups = _groups(sizes, offsets)
@@ -743,14 +743,15 @@ def nvfp4_group_gemm(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch
     if C_add is not None:
         _cuda(C_add, torch.bfloat16, "C_add", (rows, N))
     _check(lib.nvfp4_group_gemm(A.desc, B.desc, b_view, sizes.data_ptr(), offsets.data_ptr(),
-                                groups, out.data_ptr(), d_mode, _ptr(C_add), rows, N, K,
+                                groups, out.data_ptr(), d_mode, _ptr(C_add), rows, N, K, tile,
                                 _stream(None)), "nvfp4_group_gemm")
     return out
 
 
 @_on_stream
 def nvfp4_group_wgrad(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch.Tensor,
-                      out: torch.Tensor | None = None, d_mode: int = D_BF16) -> torch.Tensor:
+                      out: torch.Tensor | None = None, d_mode: int = D_BF16,
+                      tile: int = TILE_AUTO) -> torch.Tensor:
     """D_e = alpha A[:, rows of e] . B[:, rows of e]^T (see nvfp4_group_wgrad in
     nvfp4.h); returns D [groups, M, N], bf16 or (D_F32_ACCUM: folded into) fp32."""
     groups = _groups(sizes, offsets)
@@ -762,7 +763,7 @@ def nvfp4_group_wgrad(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torc
     else:
         _cuda(out, dtype, "out", (groups, M, N))
     _check(lib.nvfp4_group_wgrad(A.desc, B.desc, sizes.data_ptr(), offsets.data_ptr(), groups,
-                                 out.data_ptr(), d_mode, M, N, rows, _stream(None)),
+                                 out.data_ptr(), d_mode, M, N, rows, tile, _stream(None)),
            "nvfp4_group_wgrad")
     return out
 

@@ -232,16 +232,16 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, const void* o, const int32_t* row
 nvfp4_status nvfp4_group_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
                               const int32_t* sizes, const int32_t* offsets, int32_t groups,
                               void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
-                              int64_t K, nvfp4_stream stream) {
+                              int64_t K, int32_t tile, nvfp4_stream stream) {
   return group_gemm_impl(A, B, b_view, sizes, offsets, groups, D, d_mode, C, rows, N, K,
-                         static_cast<cudaStream_t>(stream));
+                         tile, static_cast<cudaStream_t>(stream));
 }
 
 nvfp4_status nvfp4_group_wgrad(const nvfp4_tensor* A, const nvfp4_tensor* B,
                                const int32_t* sizes, const int32_t* offsets, int32_t groups,
                                void* D, int32_t d_mode, int64_t M, int64_t N, int64_t rows,
-                               nvfp4_stream stream) {
-  return group_wgrad_impl(A, B, sizes, offsets, groups, D, d_mode, M, N, rows,
+                               int32_t tile, nvfp4_stream stream) {
+  return group_wgrad_impl(A, B, sizes, offsets, groups, D, d_mode, M, N, rows, tile,
                           static_cast<cudaStream_t>(stream));
 }
 

@@ -134,7 +134,7 @@ NVFP4_DEV Tile tile_at(int tile, int& g, const GroupTable* t, const GroupArgs& a
     r.atoms = (t->size[g] + kAtom - 1) / kAtom;
     r.d_row = (int64_t)g * a.M + r.a_row;
     r.d_col = n * BN;
-    r.live = BM;
+    r.live = a.M - r.a_row;
   }
   return r;
 }
@@ -410,14 +410,509 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// =============================================================================
+// CTA-pair kernel: tiles of 256 x BN (BN = 256 or 384) on a cluster of two SMs
+// (tcgen05 cta_group::2), for groups with many rows or long contractions.  As
+// gemm.cu's pair kernels: CTA r loads rows [128 r, 128 r + 128) of A's 256 and
+// its half of B's rows, four scale warps of each CTA store the stage's scales
+// into tensor memory, the leader issues the MMAs (a second MMA warp takes the
+// last 128 columns of a 384-wide tile), and 8 epilogue warps of each CTA drain
+// its 128 rows.  Of a 256-row tile whose group ends in its first half, and of
+// the last tile of an M that is an odd multiple of 128, the second CTA stores
+// nothing.
+//
+// Outputs leave through shared-memory boxes of 32 rows x 32 columns and tensor
+// stores; the FP32 fold as tensor reductions (one FP32 add in L2 for each
+// element, subnormals flushed there), so D is never read into the SM.
+// =============================================================================
+template <int BN, int DMODE>
+struct PairGroup {
+  static constexpr bool kF32 = DMODE == NVFP4_D_F32_ACCUM;
+  static constexpr int kAt = 4, kRowBlocks = BN / 128;
+  static constexpr int kStages = BN == 384 || kF32 ? 4 : 5;
+  static constexpr int kMmaWarps = BN == 384 ? 2 : 1;
+  static constexpr uint32_t kA = 128 * kBKBytes, kB = (BN / 2) * kBKBytes;
+  static constexpr uint32_t kSFA = kAt * 512, kSFB = kRowBlocks * kAt * 512;
+  static constexpr uint32_t kBox = 32 * (kF32 ? 128 : 64);
+  static constexpr uint32_t offA = 0, offB = offA + kStages * kA;
+  static constexpr uint32_t offStore = offB + kStages * kB;
+  static constexpr uint32_t offSFA = offStore + 8 * kBox;
+  static constexpr uint32_t offSFB = offSFA + kStages * kSFA;
+  static constexpr uint32_t offBar = offSFB + kStages * kSFB;
+  // full, empty, scales-ready, scales-landed per stage; acc full, acc empty;
+  // a drain barrier per MMA warp
+  static constexpr uint32_t kNumBars = 4 * kStages + 2 + kMmaWarps;
+  static constexpr uint32_t offMisc = offBar + kNumBars * 8;
+  static constexpr uint32_t offTable = offMisc + 16;
+  static constexpr uint32_t kBytes = offTable + sizeof(GroupTable);
+  static constexpr uint32_t kAlloc = kBytes + 1024;
+  // tensor memory: the accumulator, then scale slots of [B rows 256..: 4 per
+  // atom] [A: 4 per atom] [B rows 0..255: 8 per atom] columns
+  static constexpr uint32_t kSfCol0 = BN;
+  static constexpr uint32_t kColA = BN == 384 ? 16 : 0, kColB01 = kColA + 16;
+  static constexpr uint32_t kSlotCols = kColB01 + 32;
+  static constexpr int kSlots = BN == 384 ? 2 : kStages;
+  static constexpr int kThreads = 512;
+  static constexpr int kRegsIssue = 88, kRegsEpilogue = 168;
+  static constexpr int kSplitRegs = 2 * 128 * kRegsIssue + 2 * 128 * kRegsEpilogue;
+  static_assert(kSfCol0 + kSlots * kSlotCols <= kTmemCols, "tensor memory overflow");
+  static_assert(kAlloc <= 232448, "shared memory overflow");
+  static_assert(kSplitRegs <= kThreads * 128, "register split exceeds the launch's");
+  static_assert(offStore % 1024 == 0, "store boxes start on their swizzle's period");
+  static_assert(BN == 256 || (BN == 384 && !kF32), "tile");
+};
+
+// Tensor reduction (add) of a shared-memory box into global memory.
+NVFP4_DEV void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], "
+      "[%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y)
+      : "memory");
+}
+
+// One warp's 32 rows x 32 columns (lane = row) into its box and out.  The 16-byte
+// pieces of a row are permuted as the map's swizzle says (64- or 128-byte), so
+// a warp's writes hit distinct banks; the box is rewritten once the store
+// before has read it.
+NVFP4_DEV void store_box(uint8_t* box, int lane, const uint32_t (&pk)[16], const CUtensorMap* map,
+                         int32_t x, int32_t y) {
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    *reinterpret_cast<uint4*>(box + lane * 64 + ((p ^ ((lane >> 1) & 3)) * 16)) =
+        make_uint4(pk[4 * p], pk[4 * p + 1], pk[4 * p + 2], pk[4 * p + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, smem_u32(box), x, y);
+    bulk_commit_group();
+  }
+}
+NVFP4_DEV void reduce_box(uint8_t* box, int lane, const float (&v)[32], const CUtensorMap* map,
+                          int32_t x, int32_t y) {
+  if (lane == 0) bulk_wait_group_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 8; ++p)
+    *reinterpret_cast<float4*>(box + lane * 128 + ((p ^ (lane & 7)) * 16)) =
+        make_float4(v[4 * p], v[4 * p + 1], v[4 * p + 2], v[4 * p + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_reduce_add_2d(map, smem_u32(box), x, y);
+    bulk_commit_group();
+  }
+}
+
+template <int KIND, int BN, int DMODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>::kThreads, 1)
+    group_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmB2,
+                      const __grid_constant__ CUtensorMap tmSFA,
+                      const __grid_constant__ CUtensorMap tmSFB,
+                      const __grid_constant__ CUtensorMap tmD, const GroupArgs args) {
+  using L = PairGroup<BN, DMODE>;
+  constexpr int S = L::kStages, kAt = L::kAt;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + L::offBar;
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (S + s); };
+  auto sf_bar = [&](int s) { return bar0 + 8u * (2 * S + s); };
+  auto scf_bar = [&](int s) { return bar0 + 8u * (3 * S + s); };
+  const uint32_t acc_full = bar0 + 8u * (4 * S);
+  const uint32_t acc_empty = acc_full + 8;
+  const uint32_t drain_bar = acc_full + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
+  GroupTable* table = reinterpret_cast<GroupTable*>(smem + L::offTable);
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), rank ^ 1u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), L::kMmaWarps);  // one commit per MMA warp
+      mbar_init(sf_bar(s), 8);                // four scale warps in each CTA
+      mbar_init(scf_bar(s), 1);
+    }
+    mbar_init(acc_full, L::kMmaWarps);
+    mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA
+    for (int d = 0; d < L::kMmaWarps; ++d) mbar_init(drain_bar + 8u * d, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish_pair();
+  }
+  griddep_wait();
+  fill_table<KIND, 256>(table, args);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int tiles = num_tiles<KIND>(table, args);
+
+  if (warp < 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsIssue));
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmB);
+      if (BN == 384) prefetch_tmap(&tmB2);
+      prefetch_tmap(&tmSFA);
+      prefetch_tmap(&tmSFB);
+      uint32_t s = 0, ph = 0;
+      int g = 0;
+      // injected stall: no loads, so every consumer's first wait runs out
+      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
+      for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+        const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+        const int num_kb = (t.atoms + kAt - 1) / kAt;
+        const int a_row = t.a_row + (int)rank * 128;
+        const int sfa_row = (a_row >> 7) * args.kga + t.a_atom;
+        const int sfb_row = (t.b_row >> 7) * args.kgb + t.b_atom;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!wait_bounded_pair(empty_bar(s), ph ^ 1u, abort_flag, peer_abort, 0x11u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = mapa_shared(full_bar(s), 0);
+          const int a_x = (t.a_atom + kb * kAt) * (kAtom / 2);
+          const int b_x = (t.b_atom + kb * kAt) * (kAtom / 2);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (L::kA + L::kB));
+          tma_load_2d_pair(sbase + L::offA + s * L::kA, &tmA, fb, a_x, a_row);
+          tma_load_2d_pair(sbase + L::offB + s * L::kB, &tmB, fb, b_x, t.b_row + (int)rank * 128);
+          if (BN == 384)
+            tma_load_2d_pair(sbase + L::offB + s * L::kB + 128 * kBKBytes, &tmB2, fb, b_x,
+                             t.b_row + 256 + (int)rank * 64);
+          // this CTA's scale atoms on its own barrier (past the tensor: zeros)
+          mbar_arrive_expect_tx(scf_bar(s), L::kSFA + L::kSFB);
+          tma_load_2d(sbase + L::offSFA + s * L::kSFA, &tmSFA, scf_bar(s), 0,
+                      (sfa_row + kb * kAt) * 4);
+#pragma unroll
+          for (int i = 0; i < L::kRowBlocks; ++i)
+            tma_load_2d(sbase + L::offSFB + s * L::kSFB + i * kAt * 512, &tmSFB, scf_bar(s), 0,
+                        (sfb_row + i * args.kgb + kb * kAt) * 4);
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+      }
+      if (!ok) {  // give copies already issued time to land before exit
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000ull) {
+        }
+      }
+    }
+  } else if (warp <= L::kMmaWarps) {
+    if (lane == 0 && leader) {
+      // ---------------------------------------------------------------- MMA
+      const bool second = warp == 2;
+      const uint32_t idesc = second ? idesc_nvf4(256, 128) : idesc_nvf4(256, 256);
+      const uint32_t d_tmem = tmem + (second ? 256u : 0u);
+      const uint32_t b_off = second ? 128u * kBKBytes : 0u;
+      const uint32_t sfb_col = second ? 0u : L::kColB01;
+      const uint32_t sfb_step = second ? 4u : 8u;  // columns per atom
+      const uint32_t my_drain = drain_bar + (second ? 8u : 0u);
+      uint32_t s = 0, ph = 0, acc_ph = 0, it = 0;
+      int g = 0;
+      bool ok = true, issued = false;
+      for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+        const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+        if (t.atoms == 0) continue;
+        const int num_kb = (t.atoms + kAt - 1) / kAt;
+        if (!wait_bounded_pair(acc_empty, acc_ph ^ 1u, abort_flag, peer_abort, 0x22u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+          if (!wait_bounded_pair(full_bar(s), ph, abort_flag, peer_abort, 0x24u) ||
+              !wait_bounded_pair(sf_bar(s), ph, abort_flag, peer_abort, 0x23u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int nmma = min(kAt, t.atoms - kb * kAt);
+          const uint32_t slot = tmem + L::kSfCol0 + (it % L::kSlots) * L::kSlotCols;
+          const uint32_t a0 = sbase + L::offA + s * L::kA;
+          const uint32_t b0 = sbase + L::offB + s * L::kB + b_off;
+          for (int j = 0; j < nmma; ++j)
+            tc_mma_pair_nvf4(d_tmem, smem_desc_sw128(a0 + 32 * j), smem_desc_sw128(b0 + 32 * j),
+                             idesc, slot + L::kColA + 4 * j, slot + sfb_col + sfb_step * j,
+                             (kb | j) != 0 ? 1u : 0u);
+          issued = true;
+          tc_commit_pair(empty_bar(s), 3);
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        tc_commit_pair(acc_full, 3);
+        acc_ph ^= 1u;
+      }
+      if (!ok && issued) {
+        tc_commit_pair(my_drain, 1);
+        wait_drain(my_drain, 0);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scale warps
+    // Warp q stores the stage's atoms into its 32-lane quarter: lane i gets
+    // line i of an atom (the scale words of rows i, i + 32, i + 64, i + 96) in
+    // 4 columns.  A slot is rewritten once the MMAs that read it completed.
+    const int q = warp & 3;
+    const uint32_t sf_leader = mapa_shared(sf_bar(0), 0);
+    uint32_t s = 0, ph = 0, it = 0;
+    int g = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+      const int num_kb = (tile_at<KIND, 256, BN>(tile, g, table, args).atoms + kAt - 1) / kAt;
+      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        if (!wait_bounded_pair(scf_bar(s), ph, abort_flag, peer_abort, 0x26u)) {
+          ok = false;
+          break;
+        }
+        if (L::kSlots < S && it >= (uint32_t)L::kSlots) {
+          const uint32_t prev = it - L::kSlots;
+          if (!wait_bounded_pair(empty_bar(prev % S), (prev / S) & 1u, abort_flag, peer_abort,
+                                 0x25u)) {
+            ok = false;
+            break;
+          }
+        }
+        const uint8_t* sa = smem + L::offSFA + s * L::kSFA + lane * 16;
+        const uint8_t* sb = smem + L::offSFB + s * L::kSFB + lane * 16;
+        uint32_t v[L::kSlotCols];
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+          const uint4 a = *reinterpret_cast<const uint4*>(sa + j * 512);
+          const uint4 b0 = *reinterpret_cast<const uint4*>(sb + j * 512);
+          const uint4 b1 = *reinterpret_cast<const uint4*>(sb + (kAt + j) * 512);
+          const uint32_t w[12] = {a.x,  a.y,  a.z,  a.w,  b0.x, b0.y,
+                                  b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[L::kColA + 4 * j + e] = w[e];
+            v[L::kColB01 + 8 * j + e] = w[4 + e];
+            v[L::kColB01 + 8 * j + 4 + e] = w[8 + e];
+          }
+          if (BN == 384) {
+            const uint4 b2 = *reinterpret_cast<const uint4*>(sb + (2 * kAt + j) * 512);
+            v[4 * j] = b2.x;
+            v[4 * j + 1] = b2.y;
+            v[4 * j + 2] = b2.z;
+            v[4 * j + 3] = b2.w;
+          }
+        }
+        const uint32_t taddr =
+            tmem + ((uint32_t)(32 * q) << 16) + L::kSfCol0 + (it % L::kSlots) * L::kSlotCols;
+#pragma unroll
+        for (int c = 0; c < (int)L::kSlotCols; c += 16) tmem_st16(taddr + c, v + c);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(sf_leader + 8u * s);
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+    }
+  }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsEpilogue));
+    constexpr int kCols = BN / 2, kChunks = kCols / 32;
+    const int ew = warp - 8;
+    const int q = warp & 3, h = ew >> 2;
+    const uint32_t acc_empty_leader = mapa_shared(acc_empty, 0);
+    const float alpha = __fmul_rn(__ldg(args.sdec_a), __ldg(args.sdec_b));
+    uint8_t* box = smem + L::offStore + ew * L::kBox;
+    if (lane == 0) prefetch_tmap(&tmD);
+    uint32_t acc_ph = 0;
+    int g = 0;
+    bool ok = true;
+    for (int tile = pair; tile < tiles; tile += num_pairs) {
+      const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+      const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
+      const bool mine = t.live > (int)rank * 128;
+      const bool live = r0 + lane < t.live;
+      const int32_t y = (int32_t)(t.d_row + r0);
+      const int x0 = t.d_col + h * kCols;
+      if constexpr (L::kF32) {
+        if (t.atoms == 0) continue;  // nothing to add
+        if (!wait_bounded_pair(acc_full, acc_ph, abort_flag, peer_abort, 0x33u)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t r[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kCols + c * 32), r[c]);
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader);
+        acc_ph ^= 1u;
+        if (!mine) continue;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(__uint_as_float(r[c][e]), alpha);
+          if (x0 + c * 32 < args.N) reduce_box(box, lane, v, &tmD, x0 + c * 32, y);
+        }
+      } else {
+        uint32_t pk[kChunks][16];
+        if (t.atoms > 0) {
+          if (!wait_bounded_pair(acc_full, acc_ph, abort_flag, peer_abort, 0x33u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kCols + c * 32), r);
+            tmem_ld_wait();
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __fmul_rn(__uint_as_float(r[e]), alpha);
+            if (DMODE == NVFP4_D_BF16_ADD_C && live && x0 + c * 32 < args.N) {
+              const uint4* cp = reinterpret_cast<const uint4*>(
+                  static_cast<const __nv_bfloat16*>(args.C) + (t.d_row + r0 + lane) * args.N + x0 +
+                  c * 32);
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                const uint4 u = cp[p];
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  f[8 * p + 2 * e] = __fadd_rn(f[8 * p + 2 * e], __uint_as_float(w[e] << 16));
+                  f[8 * p + 2 * e + 1] =
+                      __fadd_rn(f[8 * p + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u));
+                }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[c][e] = live ? pack_bf16x2(f[2 * e], f[2 * e + 1]) : 0u;
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty_leader);
+          acc_ph ^= 1u;
+        } else {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[c][e] = 0u;
+        }
+        if (!mine) continue;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (x0 + c * 32 < args.N) store_box(box, lane, pk[c], &tmD, x0 + c * 32, y);
+      }
+    }
+    if (KIND == kRows && ok)
+      clear_tail(args, (int64_t)blockIdx.x * 256 + threadIdx.x - 256, (int64_t)gridDim.x * 256);
+    if (lane == 0) bulk_wait_group<0>();  // stores done before exit
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// 2-D map over an output [rows, cols] with boxes of 32 x 32, swizzled over a
+// box row's 64 (bf16) or 128 (FP32) bytes.
+bool make_box_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, bool f32) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)(cols * (f32 ? 4 : 2))};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Where the operands of a product lie, for the maps.
+struct Operands {
+  const void *a_codes, *a_sf, *b_codes, *b_sf;
+  int64_t a_rows, a_cols, b_rows, b_cols, d_rows;
+};
+
+template <int KIND, int BN, int DMODE>
+nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStream_t stream) {
+  using L = PairGroup<BN, DMODE>;
+  auto kern = group_pair_kernel<KIND, BN, DMODE>;
+  static GemmLaunchState ls;
+  const int pairs = gemm_setup(ls, kern, L::kAlloc, L::kThreads, L::kSplitRegs, true, sms);
+  if (pairs <= 0) return NVFP4_ERR_CUDA;
+  a.num_m_blk = (a.M + 255) / 256;
+  a.num_n_blk = (a.N + BN - 1) / BN;
+  CUtensorMap ma, mb, mb2, msa, msb, md;
+  if (!make_code_map(&ma, o.a_codes, o.a_rows, o.a_cols / 2, 128) ||
+      !make_code_map(&mb, o.b_codes, o.b_rows, o.b_cols / 2, 128) ||
+      !make_code_map(&mb2, o.b_codes, o.b_rows, o.b_cols / 2, 64) ||
+      !make_sf_map(&msa, o.a_sf, swizzled_scale_bytes(o.a_rows, o.a_cols)) ||
+      !make_sf_map(&msb, o.b_sf, swizzled_scale_bytes(o.b_rows, o.b_cols)) ||
+      !make_box_map(&md, a.D, o.d_rows, a.N, L::kF32))
+    return NVFP4_ERR_CUDA;
+  return cuda_status(launch_pdl(kern, 2 * pairs, L::kThreads, L::kAlloc, stream, ma, mb, mb2, msa,
+                                msb, md, a));
+}
+
 template <int KIND, int BN, int STAGES, int DMODE>
-nvfp4_status launch_group(const CUtensorMap& ma, const CUtensorMap& mb, const GroupArgs& a,
-                          int sms, cudaStream_t stream) {
+nvfp4_status launch_group(const Operands& o, GroupArgs a, int sms, cudaStream_t stream) {
   using L = GroupSmem<BN, STAGES>;
   auto kern = group_gemm_kernel<KIND, BN, STAGES, DMODE>;
   static GemmLaunchState ls;
   if (gemm_setup(ls, kern, L::kAlloc, kThreads, 0, false, sms) <= 0) return NVFP4_ERR_CUDA;
+  a.num_m_blk = a.M / kBM;
+  a.num_n_blk = (a.N + BN - 1) / BN;
+  CUtensorMap ma, mb;
+  if (!make_code_map(&ma, o.a_codes, o.a_rows, o.a_cols / 2, kBM) ||
+      !make_code_map(&mb, o.b_codes, o.b_rows, o.b_cols / 2, BN))
+    return NVFP4_ERR_CUDA;
   return cuda_status(launch_pdl(kern, sms, kThreads, L::kAlloc, stream, ma, mb, a));
+}
+
+template <int KIND, int DMODE>
+nvfp4_status launch_tile(int32_t tile, const Operands& o, const GroupArgs& a, int sms,
+                         cudaStream_t stream) {
+  if (tile == NVFP4_TILE_PAIR_256X256)
+    return launch_group_pair<KIND, 256, DMODE>(o, a, sms, stream);
+  if constexpr (DMODE != NVFP4_D_F32_ACCUM)
+    if (tile == NVFP4_TILE_PAIR_256X384)
+      return launch_group_pair<KIND, 384, DMODE>(o, a, sms, stream);
+  return launch_group<KIND, 256, 4, DMODE>(o, a, sms, stream);
+}
+
+// The tile of a product whose groups have `per` rows (a contraction: elements)
+// on average.
+int32_t group_tile(int32_t tile, int kind, int64_t per, int64_t n, bool f32) {
+  if (tile != NVFP4_TILE_AUTO) return tile;
+  return f32 || per < 256 || n < 2048 ? NVFP4_TILE_PAIR_256X256 : NVFP4_TILE_PAIR_256X384;
+}
+
+bool known_tile(int32_t tile, int32_t d_mode) {
+  return tile == NVFP4_TILE_AUTO || tile == NVFP4_TILE_128X256 ||
+         tile == NVFP4_TILE_PAIR_256X256 ||
+         (tile == NVFP4_TILE_PAIR_256X384 && d_mode != NVFP4_D_F32_ACCUM);
 }
 
 nvfp4_status check_groups(const nvfp4_tensor* A, const nvfp4_tensor* B, const int32_t* sizes,
@@ -451,17 +946,18 @@ nvfp4_status group_read_error(unsigned int* code) {
 nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
                              const int32_t* sizes, const int32_t* offsets, int32_t groups,
                              void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
-                             int64_t K, cudaStream_t stream) {
+                             int64_t K, int32_t tile, cudaStream_t stream) {
   nvfp4_status st = check_groups(A, B, sizes, offsets, groups, D);
   if (st != NVFP4_OK) return st;
   if (b_view < 0 || b_view > 1) return NVFP4_ERR_INVALID_ARG;
   if (d_mode != NVFP4_D_BF16 && d_mode != NVFP4_D_BF16_ADD_C) return NVFP4_ERR_INVALID_ARG;
-  if ((d_mode == NVFP4_D_BF16_ADD_C) != (C != nullptr)) return NVFP4_ERR_INVALID_ARG;
+  if ((d_mode == NVFP4_D_BF16_ADD_C) != (C != nullptr) || !known_tile(tile, d_mode))
+    return NVFP4_ERR_INVALID_ARG;
   const void* b_codes = b_view ? B->codes_t : B->codes;
   const void* b_sf = b_view ? B->scales_t : B->scales;
   if (!b_codes || !b_sf) return NVFP4_ERR_INVALID_ARG;
   if (rows <= 0 || rows % 128 || N <= 0 || N % 128 || K <= 0 || K % 64) return NVFP4_ERR_SHAPE;
-  if (rows > INT32_MAX - 256 || groups * N > INT32_MAX || groups * K > INT32_MAX)
+  if (rows > INT32_MAX - 256 || groups * N > INT32_MAX - 512 || groups * K > INT32_MAX)
     return NVFP4_ERR_SHAPE;
   if (A->rows != rows || A->cols != K) return NVFP4_ERR_SHAPE;
   if (b_view ? (B->rows != groups * K || B->cols != N) : (B->rows != groups * N || B->cols != K))
@@ -491,26 +987,26 @@ nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32
   a.nrb_b = (int)(b_rows / 128);
   a.b_row_step = b_view ? 0 : (int)N;
   a.b_atom_step = b_view ? (int)(K / kAtom) : 0;
-  a.num_n_blk = (int)((N + 255) / 256);
-  CUtensorMap ma, mb;
-  if (!make_code_map(&ma, A->codes, rows, K / 2, kBM) ||
-      !make_code_map(&mb, b_codes, b_rows, b_cols / 2, 256))
-    return NVFP4_ERR_CUDA;
+  const Operands o = {A->codes, A->scales, b_codes, b_sf, rows, K, b_rows, b_cols, rows};
+  tile = group_tile(tile, kRows, rows / groups, N, false);
   return d_mode == NVFP4_D_BF16
-             ? launch_group<kRows, 256, 4, NVFP4_D_BF16>(ma, mb, a, dev.sm_count, stream)
-             : launch_group<kRows, 256, 4, NVFP4_D_BF16_ADD_C>(ma, mb, a, dev.sm_count, stream);
+             ? launch_tile<kRows, NVFP4_D_BF16>(tile, o, a, dev.sm_count, stream)
+             : launch_tile<kRows, NVFP4_D_BF16_ADD_C>(tile, o, a, dev.sm_count, stream);
 }
 
 nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, const int32_t* sizes,
                               const int32_t* offsets, int32_t groups, void* D, int32_t d_mode,
-                              int64_t M, int64_t N, int64_t rows, cudaStream_t stream) {
+                              int64_t M, int64_t N, int64_t rows, int32_t tile,
+                              cudaStream_t stream) {
   nvfp4_status st = check_groups(A, B, sizes, offsets, groups, D);
   if (st != NVFP4_OK) return st;
   if (!B->codes || !B->scales) return NVFP4_ERR_INVALID_ARG;
   if (d_mode != NVFP4_D_BF16 && d_mode != NVFP4_D_F32_ACCUM) return NVFP4_ERR_INVALID_ARG;
+  if (!known_tile(tile, d_mode)) return NVFP4_ERR_INVALID_ARG;
   if (rows <= 0 || rows % 128 || M <= 0 || M % 128 || N <= 0 || N % 128) return NVFP4_ERR_SHAPE;
   if (rows > INT32_MAX - 256 || M > INT32_MAX - 256 || N > INT32_MAX - 256) return NVFP4_ERR_SHAPE;
-  if ((M / 128) * (N / 128) * groups > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
+  if ((M / 128) * (N / 128) * groups > INT32_MAX - 1024 || M * groups > INT32_MAX)
+    return NVFP4_ERR_SHAPE;
   if (A->rows != M || A->cols != rows || B->rows != N || B->cols != rows) return NVFP4_ERR_SHAPE;
   if (!aligned16(A->codes) || !aligned16(A->scales) || !aligned16(B->codes) ||
       !aligned16(B->scales) || !aligned16(D) || !aligned4(sizes) || !aligned4(offsets))
@@ -532,15 +1028,11 @@ nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, cons
   a.N = (int)N;
   a.kga = a.kgb = (int)(rows / kAtom);
   a.nrb_b = (int)(N / 128);
-  a.num_m_blk = (int)(M / kBM);
-  a.num_n_blk = (int)((N + 255) / 256);
-  CUtensorMap ma, mb;
-  if (!make_code_map(&ma, A->codes, M, rows / 2, kBM) ||
-      !make_code_map(&mb, B->codes, N, rows / 2, 256))
-    return NVFP4_ERR_CUDA;
+  const Operands o = {A->codes, A->scales, B->codes, B->scales, M, rows, N, rows, groups * M};
+  tile = group_tile(tile, kWgrad, rows / groups, N, d_mode == NVFP4_D_F32_ACCUM);
   return d_mode == NVFP4_D_BF16
-             ? launch_group<kWgrad, 256, 4, NVFP4_D_BF16>(ma, mb, a, dev.sm_count, stream)
-             : launch_group<kWgrad, 256, 4, NVFP4_D_F32_ACCUM>(ma, mb, a, dev.sm_count, stream);
+             ? launch_tile<kWgrad, NVFP4_D_BF16>(tile, o, a, dev.sm_count, stream)
+             : launch_tile<kWgrad, NVFP4_D_F32_ACCUM>(tile, o, a, dev.sm_count, stream);
 }
 
 }  // namespace nvfp4

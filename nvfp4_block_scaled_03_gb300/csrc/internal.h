@@ -114,10 +114,11 @@ nvfp4_status mx_quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int
 nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32_t b_view,
                              const int32_t* sizes, const int32_t* offsets, int32_t groups,
                              void* D, int32_t d_mode, const void* C, int64_t rows, int64_t N,
-                             int64_t K, cudaStream_t stream);
+                             int64_t K, int32_t tile, cudaStream_t stream);
 nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, const int32_t* sizes,
                               const int32_t* offsets, int32_t groups, void* D, int32_t d_mode,
-                              int64_t M, int64_t N, int64_t rows, cudaStream_t stream);
+                              int64_t M, int64_t N, int64_t rows, int32_t tile,
+                              cudaStream_t stream);
 nvfp4_status group_read_error(unsigned int* code);
 nvfp4_status group_set_injection(unsigned int stall, unsigned long long wait_ns);
 

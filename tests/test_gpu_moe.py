@@ -266,9 +266,9 @@ GROUP_DIMS = [(128, 64), (384, 320), (256, 512), (640, 1024)]
 
 @pytest.mark.parametrize("sizes", GROUP_SIZES, ids=str)
 @pytest.mark.parametrize("N,K", GROUP_DIMS)
-@pytest.mark.parametrize("view", [0, 1])
-@pytest.mark.parametrize("spare", [0, 384])
-def test_group_gemm(nv, sizes, N, K, view, spare):
+@pytest.mark.parametrize("view,spare", [(0, 0), (1, 384)])
+@pytest.mark.parametrize("tile", [0, 2, 3, 6])
+def test_group_gemm(nv, sizes, N, K, view, spare, tile):
     import torch
     E = len(sizes)
     s, o, off = _groups(sizes)
@@ -289,7 +289,7 @@ def test_group_gemm(nv, sizes, N, K, view, spare):
         live[off[e]:off[e] + n] = True
     for c in (None, C):
         out = torch.full((rows, N), float("nan"), dtype=torch.bfloat16, device="cuda")
-        nv.nvfp4_group_gemm(A, B, s, o, b_view=view, out=out, C_add=c,
+        nv.nvfp4_group_gemm(A, B, s, o, b_view=view, out=out, C_add=c, tile=tile,
                             d_mode=nv.D_BF16 if c is None else nv.D_BF16_ADD_C)
         got = _f64(out)
         assert (got[~live] == 0).all()
@@ -301,8 +301,8 @@ def test_group_gemm(nv, sizes, N, K, view, spare):
 
 @pytest.mark.parametrize("sizes", GROUP_SIZES, ids=str)
 @pytest.mark.parametrize("M,N", [(128, 128), (384, 256), (256, 640)])
-@pytest.mark.parametrize("spare", [0, 256])
-def test_group_wgrad(nv, sizes, M, N, spare):
+@pytest.mark.parametrize("spare,tile", [(0, 0), (256, 2), (256, 3), (0, 6)])
+def test_group_wgrad(nv, sizes, M, N, spare, tile):
     import torch
     E = len(sizes)
     s, o, off = _groups(sizes)
@@ -322,7 +322,7 @@ def test_group_wgrad(nv, sizes, M, N, spare):
         ref[e] = a[:, w] @ b[:, w].T
         size[e] = np.abs(a[:, w]) @ np.abs(b[:, w]).T
     out = torch.full((E, M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
-    nv.nvfp4_group_wgrad(A, B, s, o, out=out)
+    nv.nvfp4_group_wgrad(A, B, s, o, out=out, tile=tile)
     got = _f64(out)
     for e, n in enumerate(sizes):
         if n:
@@ -331,7 +331,7 @@ def test_group_wgrad(nv, sizes, M, N, spare):
             assert (got[e] == 0).all()
     start = torch.randn(E, M, N, generator=g, device="cuda")
     fold = start.clone()
-    nv.nvfp4_group_wgrad(A, B, s, o, out=fold, d_mode=nv.D_F32_ACCUM)
+    nv.nvfp4_group_wgrad(A, B, s, o, out=fold, d_mode=nv.D_F32_ACCUM, tile=tile if tile < 6 else 0)
     bound = (np.array(sizes)[:, None, None] / 64 + 64) * 2.0 ** -22 * size \
         + 2.0 ** -23 * (np.abs(_f64(start)) + np.abs(ref))
     assert (np.abs(_f64(fold) - (_f64(start) + ref)) <= bound).all()
@@ -341,7 +341,8 @@ def test_group_wgrad(nv, sizes, M, N, spare):
     nv.check_device_errors()
 
 
-def test_group_outside_the_rows_counts_as_empty(nv):
+@pytest.mark.parametrize("tile", [2, 3, 6])
+def test_group_outside_the_rows_counts_as_empty(nv, tile):
     import torch
     g = torch.Generator(device="cuda").manual_seed(1)
     A = nv.nvfp4_quantize(torch.randn(384, 128, generator=g, device="cuda"), nv.ROW_1X16)
@@ -350,7 +351,7 @@ def test_group_outside_the_rows_counts_as_empty(nv):
     sizes = torch.tensor([100, 500, -3, 40, 128], **i)
     offsets = torch.tensor([0, 128, 128, 72, 256, 1 << 30], **i)
     out = torch.full((384, 128), 7.0, dtype=torch.bfloat16, device="cuda")
-    nv.nvfp4_group_gemm(A, B, sizes, offsets, out=out)
+    nv.nvfp4_group_gemm(A, B, sizes, offsets, out=out, tile=tile)
     a, b = _decode(A, 384, 128), _decode(B, 640, 128)
     got = _f64(out)
     H.assert_gemm_close(got[:100], a[:100] @ b[:128].T, "group 0")
@@ -359,7 +360,8 @@ def test_group_outside_the_rows_counts_as_empty(nv):
     nv.check_device_errors()
 
 
-def test_group_wait_expires_then_recovers(nv):
+@pytest.mark.parametrize("tile", [2, 3, 6])
+def test_group_wait_expires_then_recovers(nv, tile):
     """The grouped kernels' bounded waits: with the injected stall nothing
     arrives, the error word is set, and the next call is whole again."""
     import torch
@@ -367,18 +369,18 @@ def test_group_wait_expires_then_recovers(nv):
     A = nv.nvfp4_quantize(torch.randn(256, 256, generator=g, device="cuda"), nv.ROW_1X16)
     B = nv.nvfp4_quantize(torch.randn(512, 256, generator=g, device="cuda"), nv.BLOCK_16X16)
     s, o, off = _groups([100, 128])
-    want = nv.nvfp4_group_gemm(A, B, s, o)
+    want = nv.nvfp4_group_gemm(A, B, s, o, tile=tile)
     nv.check_device_errors()
     nv.debug_inject(nv.STALL_GEMM, 1_000_000)
     try:
-        nv.nvfp4_group_gemm(A, B, s, o)
+        nv.nvfp4_group_gemm(A, B, s, o, tile=tile)
         with pytest.raises(nv.NVFP4Error) as e:
             nv.check_device_errors()
         assert e.value.status == nv.ERR_DEVICE_TIMEOUT
     finally:
         nv.debug_inject(0, 0)
     nv.check_device_errors()
-    assert torch.equal(nv.nvfp4_group_gemm(A, B, s, o), want)
+    assert torch.equal(nv.nvfp4_group_gemm(A, B, s, o, tile=tile), want)
     nv.check_device_errors()
 
 
