@@ -118,7 +118,8 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream);
  * issues no loads, so the consumers' first pipeline wait runs out; nothing is
  * in flight when the kernel gives up, and it returns after recording the
  * timeout (nvfp4_check_device_errors then reports NVFP4_ERR_DEVICE_TIMEOUT):
- *   NVFP4_STALL_QUANTIZE  the quantise passes of nvfp4_quantize
+ *   NVFP4_STALL_QUANTIZE  the quantise passes of nvfp4_quantize, and the row
+ *                         loads of nvfp4_residual_norm_fwd / _bwd
  *   NVFP4_STALL_GEMM      every GEMM kernel (single-SM and CTA-pair tiles;
  *                         on a pair a timeout in either CTA stops both)
  * wait_limit_ns sets how long those kernels' pipeline waits last before they

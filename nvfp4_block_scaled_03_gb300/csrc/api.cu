@@ -63,14 +63,16 @@ nvfp4_status nvfp4_device_check(int device) {
 nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  unsigned int gcode = 0, qcode = 0, ecode = 0;
+  unsigned int gcode = 0, qcode = 0, ecode = 0, ncode = 0;
   nvfp4_status st = gemm_read_error(&gcode);
   if (st != NVFP4_OK) return st;
   st = group_read_error(&ecode);
   if (st != NVFP4_OK) return st;
+  st = norm_read_error(&ncode);
+  if (st != NVFP4_OK) return st;
   st = quant_read_error(&qcode);
   if (st != NVFP4_OK) return st;
-  return (gcode || ecode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
+  return (gcode || ecode || ncode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
 }
 
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
@@ -79,6 +81,8 @@ nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
   const unsigned long long ns = wait_limit_ns ? wait_limit_ns : 2000000000ull;
   if (cudaDeviceSynchronize() != cudaSuccess) return NVFP4_ERR_CUDA;
   nvfp4_status st = quant_set_injection((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u, ns);
+  if (st != NVFP4_OK) return st;
+  st = norm_set_injection((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u, ns);
   if (st != NVFP4_OK) return st;
   st = group_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
   if (st != NVFP4_OK) return st;

@@ -136,6 +136,9 @@ nvfp4_status norm_bwd_impl(const nvfp4_norm_params* q, const void* dy, const voi
                            float* dw_pre, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+nvfp4_status norm_read_error(unsigned int* code);
+nvfp4_status norm_set_injection(unsigned int stall, unsigned long long wait_ns);
+
 // Expert routing (route.cu).
 int64_t route_rows(int64_t tokens, int64_t experts, int32_t top);
 nvfp4_status route_sizes_impl(int64_t tokens, int64_t experts, int32_t top, int64_t* rows,
