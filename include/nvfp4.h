@@ -596,7 +596,7 @@ nvfp4_status nvfp4_combine_bwd(const void* dy, const void* o, const int32_t* row
  * d_mode NVFP4_D_BF16 or NVFP4_D_BF16_ADD_C (adds C bf16 [rows, N] in FP32
  * before the rounding).  D bf16 [rows, N]: padding rows are written as zero
  * whatever A (or C) holds there.  tile: NVFP4_TILE_AUTO, or for tuning and
- * tests NVFP4_TILE_128X256, _PAIR_256X256 or _PAIR_256X384.  Shapes: rows % 128 == 0, N % 128 == 0,
+ * tests NVFP4_TILE_PAIR_256X256 or _PAIR_256X384.  Shapes: rows % 128 == 0, N % 128 == 0,
  * K % 64 == 0, 1 <= groups <= 512.  A group that does not lie in [0, rows) or
  * does not start on a multiple of 128 counts as empty.  One launch.  Returns
  * NVFP4_ERR_INVALID_ARG, _SHAPE, _ALIGN, _ARCH, _CUDA. */
@@ -612,7 +612,7 @@ nvfp4_status nvfp4_group_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, int3
  *   NVFP4_D_BF16       D bf16 [groups, M, N], zeros for an empty group
  *   NVFP4_D_F32_ACCUM  D fp32 [groups, M, N] += the FP32 product, not rounded
  *                      to bf16 in between (an empty group's D stays as it is)
- * tile as nvfp4_group_gemm, _PAIR_256X384 not with NVFP4_D_F32_ACCUM.
+ * tile: NVFP4_TILE_AUTO, _PAIR_256X256, or with NVFP4_D_BF16 _PAIR_256X384.
  * Shapes: rows, M, N multiples of 128, 1 <= groups <= 512.  One launch. */
 nvfp4_status nvfp4_group_wgrad(const nvfp4_tensor* A, const nvfp4_tensor* B,
                                const int32_t* sizes, const int32_t* offsets, int32_t groups,

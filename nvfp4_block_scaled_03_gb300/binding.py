@@ -508,38 +508,65 @@ def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool 
 
 
 # ---- mixture of experts ------------------------------------------------------
+# These calls are made once per layer and token at a server, so their checks
+# are kept to a few attribute reads, and messages are only built to be raised.
 ROUTE_ALL, ROUTE_CHOSEN = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_ROW = 0, 1, 2
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
-
-
-def _want(cond, what):
-    if not cond:
-        raise ValueError(what)
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
 def _cuda(t, dtype, name, shape=None):
-    """A contiguous CUDA tensor of one type (and shape)."""
-    _want(t.is_cuda and t.dtype == dtype and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} CUDA tensor")
-    if shape is not None:
-        _want(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}")
+    """Refuses what is not a contiguous CUDA tensor of one type (and shape)."""
+    if not (t.is_cuda and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor"
+                         + ("" if shape is None else f" of shape {tuple(shape)}"))
+
+
+def _current(t) -> int:
+    """The current stream of a tensor's device, as a handle."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _on_stream(call):
+    """Runs a call with its `stream` as the current one, so that what it
+    allocates (outputs, a workspace) belongs to the stream that uses it."""
+    @functools.wraps(call)
+    def run(*args, stream=None, **kwargs):
+        if stream is None:
+            return call(*args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(*args, **kwargs)
+    return run
+
+
+_moe_ws: dict = {}
+
+
+def _moe_workspace(nbytes, t):
+    """Scratch of the current stream (kept between calls, as large as the largest)."""
+    key = (t.get_device(), _current(t))
+    ws = _moe_ws.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _moe_ws[key] = torch.empty(max(nbytes, 16), dtype=_U8, device=t.device)
+    return ws
 
 
 def operand(codes: torch.Tensor, scales: torch.Tensor, s_dec: torch.Tensor, rows: int,
             cols: int) -> QTensor:
     """A QTensor over buffers that hold a K-major operand [rows, cols] already:
     codes and scales (MMA layout) as uint8, s_dec one float32."""
-    cb, sb, _, _ = quantize_sizes(rows, cols, ROW_1X16)
-    _cuda(codes, torch.uint8, "codes")
-    _cuda(scales, torch.uint8, "scales")
-    _cuda(s_dec, torch.float32, "s_dec")
-    _want(codes.numel() >= cb and scales.numel() >= sb and s_dec.numel() >= 1,
-          "buffers smaller than the operand")
-    q = QTensor(codes=codes, scales=scales, amax=None, s_dec=s_dec)
-    q.desc = Tensor(codes.data_ptr(), scales.data_ptr(), None, None, None, s_dec.data_ptr(), rows,
-                    cols, ROW_1X16, 0)
-    return q
+    _cuda(codes, _U8, "codes")
+    _cuda(scales, _U8, "scales")
+    _cuda(s_dec, _F32, "s_dec")
+    if (rows <= 0 or cols <= 0 or cols % 16 or codes.numel() < rows * cols // 2
+            or scales.numel() < (rows + 127) // 128 * ((cols + 63) // 64) * 512
+            or s_dec.numel() < 1):
+        raise ValueError("buffers smaller than the operand, or cols not a multiple of 16")
+    return QTensor(codes, scales, None, s_dec, None, None,
+                   Tensor(codes.data_ptr(), scales.data_ptr(), None, None, None,
+                          s_dec.data_ptr(), rows, cols, ROW_1X16, 0))
 
 
 def operand_t(codes_t: torch.Tensor, scales_t: torch.Tensor, s_dec: torch.Tensor, rows: int,
@@ -557,8 +584,7 @@ def operand_t(codes_t: torch.Tensor, scales_t: torch.Tensor, s_dec: torch.Tensor
 def route_sizes(tokens, experts, top):
     """(rows of a plan, workspace bytes of nvfp4_route_fwd)."""
     r, w = C.c_int64(), C.c_size_t()
-    _check(lib.nvfp4_route_sizes(tokens, experts, top, C.byref(r), C.byref(w)),
-           "nvfp4_route_sizes")
+    _check(lib.nvfp4_route_sizes(tokens, experts, top, r, w), "nvfp4_route_sizes")
     return r.value, w.value
 
 
@@ -578,78 +604,89 @@ class RoutePlan:
 
 
 def alloc_plan(tokens, experts, top, device="cuda") -> RoutePlan:
+    """Buffers of a plan, e.g. for a server to route into at every step."""
     rows, _ = route_sizes(tokens, experts, top)
-    i = dict(dtype=torch.int32, device=device)
-    return RoutePlan(expert=torch.empty(tokens, top, **i),
-                     weight=torch.empty(tokens, top, dtype=torch.float32, device=device),
-                     sizes=torch.empty(experts, **i), offsets=torch.empty(experts + 1, **i),
-                     row=torch.empty(tokens, top, **i), source=torch.empty(rows, **i))
-
-
-def _on_stream(call):
-    """Runs a call with its `stream` as the current one, so that what it
-    allocates (outputs, a workspace) belongs to the stream that uses it."""
-    @functools.wraps(call)
-    def run(*args, stream=None, **kwargs):
-        if stream is None:
-            return call(*args, **kwargs)
-        with torch.cuda.stream(stream):
-            return call(*args, **kwargs)
-    return run
+    empty = torch.empty
+    return RoutePlan(empty((tokens, top), dtype=_I32, device=device),
+                     empty((tokens, top), dtype=_F32, device=device),
+                     empty(experts, dtype=_I32, device=device),
+                     empty(experts + 1, dtype=_I32, device=device),
+                     empty((tokens, top), dtype=_I32, device=device),
+                     empty(rows, dtype=_I32, device=device))
 
 
 def _logits(logits):
-    _want(logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1,
-          "logits must be a 2-D CUDA tensor with unit column stride")
-    if logits.dtype not in _DTYPES:
+    if not (logits.is_cuda and logits.dim() == 2 and logits.stride(1) == 1):
+        raise ValueError("logits must be a 2-D CUDA tensor with unit column stride")
+    kind = _DTYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits must be bf16 or fp32, got {logits.dtype}")
     tokens, experts = logits.shape
-    return tokens, experts, logits.stride(0) if tokens > 1 else experts
+    return kind, tokens, experts, logits.stride(0) if tokens > 1 else experts
 
 
 @_on_stream
 def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
-                    plan: RoutePlan | None = None, workspace: torch.Tensor | None = None) -> RoutePlan:
+                    plan: RoutePlan | None = None,
+                    workspace: torch.Tensor | None = None) -> RoutePlan:
     """Choose each token's `top` experts and order the rows by expert (see
     nvfp4_route_fwd in nvfp4.h)."""
-    tokens, experts, ld = _logits(logits)
-    rows, wsb = route_sizes(tokens, experts, top)
+    kind, tokens, experts, ld = _logits(logits)
     if plan is None:
         plan = alloc_plan(tokens, experts, top, logits.device)
     else:
-        for name, shape in (("expert", (tokens, top)), ("row", (tokens, top)),
-                            ("sizes", (experts,)), ("offsets", (experts + 1,)),
-                            ("source", (rows,))):
-            _cuda(getattr(plan, name), torch.int32, name, shape)
-        _cuda(plan.weight, torch.float32, "weight", (tokens, top))
+        _cuda(plan.expert, _I32, "expert", (tokens, top))
+        _cuda(plan.weight, _F32, "weight", (tokens, top))
+        _cuda(plan.sizes, _I32, "sizes", (experts,))
+        _cuda(plan.offsets, _I32, "offsets", (experts + 1,))
+        _cuda(plan.row, _I32, "row", (tokens, top))
+        _cuda(plan.source, _I32, "source", (route_sizes(tokens, experts, top)[0],))
     if workspace is None:
-        workspace = _workspace(wsb, logits.device)
-    _check(lib.nvfp4_route_fwd(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, ld, top,
-                               mode, plan.expert.data_ptr(), plan.weight.data_ptr(),
-                               plan.sizes.data_ptr(), plan.offsets.data_ptr(),
-                               plan.row.data_ptr(), plan.source.data_ptr(), workspace.data_ptr(),
-                               workspace.numel(), _stream(None)), "nvfp4_route_fwd")
+        workspace = _moe_workspace(route_sizes(tokens, experts, top)[1], logits)
+    st = lib.nvfp4_route_fwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
+                             plan.expert.data_ptr(), plan.weight.data_ptr(),
+                             plan.sizes.data_ptr(), plan.offsets.data_ptr(), plan.row.data_ptr(),
+                             plan.source.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                             _current(logits))
+    if st:
+        raise NVFP4Error(st, "nvfp4_route_fwd")
     return plan
 
 
 @_on_stream
 def nvfp4_route_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor,
-                    mode: int = ROUTE_CHOSEN, dlogits: torch.Tensor | None = None) -> torch.Tensor:
+                    mode: int = ROUTE_CHOSEN,
+                    dlogits: torch.Tensor | None = None) -> torch.Tensor:
     """The logits' gradient from that of the plan's weights."""
-    tokens, experts, ld = _logits(logits)
+    kind, tokens, experts, ld = _logits(logits)
     top = plan.expert.shape[1]
-    _cuda(plan.expert, torch.int32, "expert", (tokens, top))
-    _cuda(plan.weight, torch.float32, "weight", (tokens, top))
-    _cuda(dweight, torch.float32, "dweight", (tokens, top))
+    _cuda(plan.expert, _I32, "expert", (tokens, top))
+    _cuda(plan.weight, _F32, "weight", (tokens, top))
+    _cuda(dweight, _F32, "dweight", (tokens, top))
     if dlogits is None:
         dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
     else:
         _cuda(dlogits, logits.dtype, "dlogits", (tokens, experts))
-    _check(lib.nvfp4_route_bwd(logits.data_ptr(), _DTYPES[logits.dtype], tokens, experts, ld, top,
-                               mode, plan.expert.data_ptr(), plan.weight.data_ptr(),
-                               dweight.data_ptr(), dlogits.data_ptr(), _stream(None)),
-           "nvfp4_route_bwd")
+    st = lib.nvfp4_route_bwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
+                             plan.expert.data_ptr(), plan.weight.data_ptr(), dweight.data_ptr(),
+                             dlogits.data_ptr(), _current(logits))
+    if st:
+        raise NVFP4Error(st, "nvfp4_route_bwd")
     return dlogits
+
+
+def _rows2d(t, name):
+    _cuda(t, _BF16, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def _slots(row):
+    _cuda(row, _I32, "row")
+    if row.dim() != 2:
+        raise ValueError("row must be [tokens, top]")
+    return row.shape
 
 
 @_on_stream
@@ -657,18 +694,20 @@ def nvfp4_dispatch(x: torch.Tensor, row: torch.Tensor, source: torch.Tensor,
                    out: torch.Tensor | None = None) -> torch.Tensor:
     """x's rows in the order of a plan's groups (`row`, `source` of a
     RoutePlan), padding rows zero (see nvfp4_dispatch in nvfp4.h)."""
-    tokens, top = row.shape
+    tokens, top = _slots(row)
+    n, cols = _rows2d(x, "x")
+    if n != tokens:
+        raise ValueError("x must have one row per token")
+    _cuda(source, _I32, "source")
     rows = source.numel()
-    _cuda(x, torch.bfloat16, "x")
-    _want(x.dim() == 2 and x.shape[0] == tokens, "x must have one row per token")
-    _cuda(row, torch.int32, "row")
-    _cuda(source, torch.int32, "source")
     if out is None:
-        out = torch.empty((rows, x.shape[1]), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((rows, cols), dtype=_BF16, device=x.device)
     else:
-        _cuda(out, torch.bfloat16, "out", (rows, x.shape[1]))
-    _check(lib.nvfp4_dispatch(x.data_ptr(), row.data_ptr(), source.data_ptr(), tokens, x.shape[1],
-                              top, rows, out.data_ptr(), _stream(None)), "nvfp4_dispatch")
+        _cuda(out, _BF16, "out", (rows, cols))
+    st = lib.nvfp4_dispatch(x.data_ptr(), row.data_ptr(), source.data_ptr(), tokens, cols, top,
+                            rows, out.data_ptr(), _current(x))
+    if st:
+        raise NVFP4Error(st, "nvfp4_dispatch")
     return out
 
 
@@ -677,18 +716,19 @@ def nvfp4_combine(o: torch.Tensor, row: torch.Tensor, weight: torch.Tensor | Non
                   out: torch.Tensor | None = None) -> torch.Tensor:
     """Each token's weighted sum of its rows of `o`; without weights, the
     gradient of nvfp4_dispatch (see nvfp4_combine in nvfp4.h)."""
-    tokens, top = row.shape
-    _cuda(o, torch.bfloat16, "o")
-    _want(o.dim() == 2, "o must be 2-D")
-    _cuda(row, torch.int32, "row")
+    tokens, top = _slots(row)
+    rows, cols = _rows2d(o, "o")
     if weight is not None:
-        _cuda(weight, torch.float32, "weight", (tokens, top))
+        _cuda(weight, _F32, "weight", (tokens, top))
     if out is None:
-        out = torch.empty((tokens, o.shape[1]), dtype=torch.bfloat16, device=o.device)
+        out = torch.empty((tokens, cols), dtype=_BF16, device=o.device)
     else:
-        _cuda(out, torch.bfloat16, "out", (tokens, o.shape[1]))
-    _check(lib.nvfp4_combine(o.data_ptr(), row.data_ptr(), _ptr(weight), tokens, o.shape[1], top,
-                             o.shape[0], out.data_ptr(), _stream(None)), "nvfp4_combine")
+        _cuda(out, _BF16, "out", (tokens, cols))
+    st = lib.nvfp4_combine(o.data_ptr(), row.data_ptr(),
+                           None if weight is None else weight.data_ptr(), tokens, cols, top, rows,
+                           out.data_ptr(), _current(o))
+    if st:
+        raise NVFP4Error(st, "nvfp4_combine")
     return out
 
 
@@ -697,33 +737,31 @@ def nvfp4_combine_bwd(dy: torch.Tensor, o: torch.Tensor, row: torch.Tensor, sour
                       weight: torch.Tensor, d_o: torch.Tensor | None = None,
                       dweight: torch.Tensor | None = None):
     """(d_o, dweight) of nvfp4_combine (see nvfp4_combine_bwd in nvfp4.h)."""
-    tokens, top = row.shape
-    _cuda(o, torch.bfloat16, "o")
-    _want(o.dim() == 2, "o must be 2-D")
-    rows, cols = o.shape
-    _cuda(dy, torch.bfloat16, "dy", (tokens, cols))
-    _cuda(row, torch.int32, "row")
-    _cuda(source, torch.int32, "source", (rows,))
-    _cuda(weight, torch.float32, "weight", (tokens, top))
+    tokens, top = _slots(row)
+    rows, cols = _rows2d(o, "o")
+    _cuda(dy, _BF16, "dy", (tokens, cols))
+    _cuda(source, _I32, "source", (rows,))
+    _cuda(weight, _F32, "weight", (tokens, top))
     if d_o is None:
         d_o = torch.empty_like(o)
     else:
-        _cuda(d_o, torch.bfloat16, "d_o", (rows, cols))
+        _cuda(d_o, _BF16, "d_o", (rows, cols))
     if dweight is None:
         dweight = torch.empty_like(weight)
     else:
-        _cuda(dweight, torch.float32, "dweight", (tokens, top))
-    _check(lib.nvfp4_combine_bwd(dy.data_ptr(), o.data_ptr(), row.data_ptr(), source.data_ptr(),
-                                 weight.data_ptr(), tokens, cols, top, rows, d_o.data_ptr(),
-                                 dweight.data_ptr(), _stream(None)), "nvfp4_combine_bwd")
+        _cuda(dweight, _F32, "dweight", (tokens, top))
+    st = lib.nvfp4_combine_bwd(dy.data_ptr(), o.data_ptr(), row.data_ptr(), source.data_ptr(),
+                               weight.data_ptr(), tokens, cols, top, rows, d_o.data_ptr(),
+                               dweight.data_ptr(), _current(o))
+    if st:
+        raise NVFP4Error(st, "nvfp4_combine_bwd")
     return d_o, dweight
 
 
 def _groups(sizes, offsets):
     groups = sizes.numel()
-    _cuda(sizes, torch.int32, "sizes")
-    _cuda(offsets, torch.int32, "offsets")
-    _want(offsets.numel() == groups + 1, "offsets must have one entry more than sizes")
+    _cuda(sizes, _I32, "sizes")
+    _cuda(offsets, _I32, "offsets", (groups + 1,))
     return groups
 
 
@@ -734,17 +772,21 @@ def nvfp4_group_gemm(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torch
     """D[r] = alpha A[r] . B_e^T for the rows r of each group e (see
     nvfp4_group_gemm in nvfp4.h); returns D bf16 [rows, N]."""
     groups = _groups(sizes, offsets)
-    rows, K = A.desc.rows, A.desc.cols
-    N = B.desc.cols if b_view else B.desc.rows // groups
+    a, b = A.desc, B.desc
+    rows, K = a.rows, a.cols
+    N = b.cols if b_view else b.rows // groups
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=A.s_dec.device)
+        out = torch.empty((rows, N), dtype=_BF16, device=sizes.device)
     else:
-        _cuda(out, torch.bfloat16, "out", (rows, N))
+        _cuda(out, _BF16, "out", (rows, N))
     if C_add is not None:
-        _cuda(C_add, torch.bfloat16, "C_add", (rows, N))
-    _check(lib.nvfp4_group_gemm(A.desc, B.desc, b_view, sizes.data_ptr(), offsets.data_ptr(),
-                                groups, out.data_ptr(), d_mode, _ptr(C_add), rows, N, K, tile,
-                                _stream(None)), "nvfp4_group_gemm")
+        _cuda(C_add, _BF16, "C_add", (rows, N))
+    st = lib.nvfp4_group_gemm(a, b, b_view, sizes.data_ptr(), offsets.data_ptr(), groups,
+                              out.data_ptr(), d_mode,
+                              None if C_add is None else C_add.data_ptr(), rows, N, K, tile,
+                              _current(sizes))
+    if st:
+        raise NVFP4Error(st, "nvfp4_group_gemm")
     return out
 
 
@@ -755,36 +797,44 @@ def nvfp4_group_wgrad(A: QTensor, B: QTensor, sizes: torch.Tensor, offsets: torc
     """D_e = alpha A[:, rows of e] . B[:, rows of e]^T (see nvfp4_group_wgrad in
     nvfp4.h); returns D [groups, M, N], bf16 or (D_F32_ACCUM: folded into) fp32."""
     groups = _groups(sizes, offsets)
-    M, rows, N = A.desc.rows, A.desc.cols, B.desc.rows
-    dtype = torch.float32 if d_mode == D_F32_ACCUM else torch.bfloat16
+    a, b = A.desc, B.desc
+    M, rows, N = a.rows, a.cols, b.rows
+    dtype = _F32 if d_mode == D_F32_ACCUM else _BF16
     if out is None:
         out = (torch.zeros if d_mode == D_F32_ACCUM else torch.empty)(
-            (groups, M, N), dtype=dtype, device=A.s_dec.device)
+            (groups, M, N), dtype=dtype, device=sizes.device)
     else:
         _cuda(out, dtype, "out", (groups, M, N))
-    _check(lib.nvfp4_group_wgrad(A.desc, B.desc, sizes.data_ptr(), offsets.data_ptr(), groups,
-                                 out.data_ptr(), d_mode, M, N, rows, tile, _stream(None)),
-           "nvfp4_group_wgrad")
+    st = lib.nvfp4_group_wgrad(a, b, sizes.data_ptr(), offsets.data_ptr(), groups, out.data_ptr(),
+                               d_mode, M, N, rows, tile, _current(sizes))
+    if st:
+        raise NVFP4Error(st, "nvfp4_group_wgrad")
     return out
 
 
 def _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale):
-    _want(x.is_cuda and x.dim() == 2 and x.is_contiguous(), "x must be a contiguous 2-D CUDA tensor")
-    if x.dtype not in _DTYPES:
+    """The call's parameters, and the five inputs' addresses."""
+    if not (x.is_cuda and x.dim() == 2 and x.is_contiguous()):
+        raise ValueError("x must be a contiguous 2-D CUDA tensor")
+    kind = _DTYPES.get(x.dtype)
+    if kind is None:
         raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
     rows, cols = x.shape
+    mode, pz, pw, pg, pp = GATE_NONE, None, None, None, None
     if z is not None:
-        _cuda(z, torch.bfloat16, "z", (rows, cols))
-    for t, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if t is not None:
-            _cuda(t, torch.float32, name, (cols,))
-    mode = GATE_NONE
+        _cuda(z, _BF16, "z", (rows, cols))
+        pz = z.data_ptr()
+    if w_post is not None:
+        _cuda(w_post, _F32, "w_post", (cols,))
+        pw = w_post.data_ptr()
     if gate is not None:
         mode = GATE_CHANNEL if gate.dim() == 1 else GATE_ROW
-        _want(tuple(gate.shape) == ((cols,) if mode == GATE_CHANNEL else (rows, 1)),
-              f"gate must have shape {(cols,)} or {(rows, 1)}")
-        _cuda(gate, torch.float32, "gate")
-    return NormParams(rows, cols, _DTYPES[x.dtype], mode, eps, x_scale, z_scale)
+        _cuda(gate, _F32, "gate", (cols,) if mode == GATE_CHANNEL else (rows, 1))
+        pg = gate.data_ptr()
+    if w_pre is not None:
+        _cuda(w_pre, _F32, "w_pre", (cols,))
+        pp = w_pre.data_ptr()
+    return NormParams(rows, cols, kind, mode, eps, x_scale, z_scale), (x.data_ptr(), pz, pw, pg, pp)
 
 
 @_on_stream
@@ -798,18 +848,19 @@ def nvfp4_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor | None = None,
     z, y is only written when given or x_scale is not 1 (and is x otherwise);
     without w_pre, h is None.  A gate [rows, 1] is per row, one of [cols] per
     channel."""
-    p = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
-    if y is None:
-        y = torch.empty_like(x) if z is not None or x_scale != 1.0 else None
-    else:
+    p, ins = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
+    if y is not None:
         _cuda(y, x.dtype, "y", x.shape)
-    if h is None:
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if w_pre is not None else None
-    else:
-        _cuda(h, torch.bfloat16, "h", x.shape)
-    _check(lib.nvfp4_residual_norm_fwd(p, x.data_ptr(), _ptr(z), _ptr(w_post), _ptr(gate),
-                                       _ptr(w_pre), _ptr(y), _ptr(h), _stream(None)),
-           "nvfp4_residual_norm_fwd")
+    elif z is not None or x_scale != 1.0:
+        y = torch.empty_like(x)
+    if h is not None:
+        _cuda(h, _BF16, "h", x.shape)
+    elif w_pre is not None:
+        h = torch.empty_like(x, dtype=_BF16)
+    st = lib.nvfp4_residual_norm_fwd(p, *ins, None if y is None else y.data_ptr(),
+                                     None if h is None else h.data_ptr(), _current(x))
+    if st:
+        raise NVFP4Error(st, "nvfp4_residual_norm_fwd")
     return (x if y is None else y), h
 
 
@@ -821,24 +872,22 @@ def nvfp4_residual_norm_bwd(dy: torch.Tensor | None, dh: torch.Tensor | None, x:
                             workspace: torch.Tensor | None = None):
     """(dx, dz, dw_post, dgate, dw_pre) of nvfp4_residual_norm_fwd from the
     gradients of y and h (None: zero); an entry is None where its input is."""
-    p = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
+    p, ins = _norm_args(x, z, w_post, gate, w_pre, eps, x_scale, z_scale)
     if dy is not None:
         _cuda(dy, x.dtype, "dy", x.shape)
     if dh is not None:
-        _cuda(dh, torch.bfloat16, "dh", x.shape)
+        _cuda(dh, _BF16, "dh", x.shape)
     if workspace is None:
         n = C.c_size_t()
-        _check(lib.nvfp4_residual_norm_bwd_sizes(p.rows, p.cols, C.byref(n)),
+        _check(lib.nvfp4_residual_norm_bwd_sizes(p.rows, p.cols, n),
                "nvfp4_residual_norm_bwd_sizes")
-        workspace = _workspace(n.value, x.device)
-    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    dx, dz, dw_post, dgate, dw_pre = like(x), like(z), like(w_post), like(gate), like(w_pre)
-    _check(lib.nvfp4_residual_norm_bwd(p, _ptr(dy), _ptr(dh), x.data_ptr(), _ptr(z), _ptr(w_post),
-                                       _ptr(gate), _ptr(w_pre), dx.data_ptr(), _ptr(dz),
-                                       _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
-                                       workspace.data_ptr(), workspace.numel(), _stream(None)),
-           "nvfp4_residual_norm_bwd")
-    return dx, dz, dw_post, dgate, dw_pre
+        workspace = _moe_workspace(n.value, x)
+    outs = [None if t is None else torch.empty_like(t) for t in (x, z, w_post, gate, w_pre)]
+    st = lib.nvfp4_residual_norm_bwd(p, _ptr(dy), _ptr(dh), *ins, *[_ptr(t) for t in outs],
+                                     workspace.data_ptr(), workspace.numel(), _current(x))
+    if st:
+        raise NVFP4Error(st, "nvfp4_residual_norm_bwd")
+    return tuple(outs)
 
 
 STALL_QUANTIZE, STALL_GEMM = 1, 2

@@ -10,22 +10,20 @@
 // sizes and offsets once into a table in shared memory and walks its output
 // tiles, group after group; no host round trip, one launch for all groups.
 //
-// Kernel (one CTA per SM, persistent): warp 0 the TMA producer, warp 1 the
-// thread that copies scales to tensor memory and issues the MMAs
-// (tcgen05.mma kind::mxf4nvf4, K = 64), warps 2..9 the epilogue, as in
-// gemm.cu's single-SM kernel, whose waits, abort and drain rules hold here too.
-// What differs: a tile's operand rows, contraction window and length come from
-// the table; a contraction ends at the group's last whole atom of 64 (rows past
-// a group's size hold zeros there); output rows past a group's size are
-// written as zeros whatever A holds there, and so are the rows behind the
-// last group; an empty group's weight gradient is zero.
+// The kernels follow gemm.cu's (persistent CTAs; a TMA producer, MMA, scale and
+// epilogue warps around a ring of stages; tcgen05.mma kind::mxf4nvf4, K = 64) and
+// its rules on waits, aborts and drains.  What differs: a tile's operand rows,
+// contraction window and length come from the table; a contraction ends at the
+// group's last whole atom of 64 (rows past a group's size hold zeros there);
+// output rows past a group's size are written as zeros whatever A holds there,
+// and so are the rows behind the last group; an empty group's weight gradient
+// is zero.
 #include "gemm_common.cuh"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 320;  // producer, MMA, 8 epilogue warps
-constexpr int kBM = 128;
+constexpr int kBM = 256;       // rows of a CTA pair's tile
 constexpr int kAtom = 64;      // contraction elements per scale atom
 constexpr int kMaxGroups = 512;
 
@@ -58,7 +56,6 @@ struct GroupTable {
 
 // A group that does not lie in [0, rows), or starts inside a block of 128,
 // counts as empty.
-template <int KIND, int BM>
 NVFP4_DEV void fill_table(GroupTable* t, const GroupArgs& a) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
@@ -71,7 +68,7 @@ NVFP4_DEV void fill_table(GroupTable* t, const GroupArgs& a) {
         off = a.offsets[g];
         if (size < 0 || off < 0 || off % 128 || off > a.rows || size > a.rows - off) size = off = 0;
       }
-      const int blocks = (size + BM - 1) / BM;
+      const int blocks = (size + kBM - 1) / kBM;
       int s = blocks;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -107,7 +104,7 @@ struct Tile {
 // Tiles come in rising order, so the group is found by stepping on from the
 // last one.  Within a group the row blocks run fastest: neighbouring CTAs
 // share a tile of weights.
-template <int KIND, int BM, int BN>
+template <int KIND, int BN>
 NVFP4_DEV Tile tile_at(int tile, int& g, const GroupTable* t, const GroupArgs& a) {
   Tile r;
   if (KIND == kRows) {
@@ -115,20 +112,20 @@ NVFP4_DEV Tile tile_at(int tile, int& g, const GroupTable* t, const GroupArgs& a
     const int mb = t->first[g + 1] - t->first[g];
     const int local = tile - t->first[g] * a.num_n_blk;
     const int m = local % mb, n = local / mb;
-    r.a_row = t->off[g] + m * BM;
+    r.a_row = t->off[g] + m * kBM;
     r.b_row = g * a.b_row_step + n * BN;
     r.a_atom = 0;
     r.b_atom = g * a.b_atom_step;
     r.atoms = a.K / kAtom;
     r.d_row = r.a_row;
     r.d_col = n * BN;
-    r.live = t->size[g] - m * BM;
+    r.live = t->size[g] - m * kBM;
   } else {
     const int per = a.num_m_blk * a.num_n_blk;
     g = tile / per;
     const int local = tile - g * per;
     const int m = local % a.num_m_blk, n = local / a.num_m_blk;
-    r.a_row = m * BM;
+    r.a_row = m * kBM;
     r.b_row = n * BN;
     r.a_atom = r.b_atom = t->off[g] / kAtom;
     r.atoms = (t->size[g] + kAtom - 1) / kAtom;
@@ -137,58 +134,6 @@ NVFP4_DEV Tile tile_at(int tile, int& g, const GroupTable* t, const GroupArgs& a
     r.live = a.M - r.a_row;
   }
   return r;
-}
-
-// Thirty-two columns of one row of D from FP32 accumulators.  A row that is
-// not live is written as zero (as C alone where C is added).
-template <int DMODE>
-NVFP4_DEV void store_cols(const GroupArgs& a, int64_t row, int col0, const uint32_t (&r)[32],
-                          float alpha, bool live) {
-  if (DMODE == NVFP4_D_F32_ACCUM) {
-    float* D = static_cast<float*>(a.D) + row * a.N + col0;
-#pragma unroll
-    for (int g0 = 0; g0 < 8; g0 += 4) {
-      float4 d[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if (col0 + (g0 + g) * 4 < a.N) d[g] = *reinterpret_cast<const float4*>(D + (g0 + g) * 4);
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (col0 + (g0 + g) * 4 >= a.N) break;
-        const uint32_t* v = r + (g0 + g) * 4;
-        d[g].x = fmaf(alpha, __uint_as_float(v[0]), d[g].x);
-        d[g].y = fmaf(alpha, __uint_as_float(v[1]), d[g].y);
-        d[g].z = fmaf(alpha, __uint_as_float(v[2]), d[g].z);
-        d[g].w = fmaf(alpha, __uint_as_float(v[3]), d[g].w);
-        *reinterpret_cast<float4*>(D + (g0 + g) * 4) = d[g];
-      }
-    }
-    return;
-  }
-  __nv_bfloat16* D = static_cast<__nv_bfloat16*>(a.D) + row * a.N + col0;
-  const __nv_bfloat16* Cp = static_cast<const __nv_bfloat16*>(a.C) + row * a.N + col0;
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    if (col0 + g * 8 >= a.N) break;
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = live ? __fmul_rn(__uint_as_float(r[g * 8 + e]), alpha) : 0.0f;
-    if (DMODE == NVFP4_D_BF16_ADD_C && live) {
-      const uint4 c = *reinterpret_cast<const uint4*>(Cp + g * 8);
-      const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[2 * e] = __fadd_rn(f[2 * e], __uint_as_float(cw[e] << 16));
-        f[2 * e + 1] = __fadd_rn(f[2 * e + 1], __uint_as_float(cw[e] & 0xFFFF0000u));
-      }
-    }
-    uint4 o;
-    o.x = pack_bf16x2(f[0], f[1]);
-    o.y = pack_bf16x2(f[2], f[3]);
-    o.z = pack_bf16x2(f[4], f[5]);
-    o.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4*>(D + g * 8) = o;
-  }
 }
 
 // The rows of D behind the last group become zero (thread `i` of `n`).
@@ -200,220 +145,9 @@ NVFP4_DEV void clear_tail(const GroupArgs& a, int64_t i, int64_t n) {
   for (; i < count; i += n) D[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <int BN, int STAGES>
-struct GroupSmem {
-  static constexpr int kAt = 4;  // scale atoms per stage (256 elements of K)
-  static constexpr uint32_t kA = kBM * kBKBytes, kB = BN * kBKBytes;
-  static constexpr uint32_t kSFA = kAt * 512, kSFB = (BN / 128) * kAt * 512;
-  static constexpr uint32_t offA = 0, offB = offA + STAGES * kA;
-  static constexpr uint32_t offSFA = offB + STAGES * kB, offSFB = offSFA + STAGES * kSFA;
-  static constexpr uint32_t offBar = offSFB + STAGES * kSFB;
-  static constexpr uint32_t kNumBars = 2 * STAGES + 3;  // full, empty, acc full, acc empty, drain
-  static constexpr uint32_t offMisc = offBar + kNumBars * 8;
-  static constexpr uint32_t offTable = offMisc + 16;
-  static constexpr uint32_t kBytes = offTable + sizeof(GroupTable);
-  static constexpr uint32_t kAlloc = kBytes + 1024;  // room to align the base to 1024
-  static constexpr uint32_t kSfCol0 = BN;
-  static constexpr uint32_t kSfColsPerStage = 16 + BN / 8;
-  static_assert(kSfCol0 + STAGES * kSfColsPerStage <= kTmemCols, "tensor memory overflow");
-  static_assert(kAlloc <= 232448, "shared memory overflow");
-};
-
-template <int KIND, int BN, int STAGES, int DMODE>
-__global__ void __launch_bounds__(kThreads, 1)
-    group_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB, const GroupArgs args) {
-  using L = GroupSmem<BN, STAGES>;
-  constexpr int kAt = L::kAt;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + L::offBar;
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  const uint32_t acc_full = bar0 + 8u * (2 * STAGES);
-  const uint32_t acc_empty = acc_full + 8;
-  const uint32_t drain_bar = acc_full + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
-  GroupTable* table = reinterpret_cast<GroupTable*>(smem + L::offTable);
-
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-    }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 8);
-    mbar_init(drain_bar, 1);
-    *abort_flag = 0;
-    fence_mbar_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish();
-  }
-  griddep_wait();
-  fill_table<KIND, kBM>(table, args);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int tiles = num_tiles<KIND>(table, args);
-
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-      uint32_t s = 0, ph = 0;
-      int g = 0;
-      int armed[STAGES];
-      for (int i = 0; i < STAGES; ++i) armed[i] = -1;
-      // injected stall: no loads, so the MMA thread's first wait runs out
-      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const Tile t = tile_at<KIND, kBM, BN>(tile, g, table, args);
-        const int num_kb = (t.atoms + kAt - 1) / kAt;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bounded(empty_bar(s), ph ^ 1u, abort_flag, 0x10u)) {
-            ok = false;
-            break;
-          }
-          const int natoms = min(kAt, t.atoms - kb * kAt);
-          const int a_at = t.a_atom + kb * kAt, b_at = t.b_atom + kb * kAt;
-          const int rb_b = t.b_row >> 7;
-          const int nb = min(BN / 128, args.nrb_b - rb_b);
-          mbar_arrive_expect_tx(full_bar(s),
-                                L::kA + L::kB + (uint32_t)natoms * 512u * (1u + (uint32_t)nb));
-          armed[s] = (int)ph;
-          tma_load_2d(sbase + L::offA + s * L::kA, &tmA, full_bar(s), a_at * (kAtom / 2), t.a_row);
-          tma_load_2d(sbase + L::offB + s * L::kB, &tmB, full_bar(s), b_at * (kAtom / 2), t.b_row);
-          bulk_load(sbase + L::offSFA + s * L::kSFA,
-                    args.sfa + ((int64_t)(t.a_row >> 7) * args.kga + a_at) * 512, natoms * 512u,
-                    full_bar(s));
-          for (int j = 0; j < nb; ++j)
-            bulk_load(sbase + L::offSFB + s * L::kSFB + j * (kAt * 512),
-                      args.sfb + ((int64_t)(rb_b + j) * args.kgb + b_at) * 512, natoms * 512u,
-                      full_bar(s));
-          if (++s == STAGES) { s = 0; ph ^= 1u; }
-        }
-      }
-      if (!ok) {  // let the copies already issued land before the CTA exits
-        for (int i = 0; i < STAGES; ++i)
-          if (armed[i] >= 0) wait_drain(full_bar(i), (uint32_t)armed[i]);
-      }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------------- MMA
-      constexpr uint32_t idesc = idesc_nvf4(kBM, BN);
-      uint32_t s = 0, ph = 0, acc_ph = 0;
-      int g = 0;
-      bool ok = true, issued = false;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const Tile t = tile_at<KIND, kBM, BN>(tile, g, table, args);
-        if (t.atoms == 0) continue;
-        if (!wait_bounded(acc_empty, acc_ph ^ 1u, abort_flag, 0x20u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const int num_kb = (t.atoms + kAt - 1) / kAt;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bounded(full_bar(s), ph, abort_flag, 0x21u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const int natoms = min(kAt, t.atoms - kb * kAt);
-          const uint32_t sfa_t = tmem + L::kSfCol0 + s * L::kSfColsPerStage;
-          const uint32_t sfb_t = sfa_t + 16;
-          const uint32_t sa = sbase + L::offSFA + s * L::kSFA;
-          const uint32_t sb = sbase + L::offSFB + s * L::kSFB;
-          const uint32_t a0 = sbase + L::offA + s * L::kA;
-          const uint32_t b0 = sbase + L::offB + s * L::kB;
-          for (int j = 0; j < natoms; ++j) {
-            tc_cp_32x128b_warpx4(sfa_t + 4 * j, smem_desc_sf(sa + j * 512));
-#pragma unroll
-            for (int b = 0; b < BN / 128; ++b)
-              tc_cp_32x128b_warpx4(sfb_t + j * (BN / 32) + 4 * b,
-                                   smem_desc_sf(sb + b * (kAt * 512) + j * 512));
-            tc_mma_nvf4(tmem, smem_desc_sw128(a0 + 32 * j), smem_desc_sw128(b0 + 32 * j), idesc,
-                        sfa_t + 4 * j, sfb_t + j * (BN / 32), (kb | j) != 0 ? 1u : 0u);
-          }
-          issued = true;
-          tc_commit(empty_bar(s));
-          if (++s == STAGES) { s = 0; ph ^= 1u; }
-        }
-        if (!ok) break;
-        tc_commit(acc_full);
-        acc_ph ^= 1u;
-      }
-      if (!ok && issued) {  // MMAs in flight must finish before tensor memory is freed
-        tc_commit(drain_bar);
-        wait_drain(drain_bar, 0);
-      }
-    }
-  } else {
-    // -------------------------------------------------------------- epilogue
-    constexpr int kCols = BN / 2, kChunks = kCols / 32;
-    const int q = warp & 3, h = (warp - 2) >> 2;
-    const float alpha = __fmul_rn(__ldg(args.sdec_a), __ldg(args.sdec_b));
-    uint32_t acc_ph = 0;
-    int g = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      const Tile t = tile_at<KIND, kBM, BN>(tile, g, table, args);
-      const int64_t row = t.d_row + q * 32 + lane;
-      const bool live = q * 32 + lane < t.live;
-      uint32_t r[kChunks][32];
-      if (t.atoms > 0) {
-        if (!wait_bounded(acc_full, acc_ph, abort_flag, 0x30u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kCols + c * 32), r[c]);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-        acc_ph ^= 1u;
-      } else if (DMODE == NVFP4_D_F32_ACCUM) {
-        continue;  // nothing to add
-      } else {
-#pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[c][e] = 0u;
-      }
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c) {
-        const int col0 = t.d_col + h * kCols + c * 32;
-        if (col0 < args.N) store_cols<DMODE>(args, row, col0, r[c], alpha, live);
-      }
-    }
-    if (KIND == kRows && ok)
-      clear_tail(args, (int64_t)blockIdx.x * 256 + threadIdx.x - 64, (int64_t)gridDim.x * 256);
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-}
-
 // =============================================================================
 // CTA-pair kernel: tiles of 256 x BN (BN = 256 or 384) on a cluster of two SMs
-// (tcgen05 cta_group::2), for groups with many rows or long contractions.  As
-// gemm.cu's pair kernels: CTA r loads rows [128 r, 128 r + 128) of A's 256 and
+// (tcgen05 cta_group::2).  As gemm.cu's pair kernels: CTA r loads rows [128 r, 128 r + 128) of A's 256 and
 // its half of B's rows, four scale warps of each CTA store the stage's scales
 // into tensor memory, the leader issues the MMAs (a second MMA warp takes the
 // last 128 columns of a 384-wide tile), and 8 epilogue warps of each CTA drain
@@ -555,7 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
     tmem_relinquish_pair();
   }
   griddep_wait();
-  fill_table<KIND, 256>(table, args);
+  fill_table(table, args);
   tc_fence_before();
   __syncthreads();
   cluster_sync();
@@ -578,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
       // injected stall: no loads, so every consumer's first wait runs out
       bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
       for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
-        const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+        const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         const int num_kb = (t.atoms + kAt - 1) / kAt;
         const int a_row = t.a_row + (int)rank * 128;
         const int sfa_row = (a_row >> 7) * args.kga + t.a_atom;
@@ -628,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
       int g = 0;
       bool ok = true, issued = false;
       for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
-        const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+        const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         if (t.atoms == 0) continue;
         const int num_kb = (t.atoms + kAt - 1) / kAt;
         if (!wait_bounded_pair(acc_empty, acc_ph ^ 1u, abort_flag, peer_abort, 0x22u)) {
@@ -675,7 +409,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
     int g = 0;
     bool ok = true;
     for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
-      const int num_kb = (tile_at<KIND, 256, BN>(tile, g, table, args).atoms + kAt - 1) / kAt;
+      const int num_kb = (tile_at<KIND, BN>(tile, g, table, args).atoms + kAt - 1) / kAt;
       for (int kb = 0; kb < num_kb; ++kb, ++it) {
         if (!wait_bounded_pair(scf_bar(s), ph, abort_flag, peer_abort, 0x26u)) {
           ok = false;
@@ -739,7 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
     int g = 0;
     bool ok = true;
     for (int tile = pair; tile < tiles; tile += num_pairs) {
-      const Tile t = tile_at<KIND, 256, BN>(tile, g, table, args);
+      const Tile t = tile_at<KIND, BN>(tile, g, table, args);
       const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
       const bool mine = t.live > (int)rank * 128;
       const bool live = r0 + lane < t.live;
@@ -876,42 +610,35 @@ nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStre
                                 msb, md, a));
 }
 
-template <int KIND, int BN, int STAGES, int DMODE>
-nvfp4_status launch_group(const Operands& o, GroupArgs a, int sms, cudaStream_t stream) {
-  using L = GroupSmem<BN, STAGES>;
-  auto kern = group_gemm_kernel<KIND, BN, STAGES, DMODE>;
-  static GemmLaunchState ls;
-  if (gemm_setup(ls, kern, L::kAlloc, kThreads, 0, false, sms) <= 0) return NVFP4_ERR_CUDA;
-  a.num_m_blk = a.M / kBM;
-  a.num_n_blk = (a.N + BN - 1) / BN;
-  CUtensorMap ma, mb;
-  if (!make_code_map(&ma, o.a_codes, o.a_rows, o.a_cols / 2, kBM) ||
-      !make_code_map(&mb, o.b_codes, o.b_rows, o.b_cols / 2, BN))
-    return NVFP4_ERR_CUDA;
-  return cuda_status(launch_pdl(kern, sms, kThreads, L::kAlloc, stream, ma, mb, a));
-}
-
 template <int KIND, int DMODE>
 nvfp4_status launch_tile(int32_t tile, const Operands& o, const GroupArgs& a, int sms,
                          cudaStream_t stream) {
-  if (tile == NVFP4_TILE_PAIR_256X256)
-    return launch_group_pair<KIND, 256, DMODE>(o, a, sms, stream);
   if constexpr (DMODE != NVFP4_D_F32_ACCUM)
     if (tile == NVFP4_TILE_PAIR_256X384)
       return launch_group_pair<KIND, 384, DMODE>(o, a, sms, stream);
-  return launch_group<KIND, 256, 4, DMODE>(o, a, sms, stream);
+  return launch_group_pair<KIND, 256, DMODE>(o, a, sms, stream);
 }
 
-// The tile of a product whose groups have `per` rows (a contraction: elements)
-// on average.
-int32_t group_tile(int32_t tile, int kind, int64_t per, int64_t n, bool f32) {
-  if (tile != NVFP4_TILE_AUTO) return tile;
-  return f32 || per < 256 || n < 2048 ? NVFP4_TILE_PAIR_256X256 : NVFP4_TILE_PAIR_256X384;
+// The width of a product's tiles: the one whose rounds of tiles over the pairs
+// cost less.  The host knows the rows and the number of groups, not the sizes;
+// with the padding to 128 taken off, that gives about `m_blocks` blocks of 256
+// rows.  A 384-wide tile costs 1.2 256-wide ones where the tensor cores set the
+// pace (as in gemm.cu), 1.5, its bytes, where groups have too few rows for
+// that.  Measured (us, 256 and 384 wide): 16384 rows, 8 groups, 4096 x 14336:
+// 381, 321; 2 rows, 2 of 8 groups, the same weights: 23.0, 20.2; 2 rows,
+// 14336 x 4096: 30.5, 36.0; 6216 rows, 64 groups, 2048 x 1024: 29.6, 28.9.
+int32_t rows_tile(int64_t rows, int64_t groups, int64_t n, int pairs) {
+  const int64_t used = std::min(groups, rows / 128);
+  const int64_t per = std::max<int64_t>(1, rows / used - 64);
+  const int64_t m_blocks = used * ((per + 255) / 256);
+  const int64_t r256 = (m_blocks * ((n + 255) / 256) + pairs - 1) / pairs;
+  const int64_t r384 = (m_blocks * ((n + 383) / 384) + pairs - 1) / pairs;
+  return 10 * r256 <= (per >= 256 ? 12 : 15) * r384 ? NVFP4_TILE_PAIR_256X256
+                                                    : NVFP4_TILE_PAIR_256X384;
 }
 
 bool known_tile(int32_t tile, int32_t d_mode) {
-  return tile == NVFP4_TILE_AUTO || tile == NVFP4_TILE_128X256 ||
-         tile == NVFP4_TILE_PAIR_256X256 ||
+  return tile == NVFP4_TILE_AUTO || tile == NVFP4_TILE_PAIR_256X256 ||
          (tile == NVFP4_TILE_PAIR_256X384 && d_mode != NVFP4_D_F32_ACCUM);
 }
 
@@ -988,7 +715,7 @@ nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32
   a.b_row_step = b_view ? 0 : (int)N;
   a.b_atom_step = b_view ? (int)(K / kAtom) : 0;
   const Operands o = {A->codes, A->scales, b_codes, b_sf, rows, K, b_rows, b_cols, rows};
-  tile = group_tile(tile, kRows, rows / groups, N, false);
+  if (tile == NVFP4_TILE_AUTO) tile = rows_tile(rows, groups, N, dev.sm_count / 2);
   return d_mode == NVFP4_D_BF16
              ? launch_tile<kRows, NVFP4_D_BF16>(tile, o, a, dev.sm_count, stream)
              : launch_tile<kRows, NVFP4_D_BF16_ADD_C>(tile, o, a, dev.sm_count, stream);
@@ -1029,7 +756,9 @@ nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, cons
   a.kga = a.kgb = (int)(rows / kAtom);
   a.nrb_b = (int)(N / 128);
   const Operands o = {A->codes, A->scales, B->codes, B->scales, M, rows, N, rows, groups * M};
-  tile = group_tile(tile, kWgrad, rows / groups, N, d_mode == NVFP4_D_F32_ACCUM);
+  // weight gradients are bound by D: both widths take the same time (64 x [1024,
+  // 2048] over 32000 rows: 74 us), and the narrow one wastes less of odd widths
+  if (tile == NVFP4_TILE_AUTO) tile = NVFP4_TILE_PAIR_256X256;
   return d_mode == NVFP4_D_BF16
              ? launch_tile<kWgrad, NVFP4_D_BF16>(tile, o, a, dev.sm_count, stream)
              : launch_tile<kWgrad, NVFP4_D_F32_ACCUM>(tile, o, a, dev.sm_count, stream);
