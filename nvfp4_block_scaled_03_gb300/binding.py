@@ -856,7 +856,7 @@ def nvfp4_residual_norm_fwd(x: torch.Tensor, z: torch.Tensor | None = None,
     if h is not None:
         _cuda(h, _BF16, "h", x.shape)
     elif w_pre is not None:
-        h = torch.empty_like(x, dtype=_BF16)
+        h = torch.empty_like(x) if x.dtype is _BF16 else torch.empty_like(x, dtype=_BF16)
     st = lib.nvfp4_residual_norm_fwd(p, *ins, None if y is None else y.data_ptr(),
                                      None if h is None else h.data_ptr(), _current(x))
     if st:

@@ -6,17 +6,23 @@
 // Choice: the k largest logits of a row, the largest first, the lowest index
 // among equals; compared on the bit patterns (mapped so that unsigned order is
 // the floats' order), so the choice is exact.  -inf and NaN are never chosen.
-// One warp takes a token: lane l holds logits l, l + 32, ..; each of the k
-// rounds is a local maximum and two warp reductions (redux).
+// One warp takes a token, two at a time: lane l holds experts NI l .. NI l + NI
+// - 1; each of the k rounds is a local maximum and one warp reduction (redux).
+// A bf16 logit leaves 16 bits of its key for the index, so the reduction finds
+// both; for FP32 a ballot follows, whose first lane holds the lowest index.
+// The instructions of the rounds set the time (16384 tokens, 8 of 128 experts).
 //
 // Plan: expert e owns rows offsets[e] .. offsets[e] + sizes[e] - 1, in the
 // order of (token, slot), and the offsets are multiples of 128, the rows of a
-// scale atom.  Each CTA counts its tokens' choices per expert; the second
-// kernel sums the counts of the CTAs before it (at most one CTA per SM, so
-// this is a short read from L2) and ranks its own choices warp by warp.  No
-// atomic decides an order: the plan is the same every time.  Few tokens take
-// one CTA and one launch for both steps.
+// scale atom.  The first kernel clears `source` and counts each CTA's choices
+// per expert, the second turns the counts into running sums over the CTAs, the
+// third ranks each CTA's choices warp by warp.  (Two kernels, the last summing
+// the counts of the CTAs before it by itself, read 152 x experts counts in
+// every CTA: 4096 tokens of 512 experts took 43 us that way.)  No atomic
+// decides an order: the plan is the same every time.  Few tokens take one CTA
+// and one launch for all of it.
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -24,19 +30,21 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kWarps = 16;            // that rank a CTA's choices
 constexpr int kThreads = kWarps * 32;
+constexpr int kChooseWarps = 32;      // that make them
+constexpr int kChooseThreads = kChooseWarps * 32;
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 16;
 constexpr int kGroupAlign = 128;
-constexpr int kSmallTokens = 128;  // up to here one CTA does it all
+constexpr int kSmallTokens = 2 * kChooseWarps;  // up to here one CTA does it all
 
 struct RouteArgs {
   const void* logits;
   int64_t ld;
   int tokens, experts, top;
   int mode;
-  int per_cta, per_warp;  // tokens of a CTA, of a warp
+  int per_cta;  // tokens of a CTA
   int32_t* expert;
   float* weight;
   int32_t* sizes;
@@ -44,7 +52,8 @@ struct RouteArgs {
   int32_t* row;
   int32_t* source;
   int64_t rows;     // entries of source
-  int32_t* counts;  // [CTAs][experts]
+  int32_t* counts;  // [CTAs + 1][experts], after the second kernel running sums
+  int ctas;
   // backward
   const float* dweight;
   void* dlogits;
@@ -57,15 +66,15 @@ NVFP4_DEV float load_logit(const void* p, int64_t at) {
 }
 
 // Unsigned key in the order of the floats, 0 for what is never chosen; +-0 are
-// equal, and +inf counts as the largest finite value.
-NVFP4_DEV uint32_t logit_key(float& v) {
-  if (!(v > -INFINITY)) {
-    v = -INFINITY;
-    return 0u;
-  }
-  v = fminf(v, 3.402823466e38f) + 0.0f;
+// equal, and +inf counts as the type's largest finite value.  A bf16 logit's
+// key has its expert e in the low half, the lower the larger.
+template <bool WIDE>
+NVFP4_DEV uint32_t logit_key(float& v, int e) {
+  const bool none = !(v > -INFINITY);
+  v = none ? -INFINITY : fminf(v, WIDE ? 3.402823466e38f : 3.3895314e38f) + 0.0f;
   const uint32_t b = __float_as_uint(v);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return none ? 0u : WIDE ? k : (k & 0xFFFF0000u) | (0xFFFFu - (uint32_t)e);
 }
 
 NVFP4_DEV float warp_sum(float v) {
@@ -75,71 +84,119 @@ NVFP4_DEV float warp_sum(float v) {
 }
 
 // The logits of one token in a warp's registers: value and key of experts
-// lane + 32 i.
+// NI lane + i.
 template <int NI, bool WIDE>
 NVFP4_DEV void load_token(const RouteArgs& a, int64_t t, int lane, float (&v)[NI],
                           uint32_t (&key)[NI]) {
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    const int e = lane + 32 * i;
+    const int e = NI * lane + i;
     v[i] = e < a.experts ? load_logit<WIDE>(a.logits, t * a.ld + e) : -INFINITY;
-    key[i] = logit_key(v[i]);
+    key[i] = logit_key<WIDE>(v[i], e);
   }
 }
 
-// Step 1 for the tokens of this CTA: experts and weights to global memory,
-// the count of each expert to `hist` (shared).
-template <int NI, bool WIDE>
-NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) hist[e] = 0;
-  __syncthreads();
-  const int t0 = blockIdx.x * a.per_cta + warp * a.per_warp;
-  const int t1 = min(min(t0 + a.per_warp, (int)(blockIdx.x + 1) * a.per_cta), a.tokens);
-  for (int t = t0; t < t1; ++t) {
-    float v[NI];
-    uint32_t key[NI];
-    load_token<NI, WIDE>(a, t, lane, v, key);
-    float top_logit = 0.0f, my_logit = 0.0f, all = 0.0f;
-    int my_expert = -1;
-    for (int j = 0; j < a.top; ++j) {
-      uint32_t best = 0u;
-      int at = 0;
+template <bool WIDE>
+NVFP4_DEV float key_value(uint32_t k) {
+  const uint32_t b = (k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k;
+  return __uint_as_float(WIDE ? b : b & 0xFFFF0000u);
+}
+
+// The tokens of one of `warps` warps of this CTA: [first, last).
+NVFP4_DEV void warp_tokens(const RouteArgs& a, int warps, int& first, int& last) {
+  const int per = (a.per_cta + warps - 1) / warps, c0 = blockIdx.x * a.per_cta;
+  const int end = min(c0 + a.per_cta, a.tokens);
+  first = min(c0 + (int)(threadIdx.x >> 5) * per, end);
+  last = min(first + per, end);
+}
+
+// Experts and weights of B tokens from t on, one warp: to global memory, and
+// counted in `hist` (shared).
+template <int NI, bool WIDE, int B>
+NVFP4_DEV void choose_tokens(const RouteArgs& a, int t, int* hist) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[B][NI];
+  float v[B][NI], top_logit[B], my_logit[B], all[B];
+  int my_expert[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b)
+    load_token<NI, WIDE>(a, t + b, lane, v[b], key[b]);
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    uint32_t best = key[b][0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) best = max(best, key[b][i]);
+    top_logit[b] = key_value<WIDE>(max(__reduce_max_sync(0xFFFFFFFFu, best), 1u));
+    all[b] = my_logit[b] = 0.0f;
+    my_expert[b] = -1;
+    if (a.mode == NVFP4_ROUTE_ALL)
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (key[i] > best) best = key[i], at = i;
+        all[b] += key[b][i] ? expf(v[b][i] - top_logit[b]) : 0.0f;
+  }
+  for (int j = 0; j < a.top; ++j) {
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      uint32_t best = key[b][0];
+#pragma unroll
+      for (int i = 1; i < NI; ++i) best = max(best, key[b][i]);
+      // m is 0 where nothing is left to choose; then the slot stays empty
       const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-      if (m == 0u) break;  // nothing left to choose
-      const int e = __reduce_min_sync(0xFFFFFFFFu, best == m ? lane + 32 * at : kMaxExperts);
-      const float l = __uint_as_float((m & 0x80000000u) ? (m & 0x7FFFFFFFu) : ~m);
-      if (j == 0) {
-        top_logit = l;
+      int e;
+      if (WIDE) {
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < NI; ++i) all += expf(v[i] - l);  // -inf adds 0
+        for (int i = NI - 1; i >= 0; --i) at = key[b][i] == m ? i : at;
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+        e = NI * from + __shfl_sync(0xFFFFFFFFu, at, from);
+      } else {
+        e = 0xFFFF - (int)(m & 0xFFFFu);
       }
-      if (lane == j) my_expert = e, my_logit = l;
+      const bool slot = lane == j && m != 0u;
+      my_expert[b] = slot ? e : my_expert[b];
+      my_logit[b] = slot ? key_value<WIDE>(m) : my_logit[b];
 #pragma unroll
       for (int i = 0; i < NI; ++i)
-        if (e == lane + 32 * i) key[i] = 0u;
-    }
-    const float ex = my_expert >= 0 ? expf(my_logit - top_logit) : 0.0f;
-    const float total = warp_sum(a.mode == NVFP4_ROUTE_CHOSEN ? ex : all);
-    if (lane < a.top) {
-      const int64_t at = (int64_t)t * a.top + lane;
-      a.expert[at] = my_expert;
-      a.weight[at] = my_expert >= 0 ? ex / total : 0.0f;
-      if (my_expert >= 0) atomicAdd(&hist[my_expert], 1);
+        key[b][i] = (WIDE ? e - NI * lane == i : key[b][i] == m) ? 0u : key[b][i];
     }
   }
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const float ex = my_expert[b] >= 0 ? expf(my_logit[b] - top_logit[b]) : 0.0f;
+    const float total = warp_sum(a.mode == NVFP4_ROUTE_CHOSEN ? ex : all[b]);
+    if (lane < a.top) {
+      const int64_t at = (int64_t)(t + b) * a.top + lane;
+      a.expert[at] = my_expert[b];
+      a.weight[at] = my_expert[b] >= 0 ? ex / total : 0.0f;
+      if (my_expert[b] >= 0) atomicAdd(&hist[my_expert[b]], 1);
+    }
+  }
+}
+
+// Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
+template <int NI, bool WIDE>
+NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) hist[e] = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kChooseThreads + threadIdx.x; r < a.rows;
+       r += (int64_t)gridDim.x * kChooseThreads)
+    a.source[r] = -1;
+  __syncthreads();
+  int t, t1;
+  warp_tokens(a, kChooseWarps, t, t1);
+  if (NI <= 8)  // more would not leave registers for two tokens
+    for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
+  for (; t < t1; ++t) choose_tokens<NI, WIDE, 1>(a, t, hist);
   __syncthreads();
 }
 
 // Step 2: rows of this CTA's choices.  before[e]: choices of e in the CTAs
 // before this one; total[e]: in all.  Both in shared memory; base [kWarps]
-// [experts] is scratch.
+// [experts] is scratch.  The slots' experts are read twice (counted, then
+// placed): the second time from L1.  The first kWarps warps work.
 NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, int* offset,
                       int* base) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x < kThreads ? threadIdx.x : INT_MAX / 2;  // else beyond every loop
   // offsets: warp 0 scans the padded sizes, 32 experts at a time
   if (warp == 0) {
     int run = 0;
@@ -162,37 +219,39 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
       }
       run += __shfl_sync(0xFFFFFFFFu, s, 31);
     }
-    if (lane == 0) {
-      offset[a.experts] = run;
-      if (blockIdx.x == 0) a.offsets[a.experts] = run;
-    }
+    if (lane == 0 && blockIdx.x == 0) a.offsets[a.experts] = run;
   }
-  for (int i = threadIdx.x; i < kWarps * a.experts; i += kThreads) base[i] = 0;
+  for (int i = tid; i < kWarps * a.experts; i += kThreads) base[i] = 0;
   __syncthreads();
-  const int t0 = blockIdx.x * a.per_cta + warp * a.per_warp;
-  const int t1 = min(min(t0 + a.per_warp, (int)(blockIdx.x + 1) * a.per_cta), a.tokens);
+  int t0 = 0, t1 = 0;
+  if (warp < kWarps) warp_tokens(a, kWarps, t0, t1);
   int* mine = base + warp * a.experts;
-  const int64_t i0 = (int64_t)t0 * a.top, i1 = (int64_t)max(t1, t0) * a.top;
+  const int64_t i0 = (int64_t)t0 * a.top, i1 = (int64_t)t1 * a.top;
   for (int64_t i = i0 + lane; i < i1; i += 32) {
     const int e = a.expert[i];
     if (e >= 0) atomicAdd(&mine[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-    int run = offset[e] + before[e];
+  for (int e = tid; e < a.experts; e += kThreads) {
+    int n[kWarps], run = offset[e] + before[e];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n[w] = base[w * a.experts + e];
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const int n = base[w * a.experts + e];
       base[w * a.experts + e] = run;
-      run += n;
+      run += n[w];
     }
   }
   __syncthreads();
   // a token's experts differ, so its slots take their places side by side;
   // the warp's tokens follow one another
+  int next = -1;
+  if (lane < a.top && t0 < t1) next = a.expert[i0 + lane];
   for (int t = t0; t < t1; ++t) {
+    const int64_t i = (int64_t)t * a.top + lane;
+    const int e = next;
     if (lane < a.top) {
-      const int64_t i = (int64_t)t * a.top + lane;
-      const int e = a.expert[i];
+      if (t + 1 < t1) next = a.expert[i + a.top];
       int r = -1;
       if (e >= 0) {
         r = mine[e]++;
@@ -202,53 +261,78 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
     }
     __syncwarp();
   }
-  // rows that no choice takes: each expert's padding, and what is behind the last
-  for (int e = blockIdx.x; e < a.experts; e += gridDim.x)
-    for (int r = offset[e] + total[e] + (int)threadIdx.x; r < offset[e + 1]; r += kThreads)
-      if (r < a.rows) a.source[r] = -1;
-  for (int64_t r = (int64_t)offset[a.experts] + (int64_t)blockIdx.x * kThreads + threadIdx.x;
-       r < a.rows; r += (int64_t)gridDim.x * kThreads)
-    a.source[r] = -1;
 }
 
 template <int NI, bool WIDE>
-__global__ void __launch_bounds__(kThreads) route_choose_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
   griddep_wait();
   choose<NI, WIDE>(a, hist);
-  for (int e = threadIdx.x; e < a.experts; e += kThreads)
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads)
     a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
 struct AssignSmem {
-  int before[kMaxExperts], total[kMaxExperts], offset[kMaxExperts + 1];
+  int before[kMaxExperts], total[kMaxExperts], offset[kMaxExperts];
   int base[kWarps * kMaxExperts];
 };
+
+// counts [CTAs][experts] becomes its running sums over the CTAs, without the
+// CTA's own, and the totals behind them.  A CTA takes 32 experts (lanes), its
+// 32 warps up to five CTAs' counts each.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a) {
+  constexpr int kPer = (kMaxSms + 31) / 32;
+  __shared__ int part[32][33];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  int n[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = warp * kPer + i;
+    n[i] = e < a.experts && b < a.ctas ? a.counts[(int64_t)b * a.experts + e] : 0;
+    sum += n[i];
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  // warp w scans expert w of the 32 over the parts
+  int v = part[lane][warp];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += u;
+  }
+  __syncthreads();
+  part[lane][warp] = v;
+  __syncthreads();
+  int run = part[warp][lane] - sum;
+  if (e >= a.experts) return;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = warp * kPer + i;
+    if (b < a.ctas) a.counts[(int64_t)b * a.experts + e] = run;
+    run += n[i];
+  }
+  if (warp == 31) a.counts[(int64_t)a.ctas * a.experts + e] = run;
+}
 
 __global__ void __launch_bounds__(kThreads) route_assign_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
   for (int e = threadIdx.x; e < a.experts; e += kThreads) {
-    int before = 0, total = 0;
-#pragma unroll 8
-    for (int b = 0; b < (int)gridDim.x; ++b) {
-      const int n = a.counts[(int64_t)b * a.experts + e];
-      total += n;
-      if (b < (int)blockIdx.x) before += n;
-    }
-    s.before[e] = before;
-    s.total[e] = total;
+    s.before[e] = a.counts[(int64_t)blockIdx.x * a.experts + e];
+    s.total[e] = a.counts[(int64_t)a.ctas * a.experts + e];
   }
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);
 }
 
 template <int NI, bool WIDE>
-__global__ void __launch_bounds__(kThreads) route_small_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
   choose<NI, WIDE>(a, s.total);
-  for (int e = threadIdx.x; e < a.experts; e += kThreads) s.before[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) s.before[e] = 0;
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);
 }
@@ -257,10 +341,14 @@ __global__ void __launch_bounds__(kThreads) route_small_kernel(const RouteArgs a
 // over all experts the unchosen, whose weights have no gradient, add their
 // share of probability times dw_i, and themselves get -p sum_j w_j dw_j.  The
 // differences keep the result exact where one weight is near 1.
+// A token's row lies in shared memory: the lanes of its slots put theirs
+// into it.
 template <int NI, bool WIDE>
 __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) {
+  __shared__ float rows[kWarps][NI * 32];
   griddep_wait();
   const int lane = threadIdx.x & 31;
+  float* p = rows[threadIdx.x >> 5];
   const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= a.tokens) return;
   int e = -1;
@@ -274,67 +362,62 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) 
       e = -1;
     }
   }
-  float apart = 0.0f, mean = 0.0f;
-  for (int j = 0; j < a.top; ++j) {
-    const float wj = __shfl_sync(0xFFFFFFFFu, w, j), dj = __shfl_sync(0xFFFFFFFFu, dw, j);
-    apart += wj * (dw - dj);
-    mean += wj * dj;
-  }
-  float p[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) p[i] = 0.0f;
+  float apart = 0.0f;
+  for (int j = 0; j < a.top; ++j)
+    apart += __shfl_sync(0xFFFFFFFFu, w, j) * (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
+  float other = 0.0f;  // what an unchosen expert's probability is multiplied by
   if (a.mode == NVFP4_ROUTE_ALL) {
+    other = -warp_sum(w * dw);
+    float v[NI];
     uint32_t key[NI], best = 0u;
-    load_token<NI, WIDE>(a, t, lane, p, key);
+    load_token<NI, WIDE>(a, t, lane, v, key);
 #pragma unroll
     for (int i = 0; i < NI; ++i) best = max(best, key[i]);
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-    const float l = __uint_as_float((m & 0x80000000u) ? (m & 0x7FFFFFFFu) : ~m);
+    const float l = key_value<WIDE>(max(__reduce_max_sync(0xFFFFFFFFu, best), 1u));
     float all = 0.0f, rest = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      p[i] = key[i] ? expf(p[i] - l) : 0.0f;
-      all += p[i];
+      v[i] = key[i] ? expf(v[i] - l) : 0.0f;
+      p[NI * lane + i] = v[i];
+      all += v[i];
     }
     all = warp_sum(all);
     const float inv = all > 0.0f ? 1.0f / all : 0.0f;
-    for (int j = 0; j < a.top; ++j) {
-      const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (ej == lane + 32 * i) p[i] = 0.0f;
-    }
+    __syncwarp();
+    if (e >= 0) p[e] = 0.0f;
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      p[i] *= inv;
-      rest += p[i];
-      p[i] *= -mean;
+      v[i] = p[lane + 32 * i] * inv;
+      rest += v[i];
+      p[lane + 32 * i] = v[i] * other;
     }
     apart += warp_sum(rest) * dw;
-  }
-  const float mine = w * apart;
-  for (int j = 0; j < a.top; ++j) {
-    const int ej = __shfl_sync(0xFFFFFFFFu, e, j);
-    const float dj = __shfl_sync(0xFFFFFFFFu, mine, j);
+  } else {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (ej == lane + 32 * i) p[i] = dj;
+    for (int i = 0; i < NI; ++i) p[lane + 32 * i] = 0.0f;
   }
+  __syncwarp();
+  if (e >= 0) p[e] = w * apart;
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int c = lane + 32 * i;
     if (c < a.experts) {
       if (WIDE)
-        static_cast<float*>(a.dlogits)[t * a.experts + c] = p[i];
+        static_cast<float*>(a.dlogits)[t * a.experts + c] = p[c];
       else
-        static_cast<__nv_bfloat16*>(a.dlogits)[t * a.experts + c] = __float2bfloat16_rn(p[i]);
+        static_cast<__nv_bfloat16*>(a.dlogits)[t * a.experts + c] = __float2bfloat16_rn(p[c]);
     }
   }
 }
 
 // ---- rows to the experts and back ------------------------------------------------
-// A token (or row) is taken by `tpr` threads of a 256-thread CTA, a power of
-// two from 32 on, each 8 columns at a time.
+// A token is taken by `tpr` threads of a 256-thread CTA, a power of two from 32
+// on, each 8 columns at a time.  The kernels move rows whole and are bound by
+// memory; a token's rows (and weights) are looked up once and all its loads
+// are issued before the first is used.  The first CTAs of a grid clear the
+// padding rows, eight entries of `source` a warp.
 constexpr int kMoveThreads = 256;
 
 struct MoveArgs {
@@ -347,7 +430,7 @@ struct MoveArgs {
   float* dweight;
   int64_t tokens, rows;
   int cols, top, tpr;
-  unsigned token_ctas;  // CTAs behind these clear padding rows
+  unsigned clear_ctas;  // the first CTAs, which clear padding rows
 };
 
 NVFP4_DEV void unpack8(const uint4 u, float (&v)[8]) {
@@ -367,55 +450,77 @@ NVFP4_DEV uint4 pack8(const float (&v)[8]) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+NVFP4_DEV uint4 load8(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+NVFP4_DEV void store8(uint16_t* p, const uint4 v) { *reinterpret_cast<uint4*>(p) = v; }
 
 // The rows of `out` without a source become zero.
+constexpr int kClearRows = 8;  // of a warp
 NVFP4_DEV void clear_padding(const MoveArgs& a) {
-  const int per = kMoveThreads / a.tpr, sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
-  const int64_t r = (int64_t)(blockIdx.x - a.token_ctas) * per + sub;
-  if (r >= a.rows || a.source[r] >= 0) return;
-  for (int c = tid * 8; c < a.cols; c += a.tpr * 8)
-    *reinterpret_cast<uint4*>(a.out + r * a.cols + c) = make_uint4(0u, 0u, 0u, 0u);
-}
-
-// The row of slot j of token t, or -1 (none, or not a row of the tensor).
-NVFP4_DEV int64_t slot_row(const MoveArgs& a, int64_t t, int j) {
-  const int r = a.row[t * a.top + j];
-  return (uint32_t)r < (uint64_t)a.rows ? r : -1;
-}
-
-__global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const MoveArgs a) {
-  griddep_wait();
-  if (blockIdx.x >= a.token_ctas) return clear_padding(a);
-  const int per = kMoveThreads / a.tpr, sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
-  const int64_t t = (int64_t)blockIdx.x * per + sub;
-  if (t >= a.tokens) return;
-  for (int c = tid * 8; c < a.cols; c += a.tpr * 8) {
-    const uint4 v = *reinterpret_cast<const uint4*>(a.in + t * a.cols + c);
-    for (int j = 0; j < a.top; ++j) {
-      const int64_t r = slot_row(a, t, j);
-      if (r >= 0) *reinterpret_cast<uint4*>(a.out + r * a.cols + c) = v;
-    }
+  const int lane = threadIdx.x & 31;
+  const int64_t r0 =
+      ((int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * kClearRows;
+  const bool pad = lane < kClearRows && r0 + lane < a.rows && a.source[r0 + lane] < 0;
+  for (unsigned todo = __ballot_sync(0xFFFFFFFFu, pad); todo; todo &= todo - 1) {
+    uint16_t* row = a.out + (r0 + __ffs(todo) - 1) * a.cols;
+    for (int c = lane * 8; c < a.cols; c += 256) store8(row + c, make_uint4(0u, 0u, 0u, 0u));
   }
 }
 
+// The rows of token t's slots: -1 for none, or for what is not a row of the tensor.
+template <int TOP>
+NVFP4_DEV void slot_rows(const MoveArgs& a, int64_t t, bool live, int (&r)[TOP]) {
+#pragma unroll
+  for (int j = 0; j < TOP; ++j) {
+    r[j] = live && j < a.top ? a.row[t * a.top + j] : -1;
+    if ((uint32_t)r[j] >= (uint64_t)a.rows) r[j] = -1;
+  }
+}
+
+template <int TOP>
+__global__ void __launch_bounds__(kMoveThreads) dispatch_kernel(const MoveArgs a) {
+  griddep_wait();
+  if (blockIdx.x < a.clear_ctas) return clear_padding(a);
+  const int sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
+  const int64_t t = (int64_t)(blockIdx.x - a.clear_ctas) * (kMoveThreads / a.tpr) + sub;
+  if (t >= a.tokens) return;
+  int r[TOP];
+  slot_rows<TOP>(a, t, true, r);
+#pragma unroll 2
+  for (int c = tid * 8; c < a.cols; c += a.tpr * 8) {
+    const uint4 v = load8(a.in + t * a.cols + c);
+#pragma unroll
+    for (int j = 0; j < TOP; ++j)
+      if (r[j] >= 0) store8(a.out + (int64_t)r[j] * a.cols + c, v);
+  }
+}
+
+template <int TOP>
 __global__ void __launch_bounds__(kMoveThreads) combine_kernel(const MoveArgs a) {
   griddep_wait();
-  const int per = kMoveThreads / a.tpr, sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
-  const int64_t t = (int64_t)blockIdx.x * per + sub;
+  const int sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
+  const int64_t t = (int64_t)(blockIdx.x - a.clear_ctas) * (kMoveThreads / a.tpr) + sub;
   if (t >= a.tokens) return;
-  for (int c = tid * 8; c < a.cols; c += a.tpr * 8) {
-    float s[8] = {};
-#pragma unroll 4
-    for (int j = 0; j < a.top; ++j) {
-      const int64_t r = slot_row(a, t, j);
-      if (r < 0) continue;
-      const float w = a.weight ? a.weight[t * a.top + j] : 1.0f;
-      float v[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.in + r * a.cols + c), v);
+  int r[TOP];
+  float w[TOP];
+  slot_rows<TOP>(a, t, true, r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = fmaf(w, v[e], s[e]);
+  for (int j = 0; j < TOP; ++j) w[j] = a.weight && j < a.top ? a.weight[t * a.top + j] : 1.0f;
+#pragma unroll(TOP <= 4 ? 2 : 1)
+  for (int c = tid * 8; c < a.cols; c += a.tpr * 8) {
+    uint4 in[TOP];
+#pragma unroll
+    for (int j = 0; j < TOP; ++j)
+      if (r[j] >= 0) in[j] = load8(a.in + (int64_t)r[j] * a.cols + c);
+    float s[8] = {};
+#pragma unroll
+    for (int j = 0; j < TOP; ++j) {
+      if (r[j] < 0) continue;
+      float v[8];
+      unpack8(in[j], v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = fmaf(w[j], v[e], s[e]);
     }
-    *reinterpret_cast<uint4*>(a.out + t * a.cols + c) = pack8(s);
+    store8(a.out + t * a.cols + c, pack8(s));
   }
 }
 
@@ -425,29 +530,36 @@ template <int TOP>
 __global__ void __launch_bounds__(kMoveThreads) combine_bwd_kernel(const MoveArgs a) {
   __shared__ float red[kMoveThreads / 32][TOP];
   griddep_wait();
-  if (blockIdx.x >= a.token_ctas) return clear_padding(a);
-  const int per = kMoveThreads / a.tpr, sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
-  const int64_t t = (int64_t)blockIdx.x * per + sub;
+  if (blockIdx.x < a.clear_ctas) return clear_padding(a);
+  const int sub = threadIdx.x / a.tpr, tid = threadIdx.x % a.tpr;
+  const int64_t t = (int64_t)(blockIdx.x - a.clear_ctas) * (kMoveThreads / a.tpr) + sub;
   const bool live = t < a.tokens;
-  float dot[TOP] = {};
+  int r[TOP];
+  float w[TOP], dot[TOP] = {};
+  slot_rows<TOP>(a, t, live, r);
+#pragma unroll
+  for (int j = 0; j < TOP; ++j) w[j] = r[j] >= 0 ? a.weight[t * a.top + j] : 0.0f;
   if (live) {
+#pragma unroll(TOP <= 4 ? 2 : 1)
     for (int c = tid * 8; c < a.cols; c += a.tpr * 8) {
+      const uint4 dyv = load8(a.in + t * a.cols + c);
+      uint4 in[TOP];
+#pragma unroll
+      for (int j = 0; j < TOP; ++j)
+        if (r[j] >= 0) in[j] = load8(a.rows_in + (int64_t)r[j] * a.cols + c);
       float d[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.in + t * a.cols + c), d);
+      unpack8(dyv, d);
 #pragma unroll
       for (int j = 0; j < TOP; ++j) {
-        if (j >= a.top) break;
-        const int64_t r = slot_row(a, t, j);
-        if (r < 0) continue;
-        const float w = a.weight[t * a.top + j];
+        if (r[j] < 0) continue;
         float v[8];
-        unpack8(*reinterpret_cast<const uint4*>(a.rows_in + r * a.cols + c), v);
+        unpack8(in[j], v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           dot[j] = fmaf(d[e], v[e], dot[j]);
-          v[e] = w * d[e];
+          v[e] = w[j] * d[e];
         }
-        *reinterpret_cast<uint4*>(a.out + r * a.cols + c) = pack8(v);
+        store8(a.out + (int64_t)r[j] * a.cols + c, pack8(v));
       }
     }
   }
@@ -459,7 +571,7 @@ __global__ void __launch_bounds__(kMoveThreads) combine_bwd_kernel(const MoveArg
   __syncthreads();
   if (live && tid < a.top) {
     float s = 0.0f;
-    for (int w = 0; w < a.tpr / 32; ++w) s += red[sub * (a.tpr / 32) + w][tid];
+    for (int i = 0; i < a.tpr / 32; ++i) s += red[sub * (a.tpr / 32) + i][tid];
     a.dweight[t * a.top + tid] = s;  // 0 for a slot without a row
   }
 }
@@ -467,11 +579,11 @@ __global__ void __launch_bounds__(kMoveThreads) combine_bwd_kernel(const MoveArg
 bool a16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool a4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// CTAs of the two routing kernels: at most one per SM (the second reads every
-// CTA's counts), at least 16 tokens each.
+// CTAs of the routing kernels: at most one per SM, and where there are fewer
+// tokens than warps on the device, eight a CTA.
 int route_ctas(int64_t tokens, int sms) {
   if (tokens <= kSmallTokens) return 1;
-  return (int)std::min<int64_t>(std::min(sms, kMaxSms), (tokens + kWarps - 1) / kWarps);
+  return (int)std::min<int64_t>(std::min(sms, kMaxSms), (tokens + 7) / 8);
 }
 
 nvfp4_status check_route(int64_t tokens, int64_t experts, int32_t top) {
@@ -484,9 +596,11 @@ nvfp4_status check_route(int64_t tokens, int64_t experts, int32_t top) {
 
 template <int NI, bool WIDE>
 cudaError_t launch_route(RouteArgs& a, int ctas, cudaStream_t stream) {
-  if (ctas == 1) return launch_pdl(route_small_kernel<NI, WIDE>, 1, kThreads, 0, stream, a);
-  const cudaError_t e = launch_pdl(route_choose_kernel<NI, WIDE>, ctas, kThreads, 0, stream, a);
+  if (ctas == 1) return launch_pdl(route_small_kernel<NI, WIDE>, 1, kChooseThreads, 0, stream, a);
+  const cudaError_t e = launch_pdl(route_choose_kernel<NI, WIDE>, ctas, kChooseThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
+  const cudaError_t f = launch_pdl(route_scan_kernel, (a.experts + 31) / 32, 1024, 0, stream, a);
+  if (f != cudaSuccess) return f;
   return launch_pdl(route_assign_kernel, ctas, kThreads, 0, stream, a);
 }
 
@@ -512,12 +626,22 @@ nvfp4_status check_move(int64_t tokens, int64_t cols, int32_t top, int64_t rows)
   return NVFP4_OK;
 }
 
-// Threads per row: the power of two next to the row's vectors.
+// Threads per row: a power of two that leaves each about two vectors of 8.
 int move_tpr(int64_t cols) {
   int tpr = 32;
-  while (tpr < kMoveThreads && tpr * 8 < cols) tpr *= 2;
+  while (tpr < kMoveThreads && tpr * 16 < cols) tpr *= 2;
   return tpr;
 }
+
+// CTAs that look after the padding rows.
+unsigned clear_ctas(int64_t rows) {
+  constexpr int per = kMoveThreads / 32 * kClearRows;
+  return (unsigned)((rows + per - 1) / per);
+}
+
+// F<TOP> for the slots of a token.
+#define NVFP4_MOVE_KERNEL(F, top) \
+  ((top) <= 1 ? F<1> : (top) <= 2 ? F<2> : (top) <= 4 ? F<4> : (top) <= 8 ? F<8> : F<16>)
 
 }  // namespace
 
@@ -531,7 +655,7 @@ nvfp4_status route_sizes_impl(int64_t tokens, int64_t experts, int32_t top, int6
   const nvfp4_status st = check_route(tokens, experts, top);
   if (st != NVFP4_OK) return st;
   if (rows) *rows = route_rows(tokens, experts, top);
-  if (workspace_bytes) *workspace_bytes = (size_t)kMaxSms * experts * sizeof(int32_t);
+  if (workspace_bytes) *workspace_bytes = (size_t)(kMaxSms + 1) * experts * sizeof(int32_t);
   return NVFP4_OK;
 }
 
@@ -552,7 +676,7 @@ nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens
       !a4(sizes) || !a4(offsets) || !a4(row) || !a4(source))
     return NVFP4_ERR_ALIGN;
   if (!workspace || !a4(workspace) ||
-      workspace_bytes < (size_t)kMaxSms * experts * sizeof(int32_t))
+      workspace_bytes < (size_t)(kMaxSms + 1) * experts * sizeof(int32_t))
     return NVFP4_ERR_WORKSPACE;
   DeviceInfo dev;
   st = current_device(&dev);
@@ -574,8 +698,7 @@ nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens
   a.counts = static_cast<int32_t*>(workspace);
   int ctas = route_ctas(tokens, dev.sm_count);
   a.per_cta = (int)((tokens + ctas - 1) / ctas);
-  a.per_warp = (a.per_cta + kWarps - 1) / kWarps;
-  ctas = (int)((tokens + a.per_cta - 1) / a.per_cta);
+  ctas = a.ctas = (int)((tokens + a.per_cta - 1) / a.per_cta);
   return cuda_status(NVFP4_ROUTE_CALL(launch_route, experts, wide, a, ctas, stream));
 }
 
@@ -632,9 +755,10 @@ nvfp4_status dispatch_impl(const void* x, const int32_t* row, const int32_t* sou
   a.top = top;
   a.tpr = move_tpr(cols);
   const int per = kMoveThreads / a.tpr;
-  a.token_ctas = (unsigned)((tokens + per - 1) / per);
-  const unsigned grid = a.token_ctas + (unsigned)((rows + per - 1) / per);
-  return cuda_status(launch_pdl(dispatch_kernel, grid, kMoveThreads, 0, stream, a));
+  a.clear_ctas = clear_ctas(rows);
+  const unsigned token_ctas = (unsigned)((tokens + per - 1) / per);
+  return cuda_status(launch_pdl(NVFP4_MOVE_KERNEL(dispatch_kernel, top),
+                                a.clear_ctas + token_ctas, kMoveThreads, 0, stream, a));
 }
 
 nvfp4_status combine_impl(const void* o, const int32_t* row, const float* weight, int64_t tokens,
@@ -657,8 +781,8 @@ nvfp4_status combine_impl(const void* o, const int32_t* row, const float* weight
   a.top = top;
   a.tpr = move_tpr(cols);
   const int per = kMoveThreads / a.tpr;
-  a.token_ctas = (unsigned)((tokens + per - 1) / per);
-  return cuda_status(launch_pdl(combine_kernel, a.token_ctas, kMoveThreads, 0, stream, a));
+  return cuda_status(launch_pdl(NVFP4_MOVE_KERNEL(combine_kernel, top),
+                                (unsigned)((tokens + per - 1) / per), kMoveThreads, 0, stream, a));
 }
 
 nvfp4_status combine_bwd_impl(const void* dy, const void* o, const int32_t* row,
@@ -687,14 +811,10 @@ nvfp4_status combine_bwd_impl(const void* dy, const void* o, const int32_t* row,
   a.top = top;
   a.tpr = move_tpr(cols);
   const int per = kMoveThreads / a.tpr;
-  a.token_ctas = (unsigned)((tokens + per - 1) / per);
-  const unsigned grid = a.token_ctas + (unsigned)((rows + per - 1) / per);
-  auto kern = top <= 1   ? combine_bwd_kernel<1>
-              : top <= 2 ? combine_bwd_kernel<2>
-              : top <= 4 ? combine_bwd_kernel<4>
-              : top <= 8 ? combine_bwd_kernel<8>
-                         : combine_bwd_kernel<16>;
-  return cuda_status(launch_pdl(kern, grid, kMoveThreads, 0, stream, a));
+  a.clear_ctas = clear_ctas(rows);
+  const unsigned token_ctas = (unsigned)((tokens + per - 1) / per);
+  return cuda_status(launch_pdl(NVFP4_MOVE_KERNEL(combine_bwd_kernel, top),
+                                a.clear_ctas + token_ctas, kMoveThreads, 0, stream, a));
 }
 
 }  // namespace nvfp4
