@@ -1163,7 +1163,7 @@ nvfp4_status launch_pair(const CUtensorMap& ma, const CUtensorMap& mb, const CUt
   static GemmLaunchState ls;
   // persistent grid: as many pairs as are resident at once, at most one per tile
   const int max_pairs =
-      gemm_setup(ls, kern, L::kAlloc, R::kThreads, L::kST ? R::kSplitRegs : 0, true, sms);
+      gemm_setup(ls, kern, L::kAlloc, R::kThreads, L::kST ? R::kSplitRegs : 0, 2, sms);
   if (max_pairs <= 0) return NVFP4_ERR_CUDA;
   const int tiles = a.num_m_blk * a.num_n_blk;
   const int grid = 2 * std::min(tiles, max_pairs);
@@ -1181,7 +1181,7 @@ nvfp4_status launch_pair384(const CUtensorMap& ma, const CUtensorMap& mb, const 
   using L = Pair384Smem;
   auto kern = gemm_nvf4_pair384_kernel<DMODE>;
   static GemmLaunchState ls;
-  const int max_pairs = gemm_setup(ls, kern, L::kAlloc, L::kThreads, L::kSplitRegs, true, sms);
+  const int max_pairs = gemm_setup(ls, kern, L::kAlloc, L::kThreads, L::kSplitRegs, 2, sms);
   if (max_pairs <= 0) return NVFP4_ERR_CUDA;
   const int tiles = a.num_m_blk * a.num_n_blk;
   const int grid = 2 * std::min(tiles, max_pairs);
@@ -1197,7 +1197,7 @@ nvfp4_status launch(const CUtensorMap& ma, const CUtensorMap& mb, const GemmArgs
   using L = Smem<BN, STAGES, BKB>;
   auto kern = gemm_nvf4_kernel<BN, STAGES, DMODE, BKB>;
   static GemmLaunchState ls;
-  if (gemm_setup(ls, kern, L::kAlloc, kThreads, 0, false, sms) <= 0) return NVFP4_ERR_CUDA;
+  if (gemm_setup(ls, kern, L::kAlloc, kThreads, 0, 1, sms) <= 0) return NVFP4_ERR_CUDA;
   // persistent grid: one CTA per SM (tensor memory and shared memory admit
   // one), at most one per output tile
   const int units = a.num_m_blk * a.num_n_blk;

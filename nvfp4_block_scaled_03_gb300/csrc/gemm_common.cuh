@@ -181,9 +181,9 @@ inline bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64
 // with setmaxnreg the check that the compiled count covers the split
 // (setmaxnreg.inc waits until the registers it asks for are free in the
 // block's launch allotment, so a split above it would wait forever), and
-// for a CTA-pair kernel how many pairs are resident at once (cluster
-// placement can leave SMs of a GPC unpaired).  Returns the resident pairs
-// (1 for a single-SM kernel), 0 when the set-up failed.
+// for a kernel on clusters how many are resident at once (cluster placement
+// can leave SMs of a GPC over).  Returns the resident clusters (1 for a
+// single-SM kernel, `cluster` 1), 0 when the set-up failed.
 struct GemmLaunchState {
   std::mutex mu;
   int resident[64] = {};  // per device: 0 not yet set up, -1 refused for good
@@ -191,7 +191,7 @@ struct GemmLaunchState {
 
 template <typename K>
 int gemm_setup(GemmLaunchState& ls, K kern, uint32_t smem, int threads, int split_regs,
-               bool pair, int sms) {
+               int cluster, int sms) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(ls.mu);
@@ -208,20 +208,21 @@ int gemm_setup(GemmLaunchState& ls, K kern, uint32_t smem, int threads, int spli
       }
     }
     int n = 1;
-    if (pair) {
+    if (cluster > 1) {
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(2 * (sms / 2));
+      cfg.gridDim = dim3(cluster * (sms / cluster));
       cfg.blockDim = dim3(threads);
       cfg.dynamicSmemBytes = smem;
       cudaLaunchAttribute attr;
       attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = 2;
+      attr.val.clusterDim.x = cluster;
       attr.val.clusterDim.y = 1;
       attr.val.clusterDim.z = 1;
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0) n = sms / 2;
-      n = std::min(n, sms / 2);
+      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
+        n = sms / cluster;
+      n = std::min(n, sms / cluster);
     }
     ls.resident[dev] = n;
   }

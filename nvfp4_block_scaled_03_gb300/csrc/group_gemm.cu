@@ -155,6 +155,12 @@ NVFP4_DEV void clear_tail(const GroupArgs& a, int64_t i, int64_t n) {
 // the last tile of an M that is an odd multiple of 128, the second CTA stores
 // nothing.
 //
+// With SK > 1 a cluster holds SK pairs, which share a tile: pair i takes the
+// i-th part of the contraction, then the others hand their FP32 sums of the
+// rows that are the group's to pair 0 through its shared memory (the ring is
+// idle by then), which adds them in order and stores.  For a few tiles with
+// long contractions, which would leave most SMs idle.
+//
 // Outputs leave through shared-memory boxes of 32 rows x 32 columns and tensor
 // stores; the FP32 fold as tensor reductions (one FP32 add in L2 for each
 // element, subnormals flushed there), so D is never read into the SM.
@@ -194,6 +200,10 @@ struct PairGroup {
   static_assert(kSplitRegs <= kThreads * 128, "register split exceeds the launch's");
   static_assert(offStore % 1024 == 0, "store boxes start on their swizzle's period");
   static_assert(BN == 256 || (BN == 384 && !kF32), "tile");
+  // a part's sums in the ring of pair 0: rows padded by 16 bytes, so that the
+  // 16-byte pieces of 8 rows hit distinct banks
+  [[maybe_unused]] static constexpr uint32_t kPartRow = BN * 4 + 16;
+  [[maybe_unused]] static constexpr uint32_t kRing = kStages * (kA + kB);
 };
 
 // Tensor reduction (add) of a shared-memory box into global memory.
@@ -240,8 +250,15 @@ NVFP4_DEV void reduce_box(uint8_t* box, int lane, const float (&v)[32], const CU
   }
 }
 
-template <int KIND, int BN, int DMODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>::kThreads, 1)
+// 16 bytes into another CTA of the cluster.
+NVFP4_DEV void st_cluster_f4(uint32_t cluster_addr, const float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "f"(v.x),
+               "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+
+template <int KIND, int BN, int DMODE, int SK>
+__global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>::kThreads, 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB2,
@@ -265,11 +282,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
   GroupTable* table = reinterpret_cast<GroupTable*>(smem + L::offTable);
-  const uint32_t rank = cluster_ctarank();
+  // this CTA in its pair, and the pair's first CTA in the cluster
+  const uint32_t crank = cluster_ctarank(), rank = crank & 1u, first = crank & ~1u;
   const bool leader = rank == 0;
-  const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), rank ^ 1u);
+  const uint16_t both = (uint16_t)(3u << first);
+  const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), crank ^ 1u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  const int unit = blockIdx.x / (2 * SK), num_units = gridDim.x / (2 * SK);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -296,6 +315,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int tiles = num_tiles<KIND>(table, args);
+  // the pairs that share this cluster's tile (its only one then) and this
+  // pair's part of the contraction; otherwise pair 0 works alone
+  int parts = 1, part = 0;
+  if constexpr (SK > 1) {
+    part = (int)(crank >> 1);
+    if (unit < tiles && tiles <= num_units) {
+      int g = 0;
+      const Tile t = tile_at<KIND, BN>(unit, g, table, args);
+      const int rows = (min(t.live, 128) + 31) / 32 * 32;
+      parts = SK;
+      while (parts > 1 && ((parts - 1) * rows * L::kPartRow > L::kRing ||
+                           (t.atoms + kAt - 1) / kAt < 2 * parts))
+        parts /= 2;
+    }
+  }
+  const int tile0 = part < parts ? unit : tiles;
+  auto k_begin = [&](int num_kb) { return SK == 1 ? 0 : num_kb * part / parts; };
+  auto k_end = [&](int num_kb) { return SK == 1 ? num_kb : num_kb * (part + 1) / parts; };
 
   if (warp < 8) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsIssue));
@@ -311,18 +348,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
       int g = 0;
       // injected stall: no loads, so every consumer's first wait runs out
       bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
-      for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+      for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         const int num_kb = (t.atoms + kAt - 1) / kAt;
         const int a_row = t.a_row + (int)rank * 128;
         const int sfa_row = (a_row >> 7) * args.kga + t.a_atom;
         const int sfb_row = (t.b_row >> 7) * args.kgb + t.b_atom;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = k_begin(num_kb); kb < k_end(num_kb); ++kb) {
           if (!wait_bounded_pair(empty_bar(s), ph ^ 1u, abort_flag, peer_abort, 0x11u)) {
             ok = false;
             break;
           }
-          const uint32_t fb = mapa_shared(full_bar(s), 0);
+          const uint32_t fb = mapa_shared(full_bar(s), first);
           const int a_x = (t.a_atom + kb * kAt) * (kAtom / 2);
           const int b_x = (t.b_atom + kb * kAt) * (kAtom / 2);
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (L::kA + L::kB));
@@ -361,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
       uint32_t s = 0, ph = 0, acc_ph = 0, it = 0;
       int g = 0;
       bool ok = true, issued = false;
-      for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+      for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         if (t.atoms == 0) continue;
         const int num_kb = (t.atoms + kAt - 1) / kAt;
@@ -370,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
           break;
         }
         tc_fence_after();
-        for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        for (int kb = k_begin(num_kb); kb < k_end(num_kb); ++kb, ++it) {
           if (!wait_bounded_pair(full_bar(s), ph, abort_flag, peer_abort, 0x24u) ||
               !wait_bounded_pair(sf_bar(s), ph, abort_flag, peer_abort, 0x23u)) {
             ok = false;
@@ -384,17 +421,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
           for (int j = 0; j < nmma; ++j)
             tc_mma_pair_nvf4(d_tmem, smem_desc_sw128(a0 + 32 * j), smem_desc_sw128(b0 + 32 * j),
                              idesc, slot + L::kColA + 4 * j, slot + sfb_col + sfb_step * j,
-                             (kb | j) != 0 ? 1u : 0u);
+                             kb != k_begin(num_kb) || j != 0 ? 1u : 0u);
           issued = true;
-          tc_commit_pair(empty_bar(s), 3);
+          tc_commit_pair(empty_bar(s), both);
           if (++s == S) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        tc_commit_pair(acc_full, 3);
+        tc_commit_pair(acc_full, both);
         acc_ph ^= 1u;
       }
       if (!ok && issued) {
-        tc_commit_pair(my_drain, 1);
+        tc_commit_pair(my_drain, (uint16_t)(1u << first));
         wait_drain(my_drain, 0);
       }
     }
@@ -404,13 +441,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
     // line i of an atom (the scale words of rows i, i + 32, i + 64, i + 96) in
     // 4 columns.  A slot is rewritten once the MMAs that read it completed.
     const int q = warp & 3;
-    const uint32_t sf_leader = mapa_shared(sf_bar(0), 0);
+    const uint32_t sf_leader = mapa_shared(sf_bar(0), first);
     uint32_t s = 0, ph = 0, it = 0;
     int g = 0;
     bool ok = true;
-    for (int tile = pair; ok && tile < tiles; tile += num_pairs) {
+    for (int tile = tile0; ok && tile < tiles; tile += num_units) {
       const int num_kb = (tile_at<KIND, BN>(tile, g, table, args).atoms + kAt - 1) / kAt;
-      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+      for (int kb = k_begin(num_kb); kb < k_end(num_kb); ++kb, ++it) {
         if (!wait_bounded_pair(scf_bar(s), ph, abort_flag, peer_abort, 0x26u)) {
           ok = false;
           break;
@@ -459,20 +496,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
       }
     }
   }
+  if (SK > 1 && parts > 1) {  // the two barriers of the epilogue's exchange
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   } else {
     // -------------------------------------------------------------- epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsEpilogue));
     constexpr int kCols = BN / 2, kChunks = kCols / 32;
     const int ew = warp - 8;
     const int q = warp & 3, h = ew >> 2;
-    const uint32_t acc_empty_leader = mapa_shared(acc_empty, 0);
+    const uint32_t acc_empty_leader = mapa_shared(acc_empty, first);
     const float alpha = __fmul_rn(__ldg(args.sdec_a), __ldg(args.sdec_b));
     uint8_t* box = smem + L::offStore + ew * L::kBox;
     if (lane == 0) prefetch_tmap(&tmD);
+    // 32 columns of a row: times alpha, plus C, rounded; zero outside the group
+    auto finish = [&](float (&f)[32], int64_t row, int col, bool live, uint32_t (&pk)[16]) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) f[e] = __fmul_rn(f[e], alpha);
+      if (DMODE == NVFP4_D_BF16_ADD_C && live && col < args.N) {
+        const uint4* cp = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(args.C) + row * args.N + col);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint4 u = cp[p];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[8 * p + 2 * e] = __fadd_rn(f[8 * p + 2 * e], __uint_as_float(w[e] << 16));
+            f[8 * p + 2 * e + 1] =
+                __fadd_rn(f[8 * p + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u));
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = live ? pack_bf16x2(f[2 * e], f[2 * e + 1]) : 0u;
+    };
     uint32_t acc_ph = 0;
     int g = 0;
     bool ok = true;
-    for (int tile = pair; tile < tiles; tile += num_pairs) {
+    for (int tile = tile0; tile < tiles; tile += num_units) {
       const Tile t = tile_at<KIND, BN>(tile, g, table, args);
       const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
       const bool mine = t.live > (int)rank * 128;
@@ -503,6 +567,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
           for (int e = 0; e < 32; ++e) v[e] = __fmul_rn(__uint_as_float(r[c][e]), alpha);
           if (x0 + c * 32 < args.N) reduce_box(box, lane, v, &tmD, x0 + c * 32, y);
         }
+      } else if (SK > 1 && parts > 1) {
+        // every pair's MMAs are done behind the first barrier, and pair 0's ring
+        // with them; the sums have arrived behind the second
+        if (!wait_bounded_pair(acc_full, acc_ph, abort_flag, peer_abort, 0x33u)) ok = false;
+        tc_fence_after();
+        __syncwarp();
+        cluster_sync();
+        const int rows = (min(max(t.live - (int)rank * 128, 0), 128) + 31) / 32 * 32;
+        const uint32_t line = (uint32_t)(q * 32 + lane) * L::kPartRow + (uint32_t)(h * kCols) * 4;
+        const uint32_t tm = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kCols);
+        if (part > 0 && q * 32 < rows) {
+          const uint32_t to =
+              mapa_shared(sbase + (uint32_t)((part - 1) * rows) * L::kPartRow + line, rank);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tm + (uint32_t)(c * 32), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              st_cluster_f4(to + (uint32_t)(c * 128 + p * 16),
+                            make_float4(__uint_as_float(r[4 * p]), __uint_as_float(r[4 * p + 1]),
+                                        __uint_as_float(r[4 * p + 2]),
+                                        __uint_as_float(r[4 * p + 3])));
+          }
+        }
+        cluster_sync();
+        if (part == 0 && mine) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t r[32];
+            tmem_ld32(tm + (uint32_t)(c * 32), r);
+            tmem_ld_wait();
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+            if (q * 32 < rows)
+              for (int i = 0; i < parts - 1; ++i) {
+                const float4* v = reinterpret_cast<const float4*>(
+                    smem + (uint32_t)(i * rows) * L::kPartRow + line + (uint32_t)(c * 128));
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                  const float4 u = v[p];
+                  f[4 * p] += u.x;
+                  f[4 * p + 1] += u.y;
+                  f[4 * p + 2] += u.z;
+                  f[4 * p + 3] += u.w;
+                }
+              }
+            uint32_t pk[16];
+            finish(f, t.d_row + r0 + lane, x0 + c * 32, live, pk);
+            if (x0 + c * 32 < args.N) store_box(box, lane, pk, &tmD, x0 + c * 32, y);
+          }
+        }
+        break;  // the cluster's only tile
       } else {
         uint32_t pk[kChunks][16];
         if (t.atoms > 0) {
@@ -518,25 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
             tmem_ld_wait();
             float f[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = __fmul_rn(__uint_as_float(r[e]), alpha);
-            if (DMODE == NVFP4_D_BF16_ADD_C && live && x0 + c * 32 < args.N) {
-              const uint4* cp = reinterpret_cast<const uint4*>(
-                  static_cast<const __nv_bfloat16*>(args.C) + (t.d_row + r0 + lane) * args.N + x0 +
-                  c * 32);
-#pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                const uint4 u = cp[p];
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  f[8 * p + 2 * e] = __fadd_rn(f[8 * p + 2 * e], __uint_as_float(w[e] << 16));
-                  f[8 * p + 2 * e + 1] =
-                      __fadd_rn(f[8 * p + 2 * e + 1], __uint_as_float(w[e] & 0xFFFF0000u));
-                }
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) pk[c][e] = live ? pack_bf16x2(f[2 * e], f[2 * e + 1]) : 0u;
+            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
+            finish(f, t.d_row + r0 + lane, x0 + c * 32, live, pk[c]);
           }
           tc_fence_before();
           __syncwarp();
@@ -553,6 +655,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>
         for (int c = 0; c < kChunks; ++c)
           if (x0 + c * 32 < args.N) store_box(box, lane, pk[c], &tmD, x0 + c * 32, y);
       }
+    }
+    if (SK > 1 && part >= parts && parts > 1) {  // a pair without a part of the tile
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
     }
     if (KIND == kRows && ok)
       clear_tail(args, (int64_t)blockIdx.x * 256 + threadIdx.x - 256, (int64_t)gridDim.x * 256);
@@ -589,13 +696,21 @@ struct Operands {
   int64_t a_rows, a_cols, b_rows, b_cols, d_rows;
 };
 
-template <int KIND, int BN, int DMODE>
+// Clusters of a kernel that are resident at once; 0 when its set-up failed.
+template <int KIND, int BN, int DMODE, int SK>
+int group_units(int sms) {
+  using L = PairGroup<BN, DMODE>;
+  static GemmLaunchState ls;
+  return gemm_setup(ls, group_pair_kernel<KIND, BN, DMODE, SK>, L::kAlloc, L::kThreads,
+                    L::kSplitRegs, 2 * SK, sms);
+}
+
+template <int KIND, int BN, int DMODE, int SK>
 nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStream_t stream) {
   using L = PairGroup<BN, DMODE>;
-  auto kern = group_pair_kernel<KIND, BN, DMODE>;
-  static GemmLaunchState ls;
-  const int pairs = gemm_setup(ls, kern, L::kAlloc, L::kThreads, L::kSplitRegs, true, sms);
-  if (pairs <= 0) return NVFP4_ERR_CUDA;
+  auto kern = group_pair_kernel<KIND, BN, DMODE, SK>;
+  const int units = group_units<KIND, BN, DMODE, SK>(sms);
+  if (units <= 0) return NVFP4_ERR_CUDA;
   a.num_m_blk = (a.M + 255) / 256;
   a.num_n_blk = (a.N + BN - 1) / BN;
   CUtensorMap ma, mb, mb2, msa, msb, md;
@@ -606,17 +721,8 @@ nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStre
       !make_sf_map(&msb, o.b_sf, swizzled_scale_bytes(o.b_rows, o.b_cols)) ||
       !make_box_map(&md, a.D, o.d_rows, a.N, L::kF32))
     return NVFP4_ERR_CUDA;
-  return cuda_status(launch_pdl(kern, 2 * pairs, L::kThreads, L::kAlloc, stream, ma, mb, mb2, msa,
+  return cuda_status(launch_pdl(kern, 2 * SK * units, L::kThreads, L::kAlloc, stream, ma, mb, mb2, msa,
                                 msb, md, a));
-}
-
-template <int KIND, int DMODE>
-nvfp4_status launch_tile(int32_t tile, const Operands& o, const GroupArgs& a, int sms,
-                         cudaStream_t stream) {
-  if constexpr (DMODE != NVFP4_D_F32_ACCUM)
-    if (tile == NVFP4_TILE_PAIR_256X384)
-      return launch_group_pair<KIND, 384, DMODE>(o, a, sms, stream);
-  return launch_group_pair<KIND, 256, DMODE>(o, a, sms, stream);
 }
 
 // The width of a product's tiles: the one whose rounds of tiles over the pairs
@@ -635,6 +741,32 @@ int32_t rows_tile(int64_t rows, int64_t groups, int64_t n, int pairs) {
   const int64_t r384 = (m_blocks * ((n + 383) / 384) + pairs - 1) / pairs;
   return 10 * r256 <= (per >= 256 ? 12 : 15) * r384 ? NVFP4_TILE_PAIR_256X256
                                                     : NVFP4_TILE_PAIR_256X384;
+}
+
+// A contraction from here on is shared by pairs where tiles are few.  Measured
+// (us, one pair a tile and shared): 2 rows x 14336 x 4096: 29.6, 22.0; 1 row x
+// 8192 x 1024: 18.5, 14.1; 2 rows x 4096 x 2048: 12.3, 11.9; 8 rows x 2048 x
+// 1024: 11.1, 13.6.
+constexpr int kSharedK = 4096;
+
+template <int KIND, int DMODE>
+nvfp4_status launch_tile(int32_t tile, const Operands& o, const GroupArgs& a, int sms,
+                         cudaStream_t stream) {
+  if constexpr (KIND == kRows) {
+    if (tile == NVFP4_TILE_AUTO) {
+      // the most tiles there can be, each with a cluster of its own
+      const int64_t tiles = (int64_t)a.rows / 128 * ((a.N + 255) / 256);
+      if (a.K >= kSharedK && tiles <= group_units<KIND, 256, DMODE, 4>(sms))
+        return launch_group_pair<KIND, 256, DMODE, 4>(o, a, sms, stream);
+      if (a.K >= kSharedK && tiles <= group_units<KIND, 256, DMODE, 2>(sms))
+        return launch_group_pair<KIND, 256, DMODE, 2>(o, a, sms, stream);
+      tile = rows_tile(a.rows, a.groups, a.N, sms / 2);
+    }
+  }
+  if constexpr (DMODE != NVFP4_D_F32_ACCUM)
+    if (tile == NVFP4_TILE_PAIR_256X384)
+      return launch_group_pair<KIND, 384, DMODE, 1>(o, a, sms, stream);
+  return launch_group_pair<KIND, 256, DMODE, 1>(o, a, sms, stream);
 }
 
 bool known_tile(int32_t tile, int32_t d_mode) {
@@ -715,7 +847,6 @@ nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32
   a.b_row_step = b_view ? 0 : (int)N;
   a.b_atom_step = b_view ? (int)(K / kAtom) : 0;
   const Operands o = {A->codes, A->scales, b_codes, b_sf, rows, K, b_rows, b_cols, rows};
-  if (tile == NVFP4_TILE_AUTO) tile = rows_tile(rows, groups, N, dev.sm_count / 2);
   return d_mode == NVFP4_D_BF16
              ? launch_tile<kRows, NVFP4_D_BF16>(tile, o, a, dev.sm_count, stream)
              : launch_tile<kRows, NVFP4_D_BF16_ADD_C>(tile, o, a, dev.sm_count, stream);

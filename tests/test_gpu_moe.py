@@ -299,6 +299,43 @@ def test_group_gemm(nv, sizes, N, K, view, spare, tile):
     nv.check_device_errors()
 
 
+@pytest.mark.parametrize("sizes", [[1], [0, 2], [1, 0, 1], [40], [33, 1], [128], [0], [129], [250]],
+                         ids=str)
+@pytest.mark.parametrize("N,K", [(128, 2048), (384, 2112), (1024, 4096), (1280, 14336), (2048, 4160)])
+@pytest.mark.parametrize("view", [0, 1])
+def test_group_gemm_of_few_tiles(nv, sizes, N, K, view):
+    """Few tiles with a long contraction: pairs of a cluster share a tile (two or
+    four, by the tiles there can be), and hand over the rows of the group."""
+    import torch
+    E = len(sizes)
+    s, o, off = _groups(sizes)
+    rows = max(128, int(off[-1]))
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    A = nv.nvfp4_quantize(torch.randn(rows, K, generator=g, device="cuda").bfloat16(), nv.ROW_1X16)
+    shape = (E * K, N) if view else (E * N, K)
+    B = nv.nvfp4_quantize(torch.randn(*shape, generator=g, device="cuda") * 0.05, nv.BLOCK_16X16,
+                          nv.EMIT_T)
+    C = torch.randn(rows, N, generator=g, device="cuda").bfloat16()
+    a = _decode(A, rows, K)
+    b = _decode(B, N, E * K, 1) if view else _decode(B, E * N, K)
+    out = torch.full((rows, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_group_gemm(A, B, s, o, b_view=view, out=out)
+    again = nv.nvfp4_group_gemm(A, B, s, o, b_view=view)
+    plus = nv.nvfp4_group_gemm(A, B, s, o, b_view=view, C_add=C, d_mode=nv.D_BF16_ADD_C)
+    assert torch.equal(out, again)
+    live = np.zeros(rows, dtype=bool)
+    for e, n in enumerate(sizes):
+        r = slice(off[e], off[e] + n)
+        live[r] = True
+        if n:
+            ref = a[r] @ (b[:, e * K:(e + 1) * K] if view else b[e * N:(e + 1) * N]).T
+            H.assert_gemm_close(_f64(out)[r], ref, f"group {e}")
+            H.assert_gemm_close(_f64(plus)[r], ref + _f64(C)[r], f"group {e} + C",
+                                rms=np.sqrt(np.mean(ref ** 2)))
+    assert (_f64(out)[~live] == 0).all() and (_f64(plus)[~live] == 0).all()
+    nv.check_device_errors()
+
+
 @pytest.mark.parametrize("sizes", GROUP_SIZES, ids=str)
 @pytest.mark.parametrize("M,N", [(128, 128), (384, 256), (256, 640)])
 @pytest.mark.parametrize("spare,tile", [(0, 0), (256, 3), (0, 6)])
@@ -381,6 +418,53 @@ def test_group_wait_expires_then_recovers(nv, tile):
         nv.debug_inject(0, 0)
     nv.check_device_errors()
     assert torch.equal(nv.nvfp4_group_gemm(A, B, s, o, tile=tile), want)
+    nv.check_device_errors()
+
+
+def test_shared_tile_wait_expires_then_recovers(nv):
+    """The same with pairs that share a tile: all of them give up and meet at
+    their barriers."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = nv.nvfp4_quantize(torch.randn(128, 4096, generator=g, device="cuda"), nv.ROW_1X16)
+    B = nv.nvfp4_quantize(torch.randn(1024, 4096, generator=g, device="cuda"), nv.BLOCK_16X16)
+    s, o, _ = _groups([3])
+    want = nv.nvfp4_group_gemm(A, B, s, o)
+    nv.check_device_errors()
+    nv.debug_inject(nv.STALL_GEMM, 1_000_000)
+    try:
+        nv.nvfp4_group_gemm(A, B, s, o)
+        with pytest.raises(nv.NVFP4Error) as e:
+            nv.check_device_errors()
+        assert e.value.status == nv.ERR_DEVICE_TIMEOUT
+    finally:
+        nv.debug_inject(0, 0)
+    nv.check_device_errors()
+    assert torch.equal(nv.nvfp4_group_gemm(A, B, s, o), want)
+    nv.check_device_errors()
+
+
+def test_norm_wait_expires_then_recovers(nv):
+    """The norms' ring of rows: injected, no row arrives; the error word says so
+    and the next call is whole."""
+    import torch
+    t = {k: v.cuda() for k, v in _norm_case(40, 512, False, "channel", 4).items()}
+    args = (t["x"], t["z"], t["w_post"], t["gate"], t["w_pre"])
+    calls = (lambda: nv.nvfp4_residual_norm_fwd(*args),
+             lambda: nv.nvfp4_residual_norm_bwd(t["dy"], t["dh"], *args))
+    for call in calls:
+        want = call()
+        nv.check_device_errors()
+        nv.debug_inject(nv.STALL_QUANTIZE, 1_000_000)
+        try:
+            call()
+            with pytest.raises(nv.NVFP4Error) as e:
+                nv.check_device_errors()
+            assert e.value.status == nv.ERR_DEVICE_TIMEOUT
+        finally:
+            nv.debug_inject(0, 0)
+        nv.check_device_errors()
+        assert all(torch.equal(u, v) for u, v in zip(call(), want))
     nv.check_device_errors()
 
 
