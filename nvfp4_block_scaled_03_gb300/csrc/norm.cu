@@ -20,12 +20,19 @@
 // + 2 (z, h) or 3 + 3 streams and are bound by memory, with the arithmetic
 // (about 12 and 25 instructions an element pair) not far behind.
 //
-// A persistent CTA takes `rpc` rows at a time (one from 4096 columns on, whole
+// A persistent CTA takes `rpc` rows at a time (one from 4097 columns on, whole
 // warps per row), its weights in registers.  Rows arrive by bulk copies in a
 // ring of shared-memory stages, so loads run ahead while a row is reduced; a
 // row is read from its stage once per pass instead of being held in
-// registers, which leaves those to the weights and the column sums.  Rows too
-// long for two stages are read from global memory in each pass.
+// registers, which leaves those to the weights and the column sums.  Long rows
+// (the backward from 8200 columns on, the forward from 16392) are read from
+// global memory in each pass.
+//
+// Measured (us, and the time their bytes take at the copy rate): 16384 x 4096
+// bf16 forward 85 (80), backward 149 (120); FP32 stream, 8191 x 4096 forward
+// 69 (60), backward 100 (90); 16 x 4096 forward 3.4, launch included.  The bf16
+// backward is bound by its arithmetic (0.58 of the issue slots, 16 warps an SM:
+// its column sums and weights fill the registers).
 //
 // The column sums go to per-CTA partials that a second kernel adds in a fixed
 // order: no atomics, so results repeat bit for bit.
@@ -333,6 +340,56 @@ NVFP4_DEV void refill(const NormArgs& p, Ring& ring, uint32_t smem, const Walk& 
                            at.stage == 0 ? p.stages - 1 : at.stage - 1);
 }
 
+// Where a thread's weights are: in registers up to 8192 columns; beyond, in
+// shared memory (w_post with a channel gate in it, then w_pre) where the ring
+// does not need it -- the backward, whose rows are too long for two stages --
+// else in global memory.  Measured, 4096 x 16384 bf16: forward 117 us with the
+// ring, 187 with shared weights instead; backward 249 us with global weights,
+// 229 with shared ones.
+enum { kInRegs, kInSmem, kInGlobal };
+template <int VPT, bool RING>
+struct WeightsAt {
+  static constexpr int value = VPT <= kRegVpt ? kInRegs : VPT < kMaxVpt && !RING ? kInSmem : kInGlobal;
+};
+template <int VPT, bool RING>
+struct Weights {
+  static constexpr int kAt = WeightsAt<VPT, RING>::value;
+  F8 post[kAt == kInRegs ? VPT : 1], pre[kAt == kInRegs ? VPT : 1];
+  const float* smem;
+
+  NVFP4_DEV Weights(const NormArgs& p, uint8_t* sm, int tid, int tpr, bool has_post, bool has_pre) {
+    smem = reinterpret_cast<const float*>(sm);
+    if constexpr (kAt == kInRegs) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * tpr + tid) * kVec;
+        post[i] = has_post && c < p.cols ? post_weight(p, c) : zero8();
+        pre[i] = has_pre && c < p.cols ? load_f32(p.w_pre + c) : zero8();
+      }
+    } else if constexpr (kAt == kInSmem) {  // one row a CTA: a thread reads what it wrote
+      float* w = reinterpret_cast<float*>(sm);
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int c = (i * tpr + tid) * kVec;
+        if (c < p.cols) {
+          if (has_post) store_f32(w + c, post_weight(p, c));
+          if (has_pre) store_f32(w + p.cols + c, load_f32(p.w_pre + c));
+        }
+      }
+    }
+  }
+  NVFP4_DEV F8 get_post(const NormArgs& p, int i, int c) const {
+    if constexpr (kAt == kInRegs) return post[i];
+    if constexpr (kAt == kInSmem) return load_f32(smem + c);
+    return post_weight(p, c);
+  }
+  NVFP4_DEV F8 get_pre(const NormArgs& p, int i, int c) const {
+    if constexpr (kAt == kInRegs) return pre[i];
+    if constexpr (kAt == kInSmem) return load_f32(smem + p.cols + c);
+    return load_f32(p.w_pre + c);
+  }
+};
+
 template <int VPT, bool WIDE, bool RING, int PARTS>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -346,16 +403,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p)
     start_ring<WIDE, false>(p, ring, smem_u32(smem));
   else
     griddep_wait();
-  constexpr bool kKeep = VPT <= kRegVpt;  // weights in registers
-  F8 w_post[kKeep ? VPT : 1], w_pre[kKeep ? VPT : 1];
-  if (kKeep) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int c = (i * tpr + tid) * kVec;
-      w_post[i] = post && c < p.cols ? post_weight(p, c) : zero8();
-      w_pre[i] = pre && c < p.cols ? load_f32(p.w_pre + c) : zero8();
-    }
-  }
+  const Weights<VPT, RING> weights(p, smem, tid, tpr, post, pre);
   int turn = 0;
   for (Walk at(p); at.row0 < p.rows; at.next(p)) {
     const int64_t row = at.row0 + sub, at0 = row * p.cols;
@@ -393,7 +441,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p)
         for (int e = 0; e < kPairs; ++e) y[i].v[e] = __fmul2_rn(y[i].v[e], both(p.a));
         if (post) {
           const F8 z = load_bf16(in.z + c);
-          const F8 w = kKeep ? w_post[kKeep ? i : 0] : post_weight(p, c);
+          const F8 w = weights.get_post(p, i, c);
 #pragma unroll
           for (int e = 0; e < kPairs; ++e)
             y[i].v[e] = __ffma2_rn(both(k), __fmul2_rn(z.v[e], w.v[e]), y[i].v[e]);
@@ -412,7 +460,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p)
       for (int i = 0; i < VPT; ++i) {
         const int c = (i * tpr + tid) * kVec;
         if (live && c < p.cols) {
-          const F8 w = kKeep ? w_pre[kKeep ? i : 0] : load_f32(p.w_pre + c);
+          const F8 w = weights.get_pre(p, i, c);
           F8 h;
 #pragma unroll
           for (int e = 0; e < kPairs; ++e)
@@ -437,18 +485,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs p)
     start_ring<WIDE, true>(p, ring, smem_u32(smem));
   else
     griddep_wait();
-  constexpr bool kKeep = VPT <= kRegVpt;
-  F8 w_post[kKeep ? VPT : 1], w_pre[kKeep ? VPT : 1];
+  const Weights<VPT, RING> weights(p, smem, tid, tpr, post, pre);
   F8 acc_post[VPT], acc_pre[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int c = (i * tpr + tid) * kVec;
-    if (kKeep) {
-      w_post[kKeep ? i : 0] = post && c < p.cols ? post_weight(p, c) : zero8();
-      w_pre[kKeep ? i : 0] = pre && c < p.cols ? load_f32(p.w_pre + c) : zero8();
-    }
-    acc_post[i] = acc_pre[i] = zero8();
-  }
+  for (int i = 0; i < VPT; ++i) acc_post[i] = acc_pre[i] = zero8();
   int turn = 0;
   for (Walk at(p); at.row0 < p.rows; at.next(p)) {
     const int64_t row = at.row0 + sub, at0 = row * p.cols;
@@ -488,7 +528,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs p)
       for (int e = 0; e < kPairs; ++e) v.y.v[e] = __fmul2_rn(v.y.v[e], both(p.a));
       if (post) {
         v.z = load_bf16(in.z + c);
-        v.w = kKeep ? w_post[kKeep ? i : 0] : post_weight(p, c);
+        v.w = weights.get_post(p, i, c);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) {
           v.zc.v[e] = __fmul2_rn(v.z.v[e], v.w.v[e]);
@@ -497,7 +537,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs p)
       }
       if (pre) {
         v.dh = load_bf16(in.dh + c);
-        const F8 w = kKeep ? w_pre[kKeep ? i : 0] : load_f32(p.w_pre + c);
+        const F8 w = weights.get_pre(p, i, c);
 #pragma unroll
         for (int e = 0; e < kPairs; ++e) v.u.v[e] = __fmul2_rn(v.dh.v[e], w.v[e]);
       }
@@ -620,13 +660,13 @@ Shape row_shape(int64_t cols, bool back) {
   return s;
 }
 
-// Stages of the ring: as many as leave room for two CTAs on an SM, or two in
-// all of its shared memory; 0 (no ring) where a row is too long for that.
+// Stages of the ring: as many as leave room for two CTAs on an SM, and at
+// least two, for which the longest rows that take a ring have room (196 KB:
+// backward 8192 columns, forward 16384, FP32 stream).
 constexpr uint32_t kHalfSmem = 110 * 1024, kFullSmem = 220 * 1024;
+static_assert(2 * 8192 * 12 <= kFullSmem && 2 * 16384 * 6 <= kFullSmem, "two stages");
 int ring_stages(uint64_t stage_bytes) {
-  if (2 * stage_bytes <= kHalfSmem)
-    return (int)std::min<uint64_t>(kMaxStages, kHalfSmem / stage_bytes);
-  return 2 * stage_bytes <= kFullSmem ? 2 : 0;
+  return (int)std::max<uint64_t>(2, std::min<uint64_t>(kMaxStages, kHalfSmem / stage_bytes));
 }
 
 // Sets the shared-memory limit of a kernel and looks up the CTAs that fit an SM
@@ -659,7 +699,9 @@ template <int VPT, bool WIDE, bool RING, int PARTS, bool BACK>
 cudaError_t launch_rows(const NormArgs& p, int threads, int sms, cudaStream_t stream, int* grid) {
   constexpr auto kern = BACK ? norm_bwd_kernel<VPT, WIDE, RING, PARTS>
                              : norm_fwd_kernel<VPT, WIDE, RING, PARTS>;
-  const uint32_t smem = RING ? p.stages * p.stage_bytes : 0u;
+  const uint32_t smem = RING                                           ? p.stages * p.stage_bytes
+                        : WeightsAt<VPT, RING>::value == kInSmem ? (uint32_t)p.cols * 8
+                                                                 : 0u;
   int per_sm = ctas_per_sm<kern>(threads, smem);
   if (per_sm < 1) return cudaErrorInvalidConfiguration;
   if (BACK) per_sm = std::min(per_sm, kBwdCtasPerSm);
@@ -681,12 +723,11 @@ cudaError_t launch_norm(NormArgs& p, int sms, cudaStream_t stream, int* grid) {
   p.wpr = s.wpr;
   p.rpc = s.rpc;
   const uint64_t row = (uint64_t)p.cols * ((WIDE ? 4 : 2) + 2) * (BACK ? 2 : 1);
-  p.stages = s.vpt <= 4 ? ring_stages(row * s.rpc) : 0;
+  constexpr bool kRing4 = !BACK;
+  p.stages = s.vpt == 2 || (s.vpt == 4 && kRing4) ? ring_stages(row * s.rpc) : 0;
   p.stage_bytes = p.stages ? (uint32_t)(row * s.rpc) : 0u;
   if (s.vpt == 2) return launch_parts<2, WIDE, true, BACK>(p, s.threads, sms, stream, grid);
-  if (s.vpt == 4 && p.stages)
-    return launch_parts<4, WIDE, true, BACK>(p, s.threads, sms, stream, grid);
-  if (s.vpt == 4) return launch_parts<4, WIDE, false, BACK>(p, s.threads, sms, stream, grid);
+  if (s.vpt == 4) return launch_parts<4, WIDE, kRing4, BACK>(p, s.threads, sms, stream, grid);
   return launch_rows<kMaxVpt, WIDE, false, kAsGiven, BACK>(p, s.threads, sms, stream, grid);
 }
 
