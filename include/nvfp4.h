@@ -515,9 +515,9 @@ nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t fl
  * [rows, .] tensor.  The offsets are multiples of 128 (the rows of a scale
  * atom), rows is a multiple of 128, and the rows of a group's last block of
  * 128 past its size, and those from offsets[groups] on, are padding, which
- * every producer here writes as zero.  sizes [groups] and offsets
- * [groups + 1] are device int32 arrays: nothing of a plan is known to the
- * host, so a whole block can be captured into a graph. */
+ * every producer here writes as zero.  Groups do not overlap.  sizes [groups]
+ * and offsets [groups + 1] are device int32 arrays: nothing of a plan is known
+ * to the host, so a whole block can be captured into a graph. */
 
 /* How the weights of the chosen experts are normalised. */
 enum {

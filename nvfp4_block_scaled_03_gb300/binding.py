@@ -760,8 +760,10 @@ def nvfp4_combine_bwd(dy: torch.Tensor, o: torch.Tensor, row: torch.Tensor, sour
 
 def _groups(sizes, offsets):
     groups = sizes.numel()
-    _cuda(sizes, _I32, "sizes")
+    _cuda(sizes, _I32, "sizes", (groups,))
     _cuda(offsets, _I32, "offsets", (groups + 1,))
+    if groups < 1:
+        raise ValueError("there must be a group")
     return groups
 
 

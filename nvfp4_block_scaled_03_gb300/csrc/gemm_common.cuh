@@ -220,9 +220,13 @@ int gemm_setup(GemmLaunchState& ls, K kern, uint32_t smem, int threads, int spli
       attr.val.clusterDim.z = 1;
       cfg.attrs = &attr;
       cfg.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n <= 0)
-        n = sms / cluster;
-      n = std::min(n, sms / cluster);
+      const bool known = cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+      if (!known && cluster > 2) {  // no room for such clusters: the caller has another way
+        cudaGetLastError();
+        ls.resident[dev] = -1;
+        return 0;
+      }
+      n = known ? std::min(n, sms / cluster) : sms / cluster;
     }
     ls.resident[dev] = n;
   }

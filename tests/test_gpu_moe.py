@@ -119,6 +119,31 @@ def test_residual_norm_in_place_and_zero_rows(nv):
     assert all(torch.equal(u, v) for u, v in zip(grads, again))  # fixed order of every sum
 
 
+@pytest.mark.parametrize("T,D,wide", [(37, 512, True), (700, 4096, False), (9, 16384, False)])
+def test_residual_norm_gradients_in_place(nv, T, D, wide):
+    """dx may be dy, and dz may be dh or z (the library's own call: the binding
+    allocates its outputs)."""
+    import ctypes as C
+    import torch
+    t = {k: v.cuda() for k, v in _norm_case(T, D, wide, "channel", seed=3).items()}
+    want = nv.nvfp4_residual_norm_bwd(t["dy"], t["dh"], t["x"], t["z"], t["w_post"], t["gate"],
+                                      t["w_pre"])
+    p = nv.NormParams(T, D, int(wide), nv.GATE_CHANNEL, 1e-5, 1.0, 1.0)
+    n = C.c_size_t()
+    nv.lib.nvfp4_residual_norm_bwd_sizes(T, D, n)
+    ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+    for dz in ("dh", "z"):
+        c = {k: v.clone() for k, v in t.items()}
+        dw, dg, dp = (torch.empty(D, device="cuda") for _ in range(3))
+        st = nv.lib.nvfp4_residual_norm_bwd(
+            p, *[c[k].data_ptr() for k in ("dy", "dh", "x", "z", "w_post", "gate", "w_pre")],
+            c["dy"].data_ptr(), c[dz].data_ptr(), dw.data_ptr(), dg.data_ptr(), dp.data_ptr(),
+            ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+        assert st == nv.OK
+        for got, ref in zip((c["dy"], c[dz], dw, dg, dp), want):
+            assert torch.equal(got, ref)
+
+
 def test_residual_norm_keeps_a_bad_row_to_itself(nv):
     import torch
     t = {k: None if v is None else v.cuda() for k, v in _norm_case(6, 256, False, "none", 2).items()}
@@ -514,6 +539,8 @@ def test_binding_refuses_what_does_not_fit(nv):
     s, o, _ = _groups([100, 128])
     with pytest.raises(ValueError):
         nv.nvfp4_group_gemm(A, B, s, o[:2])
+    with pytest.raises(ValueError):
+        nv.nvfp4_group_gemm(A, B, s[:0], o[:1])
     with pytest.raises(nv.NVFP4Error) as e:
         nv.nvfp4_group_gemm(A, B, s, o, d_mode=nv.D_F32_ACCUM)
     assert e.value.status == nv.ERR_INVALID_ARG
