@@ -541,16 +541,11 @@ def _on_stream(call):
     return run
 
 
-_moe_ws: dict = {}
-
-
-def _moe_workspace(nbytes, t):
-    """Scratch of the current stream (kept between calls, as large as the largest)."""
-    key = (t.get_device(), _current(t))
-    ws = _moe_ws.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _moe_ws[key] = torch.empty(max(nbytes, 16), dtype=_U8, device=t.device)
-    return ws
+def _scratch(nbytes, t):
+    """A workspace of the current stream for one call.  It comes from the
+    allocator each time: one that a later, larger call replaced would still be
+    written by the graphs that captured it."""
+    return torch.empty(max(nbytes, 16), dtype=_U8, device=t.device)
 
 
 def operand(codes: torch.Tensor, scales: torch.Tensor, s_dec: torch.Tensor, rows: int,
@@ -642,7 +637,7 @@ def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
         _cuda(plan.row, _I32, "row", (tokens, top))
         _cuda(plan.source, _I32, "source", (route_sizes(tokens, experts, top)[0],))
     if workspace is None:
-        workspace = _moe_workspace(route_sizes(tokens, experts, top)[1], logits)
+        workspace = _scratch(route_sizes(tokens, experts, top)[1], logits)
     st = lib.nvfp4_route_fwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
                              plan.expert.data_ptr(), plan.weight.data_ptr(),
                              plan.sizes.data_ptr(), plan.offsets.data_ptr(), plan.row.data_ptr(),
@@ -883,7 +878,7 @@ def nvfp4_residual_norm_bwd(dy: torch.Tensor | None, dh: torch.Tensor | None, x:
         n = C.c_size_t()
         _check(lib.nvfp4_residual_norm_bwd_sizes(p.rows, p.cols, n),
                "nvfp4_residual_norm_bwd_sizes")
-        workspace = _moe_workspace(n.value, x)
+        workspace = _scratch(n.value, x)
     outs = [None if t is None else torch.empty_like(t) for t in (x, z, w_post, gate, w_pre)]
     st = lib.nvfp4_residual_norm_bwd(p, _ptr(dy), _ptr(dh), *ins, *[_ptr(t) for t in outs],
                                      workspace.data_ptr(), workspace.numel(), _current(x))

@@ -14,6 +14,8 @@
   truncation) of the accumulator for each of the K / 64 steps, and of each of
   the 64 aligned products inside a step.
 """
+import ctypes as C
+
 import numpy as np
 import pytest
 
@@ -547,3 +549,33 @@ def test_binding_refuses_what_does_not_fit(nv):
     with pytest.raises(nv.NVFP4Error) as e:
         nv.nvfp4_group_gemm(A, B, s, o, b_view=1)  # B has no transposed codes
     assert e.value.status == nv.ERR_INVALID_ARG
+
+
+def test_a_graph_keeps_its_scratch_to_itself(nv):
+    """A captured call is replayed after a larger one on the same stream: what
+    was allocated since is not written, and the replay gives what the call gave."""
+    import torch
+    stream = torch.cuda.Stream()
+    small = [torch.randn(640, 128, device="cuda") for _ in range(2)]
+    large = [torch.randn(640, 8192, device="cuda") for _ in range(2)]
+    w = [torch.ones(n, device="cuda") for n in (128, 8192)]
+    torch.cuda.synchronize()
+
+    def call(t, w):
+        return nv.nvfp4_residual_norm_bwd(t[0], None, t[0], t[1].bfloat16(), w_post=w)
+
+    with torch.cuda.stream(stream):
+        want = call(small, w[0])
+        n = C.c_size_t()
+        nv._check(nv.lib.nvfp4_residual_norm_bwd_sizes(640, 128, n), "sizes")
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            got = call(small, w[0])
+        call(large, w[1])
+        since = [torch.full((n.value,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+        graph.replay()
+        stream.synchronize()
+    assert all((t == 7).all() for t in since)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
+    nv.check_device_errors()
