@@ -147,11 +147,11 @@ NVFP4_DEV void clear_tail(const GroupArgs& a, int64_t i, int64_t n) {
 
 // =============================================================================
 // CTA-pair kernel: tiles of 256 x BN (BN = 256 or 384) on a cluster of two SMs
-// (tcgen05 cta_group::2).  As gemm.cu's pair kernels: CTA r loads rows [128 r, 128 r + 128) of A's 256 and
-// its half of B's rows, four scale warps of each CTA store the stage's scales
-// into tensor memory, the leader issues the MMAs (a second MMA warp takes the
-// last 128 columns of a 384-wide tile), and 8 epilogue warps of each CTA drain
-// its 128 rows.  Of a 256-row tile whose group ends in its first half, and of
+// (tcgen05 cta_group::2).  As gemm.cu's pair kernels: CTA r loads rows [128 r,
+// 128 r + 128) of A's 256 and its half of B's rows, four scale warps of each CTA
+// store the stage's scales into tensor memory, the leader issues the MMAs (a
+// second MMA warp takes the last 128 columns of a 384-wide tile), and 8 epilogue
+// warps of each CTA drain its 128 rows.  Of a 256-row tile whose group ends in its first half, and of
 // the last tile of an M that is an odd multiple of 128, the second CTA stores
 // nothing.
 //
@@ -164,24 +164,35 @@ NVFP4_DEV void clear_tail(const GroupArgs& a, int64_t i, int64_t n) {
 // Outputs leave through shared-memory boxes of 32 rows x 32 columns and tensor
 // stores; the FP32 fold as tensor reductions (one FP32 add in L2 for each
 // element, subnormals flushed there), so D is never read into the SM.
+//
+// What bounds it, and measured: long contractions the tensor pipe (16384 rows, 8
+// groups, 4096 x 14336: 322 us alone, 6.0 PF/s; the dense kernel takes 304), few
+// rows the weights' bytes (2 rows of the same, 73 MB: 19.9 us, 11 at the copy
+// rate).  Weight gradients have a few stages a tile: 64 x [1024, 2048] bf16 over
+// 32000 rows take 70 us (324 MB, 4.6 TB/s), 57 without stores, 63 without MMAs;
+// the fold of 16384 rows into 8 x [4096, 2048] takes 123 (593 MB, 4.8 TB/s), 66
+// without its reductions.  256 x 128 tiles with two accumulators took 88 and 151
+// there; more boxes a warp or 128-byte box rows changed nothing.
 // =============================================================================
-template <int BN, int DMODE>
+template <int BN, int DMODE, int SK>
 struct PairGroup {
   static constexpr bool kF32 = DMODE == NVFP4_D_F32_ACCUM;
+  static constexpr bool kAddC = DMODE == NVFP4_D_BF16_ADD_C && SK == 1 && BN == 256;
   static constexpr int kAt = 4, kRowBlocks = BN / 128;
-  static constexpr int kStages = BN == 384 || kF32 ? 4 : 5;
+  static constexpr int kStages = BN == 384 || kF32 || kAddC ? 4 : 5;
+  static constexpr int kBoxes = kAddC ? 4 : 1;  // of an epilogue warp
   static constexpr int kMmaWarps = BN == 384 ? 2 : 1;
   static constexpr uint32_t kA = 128 * kBKBytes, kB = (BN / 2) * kBKBytes;
   static constexpr uint32_t kSFA = kAt * 512, kSFB = kRowBlocks * kAt * 512;
   static constexpr uint32_t kBox = 32 * (kF32 ? 128 : 64);
   static constexpr uint32_t offA = 0, offB = offA + kStages * kA;
   static constexpr uint32_t offStore = offB + kStages * kB;
-  static constexpr uint32_t offSFA = offStore + 8 * kBox;
+  static constexpr uint32_t offSFA = offStore + 8 * kBoxes * kBox;
   static constexpr uint32_t offSFB = offSFA + kStages * kSFA;
   static constexpr uint32_t offBar = offSFB + kStages * kSFB;
   // full, empty, scales-ready, scales-landed per stage; acc full, acc empty;
-  // a drain barrier per MMA warp
-  static constexpr uint32_t kNumBars = 4 * kStages + 2 + kMmaWarps;
+  // a drain barrier per MMA warp; a barrier per epilogue warp for its part of C
+  static constexpr uint32_t kNumBars = 4 * kStages + 2 + kMmaWarps + (kAddC ? 8 : 0);
   static constexpr uint32_t offMisc = offBar + kNumBars * 8;
   static constexpr uint32_t offTable = offMisc + 16;
   static constexpr uint32_t kBytes = offTable + sizeof(GroupTable);
@@ -215,7 +226,7 @@ NVFP4_DEV void tma_reduce_add_2d(const CUtensorMap* map, uint32_t src, int32_t x
       : "memory");
 }
 
-// Asks L2 for a box of D ahead of its reduction, or for a piece of a row of C.
+// Asks L2 for a box of D ahead of its reduction.
 NVFP4_DEV void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -223,18 +234,17 @@ NVFP4_DEV void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
                : "memory");
 }
 
-NVFP4_DEV void bulk_prefetch(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // One warp's 32 rows x 32 columns (lane = row) into its box and out.  The 16-byte
 // pieces of a row are permuted as the map's swizzle says (64- or 128-byte), so
 // a warp's writes hit distinct banks; the box is rewritten once the store
-// before has read it.
+// before has read it (FREE: that has been waited for).
+template <bool FREE>
 NVFP4_DEV void store_box(uint8_t* box, int lane, const uint32_t (&pk)[16], const CUtensorMap* map,
                          int32_t x, int32_t y) {
-  if (lane == 0) bulk_wait_group_read<0>();
-  __syncwarp();
+  if (!FREE) {
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
 #pragma unroll
   for (int p = 0; p < 4; ++p)
     *reinterpret_cast<uint4*>(box + lane * 64 + ((p ^ ((lane >> 1) & 3)) * 16)) =
@@ -270,14 +280,15 @@ NVFP4_DEV void st_cluster_f4(uint32_t cluster_addr, const float4 v) {
 }
 
 template <int KIND, int BN, int DMODE, int SK>
-__global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, DMODE>::kThreads, 1)
+__global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, DMODE, SK>::kThreads, 1)
     group_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ CUtensorMap tmB2,
                       const __grid_constant__ CUtensorMap tmSFA,
                       const __grid_constant__ CUtensorMap tmSFB,
-                      const __grid_constant__ CUtensorMap tmD, const GroupArgs args) {
-  using L = PairGroup<BN, DMODE>;
+                      const __grid_constant__ CUtensorMap tmD,
+                      const __grid_constant__ CUtensorMap tmC, const GroupArgs args) {
+  using L = PairGroup<BN, DMODE, SK>;
   constexpr int S = L::kStages, kAt = L::kAt;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -291,6 +302,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
   const uint32_t acc_full = bar0 + 8u * (4 * S);
   const uint32_t acc_empty = acc_full + 8;
   const uint32_t drain_bar = acc_full + 16;
+  [[maybe_unused]] const uint32_t c_bar = drain_bar + 8u * L::kMmaWarps;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
   GroupTable* table = reinterpret_cast<GroupTable*>(smem + L::offTable);
@@ -312,6 +324,8 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
     mbar_init(acc_full, L::kMmaWarps);
     mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA
     for (int d = 0; d < L::kMmaWarps; ++d) mbar_init(drain_bar + 8u * d, 1);
+    if (L::kAddC)
+      for (int w = 0; w < 8; ++w) mbar_init(c_bar + 8u * w, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -521,10 +535,12 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
     const int q = warp & 3, h = ew >> 2;
     const uint32_t acc_empty_leader = mapa_shared(acc_empty, first);
     const float alpha = __fmul_rn(__ldg(args.sdec_a), __ldg(args.sdec_b));
-    uint8_t* box = smem + L::offStore + ew * L::kBox;
+    uint8_t* box = smem + L::offStore + ew * (L::kBoxes * L::kBox);
     if (lane == 0) prefetch_tmap(&tmD);
-    // 32 columns of a row: times alpha, plus C, rounded; zero outside the group
-    auto finish = [&](float (&f)[32], int64_t row, int col, bool live, uint32_t (&pk)[16]) {
+    // 32 columns of a row: times alpha, plus C (from `c_box`, this lane's row of a
+    // box, or from memory), rounded; zero outside the group
+    auto finish = [&](float (&f)[32], int64_t row, int col, bool live, const uint8_t* c_box,
+                      uint32_t (&pk)[16]) {
 #pragma unroll
       for (int e = 0; e < 32; ++e) f[e] = __fmul_rn(f[e], alpha);
       if (DMODE == NVFP4_D_BF16_ADD_C && live && col < args.N) {
@@ -532,7 +548,9 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
             static_cast<const __nv_bfloat16*>(args.C) + row * args.N + col);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          const uint4 u = cp[p];
+          const uint4 u = L::kAddC ? *reinterpret_cast<const uint4*>(
+                                         c_box + ((p ^ ((lane >> 1) & 3)) * 16))
+                                   : cp[p];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -548,29 +566,44 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
     uint32_t acc_ph = 0;
     int g = 0;
     bool ok = true;
-    // What a later tile adds to, wanted in L2 by then.  A tile ahead takes the
-    // fold of 4000 rows into 128 x [1024, 1024] from 209 to 184 us, into 8 x
-    // [4096, 2048] (16384 rows) from 125 to 123, and 65536 rows x 1024 x 2048
-    // plus C in 64 groups from 219 to 198.
-    auto ahead = [&](int tile) {
+    // What a later tile adds to.  The fold wants its boxes of D in L2 by then: a
+    // tile ahead takes 4000 rows into 128 x [1024, 1024] from 209 to 184 us and
+    // 16384 rows into 8 x [4096, 2048] from 125 to 123.
+    [[maybe_unused]] auto ahead = [&](int tile) {
       int gn = g;
       const Tile t = tile_at<KIND, BN>(tile, gn, table, args);
-      const int x0 = t.d_col + h * kCols, r0 = (int)rank * 128 + q * 32;
-      if constexpr (L::kF32) {
-        if (lane == 0 && t.atoms > 0 && t.live > (int)rank * 128)
-          for (int c = 0; c < kChunks; ++c)
-            if (x0 + c * 32 < args.N)
-              tma_prefetch_2d(&tmD, x0 + c * 32, (int32_t)(t.d_row + r0));
-      } else if (r0 + lane < t.live && x0 < args.N) {
-        bulk_prefetch(static_cast<const __nv_bfloat16*>(args.C) + (t.d_row + r0 + lane) * args.N + x0,
-                      (uint32_t)min(kCols, args.N - x0) * 2);
-      }
+      const int x0 = t.d_col + h * kCols;
+      if (lane == 0 && t.atoms > 0 && t.live > (int)rank * 128)
+        for (int c = 0; c < kChunks; ++c)
+          if (x0 + c * 32 < args.N)
+            tma_prefetch_2d(&tmD, x0 + c * 32, (int32_t)(t.d_row + (int)rank * 128 + q * 32));
     };
-    constexpr bool kAhead = L::kF32 || (DMODE == NVFP4_D_BF16_ADD_C && SK == 1);
-    if (kAhead && tile0 < tiles) ahead(tile0);
+    if (L::kF32 && tile0 < tiles) ahead(tile0);
+    // C lands in the warp's boxes while the tile's MMAs run; the sums leave from
+    // the same places (65536 rows, 64 groups, 1024 x 2048: 127 us; 219 with C read
+    // by each lane's loads, 89 without C).  N is a multiple of 128, so a warp's
+    // kCols columns lie in N or behind it as a whole.
+    static_assert(!L::kAddC || (kCols == 128 && kChunks == L::kBoxes), "boxes");
+    [[maybe_unused]] bool c_due = false;
+    [[maybe_unused]] uint32_t c_ph = 0;
+    auto fetch = [&](int tile) {
+      int gn = g;
+      const Tile t = tile_at<KIND, BN>(tile, gn, table, args);
+      const int x0 = t.d_col + h * kCols;
+      c_due = t.live > (int)rank * 128 && x0 < args.N;
+      if (c_due && lane == 0) {
+        bulk_wait_group_read<0>();
+        mbar_arrive_expect_tx(c_bar + 8u * ew, L::kBoxes * L::kBox);
+        for (int c = 0; c < kChunks; ++c)
+          tma_load_2d(smem_u32(box + c * L::kBox), &tmC, c_bar + 8u * ew, x0 + c * 32,
+                      (int32_t)(t.d_row + (int)rank * 128 + q * 32));
+      }
+      __syncwarp();
+    };
+    if (L::kAddC && tile0 < tiles) fetch(tile0);
     for (int tile = tile0; tile < tiles; tile += num_units) {
       const Tile t = tile_at<KIND, BN>(tile, g, table, args);
-      if (kAhead && tile + num_units < tiles) ahead(tile + num_units);
+      if (L::kF32 && tile + num_units < tiles) ahead(tile + num_units);
       const int r0 = (int)rank * 128 + q * 32;  // this warp's first row of the tile
       const bool mine = t.live > (int)rank * 128;
       const bool live = r0 + lane < t.live;
@@ -650,8 +683,8 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
                 }
               }
             uint32_t pk[16];
-            finish(f, t.d_row + r0 + lane, x0 + c * 32, live, pk);
-            if (x0 + c * 32 < args.N) store_box(box, lane, pk, &tmD, x0 + c * 32, y);
+            finish(f, t.d_row + r0 + lane, x0 + c * 32, live, nullptr, pk);
+            if (x0 + c * 32 < args.N) store_box<false>(box, lane, pk, &tmD, x0 + c * 32, y);
           }
         }
         break;  // the cluster's only tile
@@ -662,6 +695,14 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
             ok = false;
             break;
           }
+          if (L::kAddC && c_due) {
+            if (!wait_bounded_pair(c_bar + 8u * ew, c_ph, abort_flag, peer_abort, 0x44u)) {
+              ok = false;
+              break;
+            }
+            c_due = false;
+            c_ph ^= 1u;
+          }
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
@@ -671,7 +712,8 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
             float f[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(r[e]);
-            finish(f, t.d_row + r0 + lane, x0 + c * 32, live, pk[c]);
+            finish(f, t.d_row + r0 + lane, x0 + c * 32, live,
+                   box + (L::kAddC ? c : 0) * L::kBox + lane * 64, pk[c]);
           }
           tc_fence_before();
           __syncwarp();
@@ -683,12 +725,16 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
 #pragma unroll
             for (int e = 0; e < 16; ++e) pk[c][e] = 0u;
         }
-        if (!mine) continue;
+        if (mine)
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (x0 + c * 32 < args.N) store_box(box, lane, pk[c], &tmD, x0 + c * 32, y);
+          for (int c = 0; c < kChunks; ++c)
+            if (x0 + c * 32 < args.N)
+              store_box<L::kAddC>(box + (L::kAddC ? c : 0) * L::kBox, lane, pk[c], &tmD,
+                                  x0 + c * 32, y);
+        if (L::kAddC && tile + num_units < tiles) fetch(tile + num_units);
       }
     }
+    if (L::kAddC && c_due) wait_drain(c_bar + 8u * ew, c_ph);  // given up: its loads have landed
     if (SK > 1 && part >= parts && parts > 1) {  // a pair without a part of the tile
       __syncwarp();
       cluster_sync();
@@ -732,7 +778,7 @@ struct Operands {
 // Clusters of a kernel that are resident at once; 0 when its set-up failed.
 template <int KIND, int BN, int DMODE, int SK>
 int group_units(int sms) {
-  using L = PairGroup<BN, DMODE>;
+  using L = PairGroup<BN, DMODE, SK>;
   static GemmLaunchState ls;
   return gemm_setup(ls, group_pair_kernel<KIND, BN, DMODE, SK>, L::kAlloc, L::kThreads,
                     L::kSplitRegs, 2 * SK, sms);
@@ -740,22 +786,23 @@ int group_units(int sms) {
 
 template <int KIND, int BN, int DMODE, int SK>
 nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStream_t stream) {
-  using L = PairGroup<BN, DMODE>;
+  using L = PairGroup<BN, DMODE, SK>;
   auto kern = group_pair_kernel<KIND, BN, DMODE, SK>;
   const int units = group_units<KIND, BN, DMODE, SK>(sms);
   if (units <= 0) return NVFP4_ERR_CUDA;
   a.num_m_blk = (a.M + 255) / 256;
   a.num_n_blk = (a.N + BN - 1) / BN;
-  CUtensorMap ma, mb, mb2, msa, msb, md;
+  CUtensorMap ma, mb, mb2, msa, msb, md, mc;
   if (!make_code_map(&ma, o.a_codes, o.a_rows, o.a_cols / 2, 128) ||
       !make_code_map(&mb, o.b_codes, o.b_rows, o.b_cols / 2, 128) ||
       !make_code_map(&mb2, o.b_codes, o.b_rows, o.b_cols / 2, 64) ||
       !make_sf_map(&msa, o.a_sf, swizzled_scale_bytes(o.a_rows, o.a_cols)) ||
       !make_sf_map(&msb, o.b_sf, swizzled_scale_bytes(o.b_rows, o.b_cols)) ||
-      !make_box_map(&md, a.D, o.d_rows, a.N, L::kF32))
+      !make_box_map(&md, a.D, o.d_rows, a.N, L::kF32) ||
+      !make_box_map(&mc, L::kAddC ? a.C : a.D, o.d_rows, a.N, L::kF32))
     return NVFP4_ERR_CUDA;
   return cuda_status(launch_pdl(kern, 2 * SK * units, L::kThreads, L::kAlloc, stream, ma, mb, mb2, msa,
-                                msb, md, a));
+                                msb, md, mc, a));
 }
 
 // The width of a product's tiles: the one whose rounds of tiles over the pairs
@@ -793,7 +840,11 @@ nvfp4_status launch_tile(int32_t tile, const Operands& o, const GroupArgs& a, in
         return launch_group_pair<KIND, 256, DMODE, 4>(o, a, sms, stream);
       if (a.K >= kSharedK && tiles <= group_units<KIND, 256, DMODE, 2>(sms))
         return launch_group_pair<KIND, 256, DMODE, 2>(o, a, sms, stream);
-      tile = rows_tile(a.rows, a.groups, a.N, sms / 2);
+      // with C the narrow tiles, whose boxes have room for it.  Measured (us, 256
+      // and 384 wide): 8192 rows, 8 groups, 14336 x 4096: 217, 215; 16384 rows, 8
+      // groups, 2048 x 4096: 94, 120; 65536 rows, 64 groups, 1024 x 2048: 127, 219.
+      tile = DMODE == NVFP4_D_BF16_ADD_C ? NVFP4_TILE_PAIR_256X256
+                                         : rows_tile(a.rows, a.groups, a.N, sms / 2);
     }
   }
   if constexpr (DMODE != NVFP4_D_F32_ACCUM)

@@ -579,3 +579,64 @@ def test_a_graph_keeps_its_scratch_to_itself(nv):
     assert all((t == 7).all() for t in since)
     assert torch.equal(got[0], want[0]) and torch.equal(got[2], want[2])
     nv.check_device_errors()
+
+
+@pytest.mark.parametrize("tile", [0, 3, 6])
+@pytest.mark.parametrize("view,N,K", [(0, 1280, 192), (1, 1408, 512)])
+def test_group_gemm_of_many_tiles_plus_c(nv, tile, view, N, K):
+    """Several tiles for each pair of SMs, C fetched for one while another leaves;
+    C holds NaN outside the groups, and may be the output."""
+    import torch
+    sizes = [(37 * e) % 300 for e in range(40)]
+    E = len(sizes)
+    s, o, off = _groups(sizes)
+    rows = int(off[-1]) + 128
+    g = torch.Generator(device="cuda").manual_seed(N + K)
+    A = nv.nvfp4_quantize(torch.randn(rows, K, generator=g, device="cuda").bfloat16(), nv.ROW_1X16)
+    shape = (E * K, N) if view else (E * N, K)
+    B = nv.nvfp4_quantize(torch.randn(*shape, generator=g, device="cuda") * 0.05, nv.BLOCK_16X16,
+                          nv.EMIT_T)
+    C = torch.randn(rows, N, generator=g, device="cuda").bfloat16()
+    a = _decode(A, rows, K)
+    b = _decode(B, N, E * K, 1) if view else _decode(B, E * N, K)
+    ref, live = np.zeros((rows, N)), np.zeros(rows, dtype=bool)
+    for e, n in enumerate(sizes):
+        be = b[:, e * K:(e + 1) * K] if view else b[e * N:(e + 1) * N]
+        ref[off[e]:off[e] + n] = a[off[e]:off[e] + n] @ be.T
+        live[off[e]:off[e] + n] = True
+    C[torch.from_numpy(~live).cuda()] = float("nan")
+    rms = np.sqrt(np.mean(ref[live] ** 2))
+    for c, out in ((None, torch.empty_like(C)), (C, torch.empty_like(C)), (C, C)):
+        want = ref if c is None else ref + _f64(c)
+        nv.nvfp4_group_gemm(A, B, s, o, b_view=view, out=out, C_add=c, tile=tile,
+                            d_mode=nv.D_BF16 if c is None else nv.D_BF16_ADD_C)
+        got = _f64(out)
+        assert (got[~live] == 0).all()
+        H.assert_gemm_close(got[live], want[live], f"{N} {K}", rms=rms)
+    nv.check_device_errors()
+
+
+@pytest.mark.parametrize("tile", [3, 6])
+def test_group_plus_c_wait_expires_then_recovers(nv, tile):
+    """The bounded waits of the calls that add C, whose own copies are in flight."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(1)
+    A = nv.nvfp4_quantize(torch.randn(256, 256, generator=g, device="cuda"), nv.ROW_1X16)
+    B = nv.nvfp4_quantize(torch.randn(512, 256, generator=g, device="cuda"), nv.BLOCK_16X16)
+    C = torch.randn(256, 256, generator=g, device="cuda").bfloat16()
+    s, o, _ = _groups([100, 128])
+    call = lambda: nv.nvfp4_group_gemm(A, B, s, o, C_add=C, d_mode=nv.D_BF16_ADD_C,  # noqa: E731
+                                       tile=tile)
+    want = call()
+    nv.check_device_errors()
+    nv.debug_inject(nv.STALL_GEMM, 1_000_000)
+    try:
+        call()
+        with pytest.raises(nv.NVFP4Error) as e:
+            nv.check_device_errors()
+        assert e.value.status == nv.ERR_DEVICE_TIMEOUT
+    finally:
+        nv.debug_inject(0, 0)
+    nv.check_device_errors()
+    assert torch.equal(call(), want)
+    nv.check_device_errors()
