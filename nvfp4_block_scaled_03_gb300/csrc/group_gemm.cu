@@ -792,14 +792,14 @@ nvfp4_status launch_group_pair(const Operands& o, GroupArgs a, int sms, cudaStre
   if (units <= 0) return NVFP4_ERR_CUDA;
   a.num_m_blk = (a.M + 255) / 256;
   a.num_n_blk = (a.N + BN - 1) / BN;
-  CUtensorMap ma, mb, mb2, msa, msb, md, mc;
+  CUtensorMap ma, mb, mb2 = {}, msa, msb, md, mc = {};  // mb2, mc: where the kernel reads them
   if (!make_code_map(&ma, o.a_codes, o.a_rows, o.a_cols / 2, 128) ||
       !make_code_map(&mb, o.b_codes, o.b_rows, o.b_cols / 2, 128) ||
-      !make_code_map(&mb2, o.b_codes, o.b_rows, o.b_cols / 2, 64) ||
+      (BN == 384 && !make_code_map(&mb2, o.b_codes, o.b_rows, o.b_cols / 2, 64)) ||
       !make_sf_map(&msa, o.a_sf, swizzled_scale_bytes(o.a_rows, o.a_cols)) ||
       !make_sf_map(&msb, o.b_sf, swizzled_scale_bytes(o.b_rows, o.b_cols)) ||
       !make_box_map(&md, a.D, o.d_rows, a.N, L::kF32) ||
-      !make_box_map(&mc, L::kAddC ? a.C : a.D, o.d_rows, a.N, L::kF32))
+      (L::kAddC && !make_box_map(&mc, a.C, o.d_rows, a.N, false)))
     return NVFP4_ERR_CUDA;
   return cuda_status(launch_pdl(kern, 2 * SK * units, L::kThreads, L::kAlloc, stream, ma, mb, mb2, msa,
                                 msb, md, mc, a));
