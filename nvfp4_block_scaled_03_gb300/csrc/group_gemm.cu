@@ -165,14 +165,15 @@ NVFP4_DEV void clear_tail(const GroupArgs& a, int64_t i, int64_t n) {
 // stores; the FP32 fold as tensor reductions (one FP32 add in L2 for each
 // element, subnormals flushed there), so D is never read into the SM.
 //
-// What bounds it, and measured: long contractions the tensor pipe (16384 rows, 8
-// groups, 4096 x 14336: 322 us alone, 6.0 PF/s; the dense kernel takes 304), few
-// rows the weights' bytes (2 rows of the same, 73 MB: 19.9 us, 11 at the copy
-// rate).  Weight gradients have a few stages a tile: 64 x [1024, 2048] bf16 over
-// 32000 rows take 70 us (324 MB, 4.6 TB/s), 57 without stores, 63 without MMAs;
-// the fold of 16384 rows into 8 x [4096, 2048] takes 123 (593 MB, 4.8 TB/s), 66
-// without its reductions.  256 x 128 tiles with two accumulators took 88 and 151
-// there; more boxes a warp or 128-byte box rows changed nothing.
+// What bounds it, and measured: long contractions the stages' 48 KB into each SM
+// and the scales' stores (16384 rows, 8 groups, 4096 x 14336: 320 us alone, 6.0
+// PF/s; 281 without scales; the dense kernel takes 304), few rows the weights'
+// bytes (2 rows of the same, 73 MB: 19.5 us, 11 at the copy rate).  Weight
+// gradients have a few stages a tile: 64 x [1024, 2048] bf16 over 32000 rows take
+// 70 us (324 MB, 4.6 TB/s), 57 without stores, 63 without MMAs; the fold of 16384
+// rows into 8 x [4096, 2048] takes 123 (593 MB, 4.8 TB/s), 66 without its
+// reductions.  256 x 128 tiles with two accumulators took 88 and 151 there; more
+// boxes a warp or 128-byte box rows changed nothing.
 // =============================================================================
 template <int BN, int DMODE, int SK>
 struct PairGroup {
