@@ -600,7 +600,10 @@ class RoutePlan:
 
 def alloc_plan(tokens, experts, top, device="cuda") -> RoutePlan:
     """Buffers of a plan, e.g. for a server to route into at every step."""
-    rows, _ = route_sizes(tokens, experts, top)
+    return _alloc_plan(tokens, experts, top, route_sizes(tokens, experts, top)[0], device)
+
+
+def _alloc_plan(tokens, experts, top, rows, device):
     empty = torch.empty
     return RoutePlan(empty((tokens, top), dtype=_I32, device=device),
                      empty((tokens, top), dtype=_F32, device=device),
@@ -627,17 +630,20 @@ def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
     """Choose each token's `top` experts and order the rows by expert (see
     nvfp4_route_fwd in nvfp4.h)."""
     kind, tokens, experts, ld = _logits(logits)
+    rows, nbytes = route_sizes(tokens, experts, top)
     if plan is None:
-        plan = alloc_plan(tokens, experts, top, logits.device)
+        plan = _alloc_plan(tokens, experts, top, rows, logits.device)
     else:
         _cuda(plan.expert, _I32, "expert", (tokens, top))
         _cuda(plan.weight, _F32, "weight", (tokens, top))
         _cuda(plan.sizes, _I32, "sizes", (experts,))
         _cuda(plan.offsets, _I32, "offsets", (experts + 1,))
         _cuda(plan.row, _I32, "row", (tokens, top))
-        _cuda(plan.source, _I32, "source", (route_sizes(tokens, experts, top)[0],))
+        _cuda(plan.source, _I32, "source", (rows,))
     if workspace is None:
-        workspace = _scratch(route_sizes(tokens, experts, top)[1], logits)
+        workspace = _scratch(nbytes, logits)
+    else:
+        _cuda(workspace, _U8, "workspace")
     st = lib.nvfp4_route_fwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
                              plan.expert.data_ptr(), plan.weight.data_ptr(),
                              plan.sizes.data_ptr(), plan.offsets.data_ptr(), plan.row.data_ptr(),
@@ -879,6 +885,8 @@ def nvfp4_residual_norm_bwd(dy: torch.Tensor | None, dh: torch.Tensor | None, x:
         _check(lib.nvfp4_residual_norm_bwd_sizes(p.rows, p.cols, n),
                "nvfp4_residual_norm_bwd_sizes")
         workspace = _scratch(n.value, x)
+    else:
+        _cuda(workspace, _U8, "workspace")
     outs = [None if t is None else torch.empty_like(t) for t in (x, z, w_post, gate, w_pre)]
     st = lib.nvfp4_residual_norm_bwd(p, _ptr(dy), _ptr(dh), *ins, *[_ptr(t) for t in outs],
                                      workspace.data_ptr(), workspace.numel(), _current(x))

@@ -640,3 +640,32 @@ def test_group_plus_c_wait_expires_then_recovers(nv, tile):
     nv.check_device_errors()
     assert torch.equal(call(), want)
     nv.check_device_errors()
+
+
+def test_given_workspaces(nv):
+    """A caller's own scratch: bytes on the device, as many as the sizes say."""
+    import torch
+    logits = torch.randn(100, 16, device="cuda")
+    x, z = torch.randn(100, 256, device="cuda"), torch.randn(100, 256, device="cuda").bfloat16()
+    w = torch.randn(256, device="cuda")
+    n = C.c_size_t()
+    nv._check(nv.lib.nvfp4_residual_norm_bwd_sizes(100, 256, n), "sizes")
+    calls = [(lambda ws: [getattr(nv.nvfp4_route_fwd(logits, 4, workspace=ws), f)
+                          for f in ("expert", "weight", "sizes", "offsets", "row", "source")],
+              nv.route_sizes(100, 16, 4)[1]),
+             (lambda ws: [t for t in nv.nvfp4_residual_norm_bwd(x, None, x, z, w_post=w,
+                                                                 workspace=ws) if t is not None],
+              n.value)]
+    for call, nbytes in calls:
+        want = call(None)
+        got = call(torch.empty(nbytes, dtype=torch.uint8, device="cuda"))
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        with pytest.raises(nv.NVFP4Error) as e:
+            call(torch.empty(64, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == nv.ERR_WORKSPACE
+        for bad in (torch.empty(nbytes, dtype=torch.uint8),
+                    torch.empty(nbytes, dtype=torch.float32, device="cuda"),
+                    torch.empty(2 * nbytes, dtype=torch.uint8, device="cuda")[::2]):
+            with pytest.raises(ValueError):
+                call(bad)
+    nv.check_device_errors()
