@@ -113,7 +113,7 @@ nvfp4_status nvfp4_device_check(int device);
 nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream);
 
 /* Failure injection for tests of the bounded waits; the pages have no
- * counterpart (they describe no failure handling).  While a bit of
+ * counterpart (they describe no failure handling).  While a STALL bit of
  * stall_mask is set, the producer of every launch of that kernel family
  * issues no loads, so the consumers' first pipeline wait runs out; nothing is
  * in flight when the kernel gives up, and it returns after recording the
@@ -122,13 +122,17 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream);
  *                         loads of nvfp4_residual_norm_fwd / _bwd
  *   NVFP4_STALL_GEMM      every GEMM kernel (single-SM and CTA-pair tiles;
  *                         on a pair a timeout in either CTA stops both)
+ * With a LOSE bit the loads are issued and each block's first wait is for 16
+ * bytes more than will come, so the kernel gives up with loads behind it:
+ *   NVFP4_LOSE_NORM       nvfp4_residual_norm_fwd / _bwd (rows to 8192 columns,
+ *                         forward 16384: the others load no rows ahead)
  * wait_limit_ns sets how long those kernels' pipeline waits last before they
  * give up (0: the default, 2 s); the waits that drain copies and MMAs
  * already issued keep their own 2 s limit.  Synchronises the device, then
  * applies to later launches until changed; call it with nothing of this
  * library in flight.  Returns NVFP4_ERR_INVALID_ARG for unknown bits,
  * NVFP4_ERR_CUDA if the device cannot be reached. */
-enum { NVFP4_STALL_QUANTIZE = 1u, NVFP4_STALL_GEMM = 2u };
+enum { NVFP4_STALL_QUANTIZE = 1u, NVFP4_STALL_GEMM = 2u, NVFP4_LOSE_NORM = 16u };
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns);
 
 /* ---------------------------------------------------------------------- */

@@ -76,13 +76,15 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream) {
 }
 
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
-  if (stall_mask & ~(uint32_t)(NVFP4_STALL_QUANTIZE | NVFP4_STALL_GEMM))
+  if (stall_mask & ~(uint32_t)(NVFP4_STALL_QUANTIZE | NVFP4_STALL_GEMM | NVFP4_LOSE_NORM))
     return NVFP4_ERR_INVALID_ARG;
   const unsigned long long ns = wait_limit_ns ? wait_limit_ns : 2000000000ull;
   if (cudaDeviceSynchronize() != cudaSuccess) return NVFP4_ERR_CUDA;
   nvfp4_status st = quant_set_injection((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u, ns);
   if (st != NVFP4_OK) return st;
-  st = norm_set_injection((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u, ns);
+  st = norm_set_injection(((stall_mask & NVFP4_STALL_QUANTIZE) ? 1u : 0u) |
+                              ((stall_mask & NVFP4_LOSE_NORM) ? 2u : 0u),
+                          ns);
   if (st != NVFP4_OK) return st;
   st = group_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
   if (st != NVFP4_OK) return st;

@@ -45,6 +45,8 @@
 namespace nvfp4 {
 
 static __device__ unsigned int g_norm_error;
+// Failure injection (nvfp4_debug_inject): bit 0, no rows are loaded; bit 1, each
+// CTA's first barrier waits for 16 bytes that do not come.
 static __device__ unsigned int g_norm_stall;
 static __device__ unsigned long long g_norm_wait_ns = 2000000000ull;
 
@@ -56,6 +58,7 @@ constexpr int kMaxThreads = 512;
 constexpr int kMaxVpt = 16;       // 512 threads x 16 x 8 = 65536 columns
 constexpr int kRegVpt = 2;        // up to here the weights stay in registers
 constexpr int kMaxStages = 4;
+constexpr uint64_t kDrainNs = 2000000000ull;
 
 struct NormArgs {
   const void* x;
@@ -218,24 +221,11 @@ NVFP4_DEV F8 post_weight(const NormArgs& p, int c) {
 // ---- the ring of rows --------------------------------------------------------------
 // Stage s of the ring holds rpc rows of x, z (and, backward, dy, dh), each
 // array behind the other; a bulk copy per array, on the stage's barrier.
+// quit_row: where thread 0 gave up (the other threads' word is not read).
 struct Ring {
   uint64_t bar[kMaxStages];
+  int64_t quit_row[2];
 };
-
-// Wait with a limit.  A copy that never lands sets the error word; from then
-// on nothing waits (the results are void, as the error says).
-NVFP4_DEV void wait_row(uint32_t bar, uint32_t parity, bool& dead) {
-  if (dead || mbar_try_wait(bar, parity)) return;
-  const uint64_t t0 = globaltimer_ns();
-  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_norm_wait_ns);
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > limit) {
-      atomicCAS(&g_norm_error, 0u, 0x50u);
-      dead = true;
-      return;
-    }
-  }
-}
 
 template <bool WIDE>
 struct RowBytes {
@@ -305,14 +295,19 @@ template <bool WIDE, bool BACK>
 NVFP4_DEV void start_ring(const NormArgs& p, Ring& ring, uint32_t smem) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) mbar_init(smem_u32(&ring.bar[s]), 1);
+    ring.quit_row[0] = -1;
     fence_mbar_init();
   }
   __syncthreads();
   griddep_wait();
-  if (threadIdx.x == 0 && *reinterpret_cast<volatile unsigned int*>(&g_norm_stall) == 0u)
-    for (int s = 0; s < p.stages; ++s)
-      fetch_rows<WIDE, BACK>(p, smem, smem_u32(ring.bar),
-                             ((int64_t)blockIdx.x + (int64_t)s * gridDim.x) * p.rpc, s);
+  if (threadIdx.x == 0) {
+    const unsigned int stall = *reinterpret_cast<volatile unsigned int*>(&g_norm_stall);
+    if (stall & 2u) mbar_expect_tx(smem_u32(ring.bar), 16);
+    if (!(stall & 1u))
+      for (int s = 0; s < p.stages; ++s)
+        fetch_rows<WIDE, BACK>(p, smem, smem_u32(ring.bar),
+                               ((int64_t)blockIdx.x + (int64_t)s * gridDim.x) * p.rpc, s);
+  }
 }
 
 // The rows of a CTA, one set of rpc after the other, and their stages.
@@ -330,6 +325,54 @@ struct Walk {
     if (++stage == p.stages) stage = 0, phase ^= 1u;
   }
 };
+
+// Until the copies that thread 0 issued have landed, with a limit of its own:
+// those of the rows at `at`, where it gave up, and of the sets behind them that
+// it had sent for -- `stages` from the start, then one short of that, as a
+// refill comes after the wait.
+NVFP4_DEV void drain_ring(const NormArgs& p, Ring& ring, Walk at) {
+  if (*reinterpret_cast<volatile unsigned int*>(&g_norm_stall) & 1u) return;  // there are none
+  const uint64_t t0 = globaltimer_ns();
+  for (int i = at.first ? 0 : 1; i < p.stages && at.row0 < p.rows; ++i, at.next(p))
+    while (!mbar_try_wait(smem_u32(&ring.bar[at.stage]), at.phase) &&
+           globaltimer_ns() - t0 <= kDrainNs) {
+    }
+}
+
+// Wait with a limit.  A copy that never lands sets the error word; from then
+// on nothing is loaded or waited for (the results are void, as the error
+// says), and no copy outlives the CTA, whose shared memory is handed on: thread
+// 0 waits for them at once or (leave_ring) at the end.  The compiler's code for
+// rows that do land depends on which: with one norm forward 16384 x 4096 bf16
+// takes 43.6 us with the former, 46.7 with the latter; the backward with both
+// norms 161 and 148.
+template <bool AT_ONCE>
+NVFP4_DEV void wait_row(const NormArgs& p, Ring& ring, Walk& at) {
+  const uint32_t bar = smem_u32(&ring.bar[at.stage]);
+  if (at.dead || mbar_try_wait(bar, at.phase)) return;
+  const uint64_t t0 = globaltimer_ns();
+  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_norm_wait_ns);
+  while (!mbar_try_wait(bar, at.phase)) {
+    if (globaltimer_ns() - t0 > limit) {
+      atomicCAS(&g_norm_error, 0u, 0x50u);
+      if constexpr (AT_ONCE) {
+        if (threadIdx.x == 0) drain_ring(p, ring, at);
+      } else {
+        ring.quit_row[threadIdx.x != 0] = at.row0;
+      }
+      at.dead = true;
+      return;
+    }
+  }
+}
+
+template <bool AT_ONCE>
+NVFP4_DEV void leave_ring(const NormArgs& p, Ring& ring) {
+  if (AT_ONCE || threadIdx.x != 0 || ring.quit_row[0] < 0) return;
+  Walk at(p);
+  while (at.row0 < ring.quit_row[0]) at.next(p);
+  drain_ring(p, ring, at);
+}
 
 // Refills the stage of the rows before, once every thread is done with them
 // (called behind a barrier of the CTA).
@@ -409,7 +452,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p)
     const int64_t row = at.row0 + sub, at0 = row * p.cols;
     const bool live = row < p.rows;
     const RowPtrs in = row_ptrs<WIDE, RING>(p, smem, at.stage, sub, row);
-    if (RING) wait_row(smem_u32(&ring.bar[at.stage]), at.phase, at.dead);
+    if (RING) wait_row<PARTS != kBoth>(p, ring, at);
     float k = 0.0f;  // b [g] r_z
     float s;
     float2 q = both(0.0f);
@@ -470,6 +513,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormArgs p)
       }
     }
   }
+  if (RING) leave_ring<PARTS != kBoth>(p, ring);
 }
 
 template <int VPT, bool WIDE, bool RING, int PARTS>
@@ -494,7 +538,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs p)
     const int64_t row = at.row0 + sub, at0 = row * p.cols;
     const bool live = row < p.rows;
     const RowPtrs in = row_ptrs<WIDE, RING>(p, smem, at.stage, sub, row);
-    if (RING) wait_row(smem_u32(&ring.bar[at.stage]), at.phase, at.dead);
+    if (RING) wait_row<false>(p, ring, at);
     float rz = 0.0f, bg = p.b;  // b [g]
     if (post) {
       float2 q = both(0.0f);
@@ -606,6 +650,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const NormArgs p)
       if (pre) store_f32(out + p.cols + c, acc_pre[i]);
     }
   }
+  if (RING) leave_ring<false>(p, ring);
 }
 
 // Adds the CTAs' partial column sums: a CTA of 8 warps takes 32 columns of

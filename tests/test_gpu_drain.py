@@ -1,0 +1,53 @@
+"""A kernel that gives up at a wait while copies that it issued are in flight sees
+them land before it ends: its shared memory goes to the next block on the SM.
+Injected, each block waits at first for more bytes than come, with the loads of
+its other stages issued behind them; the error is reported, and the calls after
+it, which take the same shared memory, give what they gave before.  (A block
+gives up after the injected limit, and its last look at the copies, of which one
+is never complete, has the library's own limit of 2 s.)"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+LIMIT_NS = 1_000
+
+
+@pytest.fixture(scope="module")
+def nv():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_block_scaled_03_gb300 import binding
+    return binding
+
+
+def _gives_up_then_recovers(nv, bit, call):
+    import torch
+    want = call()
+    nv.check_device_errors()
+    nv.debug_inject(bit, LIMIT_NS)
+    try:
+        call()
+        with pytest.raises(nv.NVFP4Error) as e:
+            nv.check_device_errors()
+        assert e.value.status == nv.ERR_DEVICE_TIMEOUT
+    finally:
+        nv.debug_inject(0, 0)
+    nv.check_device_errors()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    nv.check_device_errors()
+
+
+# one row; rows for every stage of the ring, several and one to a block
+@pytest.mark.parametrize("rows,cols,wide", [(1, 8, False), (9000, 512, False), (2000, 4096, True)])
+def test_norm_that_gives_up_waits_for_its_rows(nv, rows, cols, wide):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    kind = torch.float32 if wide else torch.bfloat16
+    x, dy = (torch.randn(rows, cols, generator=g, device="cuda").to(kind) for _ in range(2))
+    z, dh = (torch.randn(rows, cols, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = [torch.randn(cols, generator=g, device="cuda") for _ in range(3)]
+    _gives_up_then_recovers(nv, nv.LOSE_NORM, lambda: nv.nvfp4_residual_norm_fwd(x, z, *w))
+    _gives_up_then_recovers(nv, nv.LOSE_NORM, lambda: nv.nvfp4_residual_norm_bwd(dy, dh, x, z, *w))
+    _gives_up_then_recovers(nv, nv.LOSE_NORM,
+                            lambda: nv.nvfp4_residual_norm_fwd(x, w_pre=w[0])[1:])
