@@ -123,16 +123,19 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream);
  *   NVFP4_STALL_GEMM      every GEMM kernel (single-SM and CTA-pair tiles;
  *                         on a pair a timeout in either CTA stops both)
  * With a LOSE bit the loads are issued and each block's first wait is for 16
- * bytes more than will come, so the kernel gives up with loads behind it:
+ * bytes more than will come, so the kernel gives up with loads behind it; with
+ * a QUIT bit it gives up before its first wait, its loads in flight:
  *   NVFP4_LOSE_NORM       nvfp4_residual_norm_fwd / _bwd (rows to 8192 columns,
  *                         forward 16384: the others load no rows ahead)
+ *   NVFP4_QUIT_GEMM       nvfp4_group_gemm, nvfp4_group_wgrad
  * wait_limit_ns sets how long those kernels' pipeline waits last before they
  * give up (0: the default, 2 s); the waits that drain copies and MMAs
  * already issued keep their own 2 s limit.  Synchronises the device, then
  * applies to later launches until changed; call it with nothing of this
  * library in flight.  Returns NVFP4_ERR_INVALID_ARG for unknown bits,
  * NVFP4_ERR_CUDA if the device cannot be reached. */
-enum { NVFP4_STALL_QUANTIZE = 1u, NVFP4_STALL_GEMM = 2u, NVFP4_LOSE_NORM = 16u };
+enum { NVFP4_STALL_QUANTIZE = 1u, NVFP4_STALL_GEMM = 2u, NVFP4_LOSE_NORM = 16u,
+       NVFP4_QUIT_GEMM = 32u };
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns);
 
 /* ---------------------------------------------------------------------- */

@@ -895,7 +895,7 @@ def nvfp4_residual_norm_bwd(dy: torch.Tensor | None, dh: torch.Tensor | None, x:
     return tuple(outs)
 
 
-STALL_QUANTIZE, STALL_GEMM, LOSE_NORM = 1, 2, 16
+STALL_QUANTIZE, STALL_GEMM, LOSE_NORM, QUIT_GEMM = 1, 2, 16, 32
 
 
 def debug_inject(stall_mask: int = 0, wait_limit_ns: int = 0):

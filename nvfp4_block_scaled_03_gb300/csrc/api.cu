@@ -76,7 +76,8 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream) {
 }
 
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
-  if (stall_mask & ~(uint32_t)(NVFP4_STALL_QUANTIZE | NVFP4_STALL_GEMM | NVFP4_LOSE_NORM))
+  if (stall_mask & ~(uint32_t)(NVFP4_STALL_QUANTIZE | NVFP4_STALL_GEMM | NVFP4_LOSE_NORM |
+                                NVFP4_QUIT_GEMM))
     return NVFP4_ERR_INVALID_ARG;
   const unsigned long long ns = wait_limit_ns ? wait_limit_ns : 2000000000ull;
   if (cudaDeviceSynchronize() != cudaSuccess) return NVFP4_ERR_CUDA;
@@ -86,7 +87,9 @@ nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
                               ((stall_mask & NVFP4_LOSE_NORM) ? 2u : 0u),
                           ns);
   if (st != NVFP4_OK) return st;
-  st = group_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
+  st = group_set_injection(((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u) |
+                               ((stall_mask & NVFP4_QUIT_GEMM) ? 2u : 0u),
+                           ns);
   if (st != NVFP4_OK) return st;
   return gemm_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
 }

@@ -15,8 +15,10 @@ namespace nvfp4 {
 
 static __device__ unsigned int g_gemm_error;
 // Failure injection for tests of the bounded waits (nvfp4_debug_inject):
-// while g_gemm_stall is set the producers of every GEMM kernel issue no
-// loads, and the pipeline waits give up after g_gemm_wait_ns.
+// while bit 0 of g_gemm_stall is set the producers of every GEMM kernel issue
+// no loads; while bit 1 is set the MMA threads give up before their first
+// wait, the producers' loads in flight.  The pipeline waits give up after
+// g_gemm_wait_ns.
 static __device__ unsigned int g_gemm_stall;
 static __device__ unsigned long long g_gemm_wait_ns = 2000000000ull;
 
@@ -89,6 +91,33 @@ NVFP4_DEV bool wait_bounded_pair(uint32_t bar, uint32_t parity, volatile int* ab
       return false;
     }
   }
+}
+
+// Injected quit: the caller gives up as if its first wait had run out.
+NVFP4_DEV bool quits_pair(volatile int* abort_flag, uint32_t peer_abort_addr) {
+  if (!(*reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) & 2u)) return false;
+  *abort_flag = 1;
+  st_cluster_u32(peer_abort_addr, 1u);
+  atomicCAS(&g_gemm_error, 0u, 0x52u);
+  return true;
+}
+
+// After an abort, once every role has stopped: until the last copy into each
+// of S stages has landed.  Fill f of `fills` went to stage f % S.
+template <int S>
+NVFP4_DEV void drain_stages(uint32_t bars, uint32_t fills) {
+  for (uint32_t s = 0; s < (uint32_t)S && s < fills; ++s)
+    wait_drain(bars + 8u * s, ((fills - 1 - s) / S) & 1u);
+}
+// The same for the full barriers of a pair, on which the leader counts the
+// copies of both CTAs (`bytes` a fill from each).  Their producers may have
+// stopped at different fills: of those that only the peer issued the arrival
+// is missing, of those that it did not issue its bytes.
+template <int S>
+NVFP4_DEV void drain_pair_stages(uint32_t bars, uint32_t mine, uint32_t peers, uint32_t bytes) {
+  for (uint32_t f = mine; f < peers; ++f) mbar_arrive_expect_tx(bars + 8u * (f % S), bytes);
+  for (uint32_t f = peers; f < mine; ++f) mbar_complete_tx(bars + 8u * (f % S), bytes);
+  drain_stages<S>(bars, max(mine, peers));
 }
 
 // Pulls the part of D that a row of a later tile's epilogue reads (128-byte

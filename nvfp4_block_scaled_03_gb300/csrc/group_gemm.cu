@@ -314,6 +314,10 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
   const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), crank ^ 1u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / (2 * SK), num_units = gridDim.x / (2 * SK);
+  // what the roles have in flight: stages that this CTA's producer filled, and
+  // (in the MMA threads) whether there are MMAs
+  volatile uint32_t* fills = reinterpret_cast<volatile uint32_t*>(smem + L::offMisc + 8);
+  bool issued = false;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -371,10 +375,10 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
       if (BN == 384) prefetch_tmap(&tmB2);
       prefetch_tmap(&tmSFA);
       prefetch_tmap(&tmSFB);
-      uint32_t s = 0, ph = 0;
+      uint32_t s = 0, ph = 0, count = 0;
       int g = 0;
       // injected stall: no loads, so every consumer's first wait runs out
-      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
+      bool ok = !(*reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) & 1u);
       for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         const int num_kb = (t.atoms + kAt - 1) / kAt;
@@ -386,6 +390,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
             ok = false;
             break;
           }
+          ++count;
           const uint32_t fb = mapa_shared(full_bar(s), first);
           const int a_x = (t.a_atom + kb * kAt) * (kAtom / 2);
           const int b_x = (t.b_atom + kb * kAt) * (kAtom / 2);
@@ -406,11 +411,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
           if (++s == S) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {  // give copies already issued time to land before exit
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
-      }
+      *fills = count;
     }
   } else if (warp <= L::kMmaWarps) {
     if (lane == 0 && leader) {
@@ -421,10 +422,9 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
       const uint32_t b_off = second ? 128u * kBKBytes : 0u;
       const uint32_t sfb_col = second ? 0u : L::kColB01;
       const uint32_t sfb_step = second ? 4u : 8u;  // columns per atom
-      const uint32_t my_drain = drain_bar + (second ? 8u : 0u);
       uint32_t s = 0, ph = 0, acc_ph = 0, it = 0;
       int g = 0;
-      bool ok = true, issued = false;
+      bool ok = !quits_pair(abort_flag, peer_abort);
       for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         if (t.atoms == 0) continue;
@@ -456,10 +456,6 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
         if (!ok) break;
         tc_commit_pair(acc_full, both);
         acc_ph ^= 1u;
-      }
-      if (!ok && issued) {
-        tc_commit_pair(my_drain, (uint16_t)(1u << first));
-        wait_drain(my_drain, 0);
       }
     }
   } else if (warp >= 4) {
@@ -636,7 +632,8 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
         }
       } else if (SK > 1 && parts > 1) {
         // every pair's MMAs are done behind the first barrier, and pair 0's ring
-        // with them; the sums have arrived behind the second
+        // with them; the sums have arrived behind the second.  A warp that gave up
+        // meets the others at both and reads nothing: its MMAs may still run.
         if (!wait_bounded_pair(acc_full, acc_ph, abort_flag, peer_abort, 0x33u)) ok = false;
         tc_fence_after();
         __syncwarp();
@@ -644,7 +641,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
         const int rows = (min(max(t.live - (int)rank * 128, 0), 128) + 31) / 32 * 32;
         const uint32_t line = (uint32_t)(q * 32 + lane) * L::kPartRow + (uint32_t)(h * kCols) * 4;
         const uint32_t tm = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * kCols);
-        if (part > 0 && q * 32 < rows) {
+        if (ok && part > 0 && q * 32 < rows) {
           const uint32_t to =
               mapa_shared(sbase + (uint32_t)((part - 1) * rows) * L::kPartRow + line, rank);
 #pragma unroll
@@ -661,7 +658,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
           }
         }
         cluster_sync();
-        if (part == 0 && mine) {
+        if (ok && part == 0 && mine) {
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             uint32_t r[32];
@@ -748,7 +745,27 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
 
   tc_fence_before();
   __syncthreads();
+  // a flag raised in one pair of a larger cluster holds for all of it
+  if (SK > 1 && *abort_flag && threadIdx.x < 2 * SK)
+    st_cluster_u32(mapa_shared(smem_u32(smem + L::offMisc + 4), threadIdx.x), 1u);
   cluster_sync();
+  if (*abort_flag) {
+    // given up, in every CTA of the cluster alike and with every role stopped:
+    // the copies and MMAs in flight finish before memory is handed on
+    if (threadIdx.x == 0) {
+      if (leader)
+        drain_pair_stages<S>(full_bar(0), *fills,
+                             ld_cluster_u32(mapa_shared(smem_u32(smem + L::offMisc + 8), crank ^ 1u)),
+                             L::kA + L::kB);
+      drain_stages<S>(scf_bar(0), *fills);
+    } else if (issued) {
+      const uint32_t my_drain = drain_bar + 8u * (warp - 1);
+      tc_commit_pair(my_drain, (uint16_t)(1u << first));
+      wait_drain(my_drain, 0);
+    }
+    __syncthreads();
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);

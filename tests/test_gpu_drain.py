@@ -51,3 +51,42 @@ def test_norm_that_gives_up_waits_for_its_rows(nv, rows, cols, wide):
     _gives_up_then_recovers(nv, nv.LOSE_NORM, lambda: nv.nvfp4_residual_norm_bwd(dy, dh, x, z, *w))
     _gives_up_then_recovers(nv, nv.LOSE_NORM,
                             lambda: nv.nvfp4_residual_norm_fwd(x, w_pre=w[0])[1:])
+
+
+def _groups(sizes):
+    import torch
+    off = [0]
+    for n in sizes:
+        off.append(off[-1] + (n + 127) // 128 * 128)
+    i = dict(dtype=torch.int32, device="cuda")
+    return torch.tensor(sizes, **i), torch.tensor(off, **i), off[-1]
+
+
+# fewer fills than stages; more, over several tiles; a tile shared by two and by four pairs
+@pytest.mark.parametrize("sizes,N,K,tile", [([100, 128], 256, 256, 3), ([100, 128], 384, 256, 6),
+                                            ([700, 0, 900, 300] * 6, 1280, 2048, 3),
+                                            ([700, 0, 900, 300] * 6, 1280, 2048, 6),
+                                            ([3], 1024, 4096, 0), ([3], 4096, 8192, 0),
+                                            ([3, 200], 4096, 8192, 0)])
+@pytest.mark.parametrize("plus_c", [False, True])
+def test_grouped_product_that_gives_up_waits_for_its_copies(nv, sizes, N, K, tile, plus_c):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(N)
+    s, o, rows = _groups(sizes)
+    A = nv.nvfp4_quantize(torch.randn(rows, K, generator=g, device="cuda"), nv.ROW_1X16)
+    B = nv.nvfp4_quantize(torch.randn(len(sizes) * N, K, generator=g, device="cuda"), nv.BLOCK_16X16)
+    C = torch.randn(rows, N, generator=g, device="cuda").bfloat16() if plus_c else None
+    _gives_up_then_recovers(nv, nv.QUIT_GEMM, lambda: [nv.nvfp4_group_gemm(
+        A, B, s, o, C_add=C, d_mode=nv.D_BF16_ADD_C if plus_c else nv.D_BF16, tile=tile)])
+
+
+@pytest.mark.parametrize("tile,fold", [(3, False), (6, False), (3, True)])
+def test_grouped_weight_gradient_that_gives_up_waits_for_its_copies(nv, tile, fold):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(tile)
+    s, o, rows = _groups([700, 0, 900, 64] * 6)
+    a, b = (nv.nvfp4_quantize(torch.randn(rows, n, generator=g, device="cuda"), nv.COL_1X16)
+            for n in (512, 1280))
+    mode = nv.D_F32_ACCUM if fold else nv.D_BF16
+    _gives_up_then_recovers(nv, nv.QUIT_GEMM,
+                            lambda: [nv.nvfp4_group_wgrad(a, b, s, o, d_mode=mode, tile=tile)])
