@@ -127,7 +127,7 @@ nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream);
  * a QUIT bit it gives up before its first wait, its loads in flight:
  *   NVFP4_LOSE_NORM       nvfp4_residual_norm_fwd / _bwd (rows to 8192 columns,
  *                         forward 16384: the others load no rows ahead)
- *   NVFP4_QUIT_GEMM       nvfp4_group_gemm, nvfp4_group_wgrad
+ *   NVFP4_QUIT_GEMM       every GEMM kernel
  * wait_limit_ns sets how long those kernels' pipeline waits last before they
  * give up (0: the default, 2 s); the waits that drain copies and MMAs
  * already issued keep their own 2 s limit.  Synchronises the device, then

@@ -87,11 +87,11 @@ nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
                               ((stall_mask & NVFP4_LOSE_NORM) ? 2u : 0u),
                           ns);
   if (st != NVFP4_OK) return st;
-  st = group_set_injection(((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u) |
-                               ((stall_mask & NVFP4_QUIT_GEMM) ? 2u : 0u),
-                           ns);
+  const unsigned int gemm = ((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u) |
+                            ((stall_mask & NVFP4_QUIT_GEMM) ? 2u : 0u);
+  st = group_set_injection(gemm, ns);
   if (st != NVFP4_OK) return st;
-  return gemm_set_injection((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u, ns);
+  return gemm_set_injection(gemm, ns);
 }
 
 nvfp4_status nvfp4_quantize_sizes(int64_t rows, int64_t cols, int32_t mode, uint32_t flags,

@@ -178,6 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int num_mu = args.num_m_blk;
   const int num_units = num_mu * args.num_n_blk;
   const int unit0 = blockIdx.x, unit_step = gridDim.x;
+  // what the roles have in flight: stages filled, and (in the MMA thread)
+  // whether there are MMAs
+  const uint32_t fills = sbase + L::offMisc + 8, inject = fills + 4;
+  bool issued = false;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -188,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(acc_empty, 8);
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
+    st_shared_u32(inject, injected());
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -205,11 +210,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------ producer
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmB);
-      uint32_t s = 0, ph = 0;
-      int armed[STAGES];
-      for (int i = 0; i < STAGES; ++i) armed[i] = -1;
+      uint32_t s = 0, ph = 0, count = 0;
       // injected stall: no loads, so the MMA thread's first wait runs out
-      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
+      bool ok = !(ld_shared_u32(inject) & kStall);
       for (int unit = unit0; ok && unit < num_units; unit += unit_step) {
         const int m_blk = unit % num_mu, n_blk = unit / num_mu;
         for (int kb = 0; kb < num_kb; ++kb) {
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < BN / 128; ++j) nb_valid += (n_blk * (BN / 128) + j) < args.nrb_b;
           const uint32_t sf_bytes = (uint32_t)natoms * 512u * (1u + (uint32_t)nb_valid);
           mbar_arrive_expect_tx(full_bar(s), L::kA + L::kB + sf_bytes);
-          armed[s] = (int)ph;
+          ++count;
           tma_load_2d(sbase + L::offA + s * L::kA, &tmA, full_bar(s), kb * BKB, m_blk * kBM);
           tma_load_2d(sbase + L::offB + s * L::kB, &tmB, full_bar(s), kb * BKB, n_blk * BN);
           bulk_load(sbase + L::offSFA + s * L::kSFA,
@@ -238,17 +241,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {  // let the copies already issued land before the CTA exits
-        for (int i = 0; i < STAGES; ++i)
-          if (armed[i] >= 0) wait_drain(full_bar(i), (uint32_t)armed[i]);
-      }
+      st_shared_u32(fills, count);
     }
   } else if (warp == 1) {
     if (lane == 0) {
       // ---------------------------------------------------------------- MMA
       constexpr uint32_t idesc = idesc_nvf4(kBM, BN);
       uint32_t s = 0, ph = 0, acc_ph = 0;
-      bool ok = true, issued = false;
+      bool ok = !quits(ld_shared_u32(inject), abort_flag);
       for (int unit = unit0; ok && unit < num_units; unit += unit_step) {
         if (!wait_bounded(acc_empty, acc_ph ^ 1u, abort_flag, 0x20u)) {
           ok = false;
@@ -287,10 +287,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(acc_full);
         acc_ph ^= 1u;
       }
-      if (!ok && issued) {  // MMAs in flight must finish before tensor memory is freed
-        tc_commit(drain_bar);
-        wait_drain(drain_bar, 0);
-      }
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -325,6 +321,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {  // given up, with every role stopped: what is in flight finishes
+    if (threadIdx.x == 0) {
+      drain_stages<STAGES>(full_bar(0), ld_shared_u32(fills));
+    } else if (issued) {
+      tc_commit(drain_bar);
+      wait_drain(drain_bar, 0);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -500,6 +505,9 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
   const int num_kb = (args.K + PairFmt<FMT>::kStageK - 1) / PairFmt<FMT>::kStageK;
   const int num_tiles = args.num_m_blk * args.num_n_blk;  // 256 x 256 tiles
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  // what the roles leave in flight (pair_leave): stages that this CTA's producer
+  // filled, and of warps 1 to 3 whether they issued MMAs or scale copies
+  const uint32_t fills = sbase + L::offMisc + 8, inject = fills + 4;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -512,6 +520,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
     mbar_init(acc_empty, 16);  // 8 epilogue warps in each CTA of the pair
     for (int d = 0; d <= kPairCopyWarps; ++d) mbar_init(drain_bar + 8u * d, 1);  // MMA, copy warps
     *abort_flag = 0;
+    st_shared_u32(inject, injected());
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -536,9 +545,9 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
       prefetch_tmap(&tmB);
       prefetch_tmap(&tmSFA);
       prefetch_tmap(&tmSFB);
-      uint32_t s = 0, ph = 0;
+      uint32_t s = 0, ph = 0, count = 0;
       // injected stall: no loads, so every consumer's first wait runs out
-      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
+      bool ok = !(ld_shared_u32(inject) & kStall);
       for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
         const int m_blk = tile % args.num_m_blk, n_blk = tile / args.num_m_blk;
         const int a_rb = m_blk * 2 + (int)rank;  // this CTA's 128-row block of A
@@ -548,6 +557,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
             ok = false;
             break;
           }
+          ++count;
           const uint32_t fb = mapa_shared(full_bar(s), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(s), L::kStageTx);
           tma_load_2d_pair(sbase + L::offA + s * L::kA, &tmA, fb, kb * kBKBytes, a_rb * 128);
@@ -573,11 +583,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {  // give copies already issued time to land before exit
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
-      }
+      st_shared_u32(fills, count);
     }
   } else if (ST && warp >= 4) {
     // ------------------------------------------------------------ scale warps
@@ -641,7 +647,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
       // cw modulo the number of copy warps
       const int cw = warp - 2;
       uint32_t s = 0, ph = 0;
-      bool ok = true, issued = false;
+      bool ok = true;
       for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!wait_bounded_pair(full_bar(s), ph, abort_flag, peer_abort, 0x24u)) {
@@ -660,7 +666,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
             if ((kAt + j) % kPairCopyWarps == cw)
               tc_cp_pair_128x256b(sfb_t + 8 * j, smem_desc_sf_image(sb + j * 4096));
           }
-          issued = true;
+          st_shared_u8(inject + warp, 1u);
           // the MMA thread may issue as soon as these copies are issued: the
           // fence before this arrive and the MMA thread's fence after its wait
           // order its MMAs behind them in the tensor pipe
@@ -669,10 +675,6 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok && issued) {  // copies in flight must land before tensor memory is freed
-        tc_commit_pair(drain_bar + 8u * (1 + cw), 1);
-        wait_drain(drain_bar + 8u * (1 + cw), 0);
-      }
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
@@ -680,7 +682,7 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
       constexpr uint32_t idesc = FMT == kFmtNVF4 ? idesc_nvf4(256, kPairBN)
                                  : idesc_mx(256, kPairBN, FMT == kFmtMXF8 ? 0u : 1u);
       uint32_t s = 0, ph = 0, acc_ph = 0;
-      bool ok = true, issued = false;
+      bool ok = !quits_pair(ld_shared_u32(inject), abort_flag, peer_abort);
       for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
         if (!wait_bounded_pair(acc_empty, acc_ph ^ 1u, abort_flag, peer_abort, 0x22u)) {
           ok = false;
@@ -712,17 +714,13 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
                                 idesc | (sfid << 4) | (sfid << 29), sfa_t + 4 * atom,
                                 sfb_t + 8 * atom, (kb | j) != 0 ? 1u : 0u);
           }
-          issued = true;
+          st_shared_u8(inject + warp, 1u);
           tc_commit_pair(empty_bar(s), 3);
           if (++s == STAGES) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         tc_commit_pair(acc_full, 3);
         acc_ph ^= 1u;
-      }
-      if (!ok && issued) {
-        tc_commit_pair(drain_bar, 1);
-        wait_drain(drain_bar, 0);
       }
     }
   }
@@ -814,11 +812,10 @@ __launch_bounds__(PairRoles<!IMG>::kThreads, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();
+  pair_leave<L, STAGES, 2, ST>(L::kStageTx / 2);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    tmem_dealloc_pair(ld_shared_u32(sbase + L::offMisc), kTmemCols);
   }
 }
 
@@ -899,6 +896,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
   const int num_kb = (args.K + 255) / 256;
   const int num_tiles = args.num_m_blk * args.num_n_blk;  // 256 x 384 tiles
   const int pair = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  // what the roles leave in flight (pair_leave): stages that this CTA's producer
+  // filled, and of warps 1 to 3 whether they issued MMAs or scale copies
+  const uint32_t fills = sbase + L::offMisc + 8, inject = fills + 4;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -912,6 +912,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
     mbar_init(drain_bar, 1);
     mbar_init(drain_bar + 8, 1);
     *abort_flag = 0;
+    st_shared_u32(inject, injected());
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -935,9 +936,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
       prefetch_tmap(&tmB2);
       prefetch_tmap(&tmSFA);
       prefetch_tmap(&tmSFB);
-      uint32_t s = 0, ph = 0;
+      uint32_t s = 0, ph = 0, count = 0;
       // injected stall: no loads, so every consumer's first wait runs out
-      bool ok = *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) == 0u;
+      bool ok = !(ld_shared_u32(inject) & kStall);
       for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
         const int m_blk = tile % args.num_m_blk, n_blk = tile / args.num_m_blk;
         const int a_rb = m_blk * 2 + (int)rank;  // this CTA's 128-row block of A
@@ -947,6 +948,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
             ok = false;
             break;
           }
+          ++count;
           const uint32_t fb = mapa_shared(full_bar(s), 0);
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (L::kA + L::kB));
           tma_load_2d_pair(sbase + L::offA + s * L::kA, &tmA, fb, kb * kBKBytes, a_rb * 128);
@@ -965,11 +967,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
           if (++s == S) { s = 0; ph ^= 1u; }
         }
       }
-      if (!ok) {  // give copies already issued time to land before exit
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
-      }
+      st_shared_u32(fills, count);
     }
   } else if (warp == 1 || warp == 2) {
     if (lane == 0 && leader) {
@@ -980,9 +978,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
       const uint32_t b_off = second ? 128u * kBKBytes : 0u;
       const uint32_t sfb_col = second ? L::kColB2 : L::kColB01;
       const uint32_t sfb_step = second ? 4u : 8u;  // columns per atom
-      const uint32_t my_drain = drain_bar + (second ? 8u : 0u);
       uint32_t s = 0, ph = 0, acc_ph = 0, it = 0;
-      bool ok = true, issued = false;
+      bool ok = !quits_pair(ld_shared_u32(inject), abort_flag, peer_abort);
       for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
         if (!wait_bounded_pair(acc_empty, acc_ph ^ 1u, abort_flag, peer_abort, 0x22u)) {
           ok = false;
@@ -1004,17 +1001,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
             tc_mma_pair_nvf4(d_tmem, smem_desc_sw128(a0 + 32 * j), smem_desc_sw128(b0 + 32 * j),
                              idesc, slot + L::kColA + 4 * j, slot + sfb_col + sfb_step * j,
                              (kb | j) != 0 ? 1u : 0u);
-          issued = true;
+          st_shared_u8(inject + warp, 1u);
           tc_commit_pair(empty_bar(s), 3);
           if (++s == S) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
         tc_commit_pair(acc_full, 3);
         acc_ph ^= 1u;
-      }
-      if (!ok && issued) {
-        tc_commit_pair(my_drain, 1);
-        wait_drain(my_drain, 0);
       }
     }
   } else if (warp >= 4) {
@@ -1125,11 +1118,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Pair384Smem::kThread
   }
 
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();
+  pair_leave<L, S, 2, true>(L::kA + L::kB);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    tmem_dealloc_pair(ld_shared_u32(sbase + L::offMisc), kTmemCols);
   }
 }
 

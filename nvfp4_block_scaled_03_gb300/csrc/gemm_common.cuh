@@ -93,12 +93,22 @@ NVFP4_DEV bool wait_bounded_pair(uint32_t bar, uint32_t parity, volatile int* ab
   }
 }
 
+// The injection switches, which thread 0 of a CTA puts into shared memory before
+// the roles start.
+enum : uint32_t { kStall = 1, kQuit = 2 };
+NVFP4_DEV uint32_t injected() {
+  return *reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) & 3u;
+}
 // Injected quit: the caller gives up as if its first wait had run out.
-NVFP4_DEV bool quits_pair(volatile int* abort_flag, uint32_t peer_abort_addr) {
-  if (!(*reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) & 2u)) return false;
+NVFP4_DEV bool quits(uint32_t injected, volatile int* abort_flag) {
+  if (!(injected & kQuit)) return false;
   *abort_flag = 1;
-  st_cluster_u32(peer_abort_addr, 1u);
   atomicCAS(&g_gemm_error, 0u, 0x52u);
+  return true;
+}
+NVFP4_DEV bool quits_pair(uint32_t injected, volatile int* abort_flag, uint32_t peer_abort_addr) {
+  if (!quits(injected, abort_flag)) return false;
+  st_cluster_u32(peer_abort_addr, 1u);
   return true;
 }
 
@@ -106,6 +116,7 @@ NVFP4_DEV bool quits_pair(volatile int* abort_flag, uint32_t peer_abort_addr) {
 // of S stages has landed.  Fill f of `fills` went to stage f % S.
 template <int S>
 NVFP4_DEV void drain_stages(uint32_t bars, uint32_t fills) {
+#pragma unroll 1
   for (uint32_t s = 0; s < (uint32_t)S && s < fills; ++s)
     wait_drain(bars + 8u * s, ((fills - 1 - s) / S) & 1u);
 }
@@ -115,9 +126,50 @@ NVFP4_DEV void drain_stages(uint32_t bars, uint32_t fills) {
 // is missing, of those that it did not issue its bytes.
 template <int S>
 NVFP4_DEV void drain_pair_stages(uint32_t bars, uint32_t mine, uint32_t peers, uint32_t bytes) {
+#pragma unroll 1
   for (uint32_t f = mine; f < peers; ++f) mbar_arrive_expect_tx(bars + 8u * (f % S), bytes);
+#pragma unroll 1
   for (uint32_t f = peers; f < mine; ++f) mbar_complete_tx(bars + 8u * (f % S), bytes);
   drain_stages<S>(bars, max(mine, peers));
+}
+
+// The last barriers of a pair kernel, behind which it frees its tensor memory.  If
+// it has given up, its copies and MMAs in flight finish first: every role of
+// every CTA in the cluster has stopped by then.  L lays out the shared memory:
+// at offMisc + 4 the abort flag, + 8 the stages that this CTA's producer filled,
+// + 12 a byte for each of warps 1 to 3 (behind the injection switches) that says
+// whether it issued MMAs or scale copies; from offBar on S full, empty,
+// scales-ready and scales-landed barriers, two of the accumulator, the drains'.
+// `bytes`: what a fill by one CTA puts on the leader's full barrier.  SCALES: its
+// scales land on a barrier of its own.  (The addresses are computed anew: kept
+// through the kernel they cost the epilogue registers.)
+template <class L, int S, int CLUSTER, bool SCALES>
+NVFP4_DEV void pair_leave(uint32_t bytes) {
+  extern __shared__ uint8_t smem_raw[];
+  uint32_t base = smem_u32(smem_raw);
+  asm volatile("" : "+r"(base));
+  base = (base + 1023u) & ~1023u;
+  const uint32_t misc = base + L::offMisc, bars = base + L::offBar;
+  __syncthreads();
+  // a flag raised in one pair of a larger cluster holds for all of it
+  if (CLUSTER > 2 && ld_shared_u32(misc + 4) && threadIdx.x < CLUSTER)
+    st_cluster_u32(mapa_shared(misc + 4, threadIdx.x), 1u);
+  cluster_sync();
+  if (!ld_shared_u32(misc + 4)) return;
+  const uint32_t crank = cluster_ctarank(), warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    const uint32_t fills = ld_shared_u32(misc + 8);
+    if ((crank & 1u) == 0)
+      drain_pair_stages<S>(bars, fills, ld_cluster_u32(mapa_shared(misc + 8, crank ^ 1u)), bytes);
+    if (SCALES) drain_stages<S>(bars + 8u * 3 * S, fills);
+  } else if ((threadIdx.x & 31) == 0 && warp <= 3 &&
+             (ld_shared_u32(misc + 12) >> (8 * warp) & 0xFFu)) {
+    const uint32_t bar = bars + 8u * (4 * S + 2 + warp - 1);
+    tc_commit_pair(bar, (uint16_t)(1u << crank));
+    wait_drain(bar, 0);
+  }
+  __syncthreads();
+  cluster_sync();
 }
 
 // Pulls the part of D that a row of a later tile's epilogue reads (128-byte

@@ -314,10 +314,9 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
   const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), crank ^ 1u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int unit = blockIdx.x / (2 * SK), num_units = gridDim.x / (2 * SK);
-  // what the roles have in flight: stages that this CTA's producer filled, and
-  // (in the MMA threads) whether there are MMAs
-  volatile uint32_t* fills = reinterpret_cast<volatile uint32_t*>(smem + L::offMisc + 8);
-  bool issued = false;
+  // what the roles leave in flight (pair_leave): stages that this CTA's producer
+  // filled, and of the MMA warps whether they issued any
+  const uint32_t fills = sbase + L::offMisc + 8, inject = fills + 4;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -332,6 +331,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
     if (L::kAddC)
       for (int w = 0; w < 8; ++w) mbar_init(c_bar + 8u * w, 1);
     *abort_flag = 0;
+    st_shared_u32(inject, injected());
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -378,7 +378,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
       uint32_t s = 0, ph = 0, count = 0;
       int g = 0;
       // injected stall: no loads, so every consumer's first wait runs out
-      bool ok = !(*reinterpret_cast<volatile unsigned int*>(&g_gemm_stall) & 1u);
+      bool ok = !(ld_shared_u32(inject) & kStall);
       for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         const int num_kb = (t.atoms + kAt - 1) / kAt;
@@ -411,7 +411,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
           if (++s == S) { s = 0; ph ^= 1u; }
         }
       }
-      *fills = count;
+      st_shared_u32(fills, count);
     }
   } else if (warp <= L::kMmaWarps) {
     if (lane == 0 && leader) {
@@ -424,7 +424,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
       const uint32_t sfb_step = second ? 4u : 8u;  // columns per atom
       uint32_t s = 0, ph = 0, acc_ph = 0, it = 0;
       int g = 0;
-      bool ok = !quits_pair(abort_flag, peer_abort);
+      bool ok = !quits_pair(ld_shared_u32(inject), abort_flag, peer_abort);
       for (int tile = tile0; ok && tile < tiles; tile += num_units) {
         const Tile t = tile_at<KIND, BN>(tile, g, table, args);
         if (t.atoms == 0) continue;
@@ -449,7 +449,7 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
             tc_mma_pair_nvf4(d_tmem, smem_desc_sw128(a0 + 32 * j), smem_desc_sw128(b0 + 32 * j),
                              idesc, slot + L::kColA + 4 * j, slot + sfb_col + sfb_step * j,
                              kb != k_begin(num_kb) || j != 0 ? 1u : 0u);
-          issued = true;
+          st_shared_u8(inject + warp, 1u);
           tc_commit_pair(empty_bar(s), both);
           if (++s == S) { s = 0; ph ^= 1u; }
         }
@@ -744,31 +744,10 @@ __global__ void __cluster_dims__(2 * SK, 1, 1) __launch_bounds__(PairGroup<BN, D
   }
 
   tc_fence_before();
-  __syncthreads();
-  // a flag raised in one pair of a larger cluster holds for all of it
-  if (SK > 1 && *abort_flag && threadIdx.x < 2 * SK)
-    st_cluster_u32(mapa_shared(smem_u32(smem + L::offMisc + 4), threadIdx.x), 1u);
-  cluster_sync();
-  if (*abort_flag) {
-    // given up, in every CTA of the cluster alike and with every role stopped:
-    // the copies and MMAs in flight finish before memory is handed on
-    if (threadIdx.x == 0) {
-      if (leader)
-        drain_pair_stages<S>(full_bar(0), *fills,
-                             ld_cluster_u32(mapa_shared(smem_u32(smem + L::offMisc + 8), crank ^ 1u)),
-                             L::kA + L::kB);
-      drain_stages<S>(scf_bar(0), *fills);
-    } else if (issued) {
-      const uint32_t my_drain = drain_bar + 8u * (warp - 1);
-      tc_commit_pair(my_drain, (uint16_t)(1u << first));
-      wait_drain(my_drain, 0);
-    }
-    __syncthreads();
-    cluster_sync();
-  }
+  pair_leave<L, S, 2 * SK, true>(L::kA + L::kB);
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, kTmemCols);
+    tmem_dealloc_pair(ld_shared_u32(sbase + L::offMisc), kTmemCols);
   }
 }
 

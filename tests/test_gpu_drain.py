@@ -90,3 +90,35 @@ def test_grouped_weight_gradient_that_gives_up_waits_for_its_copies(nv, tile, fo
     mode = nv.D_F32_ACCUM if fold else nv.D_BF16
     _gives_up_then_recovers(nv, nv.QUIT_GEMM,
                             lambda: [nv.nvfp4_group_wgrad(a, b, s, o, d_mode=mode, tile=tile)])
+
+
+# the single-SM tiles, then the pairs; fewer fills than stages, and several tiles
+@pytest.mark.parametrize("tile", [1, 2, 5, 3, 6])
+@pytest.mark.parametrize("M,N,K", [(128, 256, 512), (4096, 8192, 2048)])
+@pytest.mark.parametrize("fold", [False, True])
+def test_gemm_that_gives_up_waits_for_its_copies(nv, tile, M, N, K, fold):
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(tile)
+    A = nv.nvfp4_quantize(torch.randn(M, K, generator=g, device="cuda"), nv.ROW_1X16)
+    B = nv.nvfp4_quantize(torch.randn(N, K, generator=g, device="cuda"), nv.BLOCK_16X16)
+    mode = nv.D_F32_ACCUM if fold else nv.D_BF16
+
+    def call():
+        out = torch.zeros(M, N, device="cuda") if fold else None
+        return [nv.nvfp4_gemm(A, B, tile=tile, d_mode=mode, out=out)]
+
+    _gives_up_then_recovers(nv, nv.QUIT_GEMM, call)
+
+
+@pytest.mark.parametrize("fmt", ["MXFP4", "MXFP8"])
+@pytest.mark.parametrize("M,N,K", [(256, 256, 512), (2048, 8192, 2048)])
+def test_mx_gemm_that_gives_up_waits_for_its_copies(nv, fmt, M, N, K):
+    import torch
+    f = getattr(nv, fmt)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    ops = []
+    for n in (M, N):
+        sw = torch.zeros(n // 128 * (K // 128) * 512, dtype=torch.uint8, device="cuda")
+        x = torch.randn(n, K, generator=g, device="cuda").bfloat16()
+        ops += [nv.nvfp4_mx_quantize(x, nv.MX_ROW, f, scales_sw=sw)[0], sw]
+    _gives_up_then_recovers(nv, nv.QUIT_GEMM, lambda: [nv.nvfp4_mx_gemm(*ops, f, M, N, K)])
