@@ -74,7 +74,13 @@ enum {
   NVFP4_RHT = 1u,        /* 16-point random Hadamard transform along the blocks (bullet 3) */
   NVFP4_SR = 2u,         /* stochastic rounding of the elements (bullet 5); else RNE       */
   NVFP4_EMIT_T = 4u,     /* BLOCK_16X16 only: also write the transposed operand            */
-  NVFP4_AMAX_GIVEN = 8u  /* use *out->amax (device, set by the caller) as the tensor amax   */
+  NVFP4_AMAX_GIVEN = 8u, /* use *out->amax (device, set by the caller) as the tensor amax   */
+  /* with NVFP4_SR: `offset` is the device address (8-byte aligned) of a uint64
+   * that holds the offset, read when the kernel runs.  A captured CUDA graph
+   * keeps the arguments of its calls, so with a plain offset every replay
+   * rounds with the same random numbers; with this one a replay takes what the
+   * caller has advanced the counter to. */
+  NVFP4_OFFSET_DEVICE = 32u
 };
 
 /* A quantised NVFP4 operand.  The caller fills the pointers; nvfp4_quantize
@@ -208,7 +214,8 @@ nvfp4_status nvfp4_amax(const void* x, int32_t in_dtype, int64_t rows, int64_t c
  *   row_out: nvfp4_quantize(x, ROW_1X16, row_flags, seed, row_offset)
  *   col_out: nvfp4_quantize(x, COL_1X16, col_flags, seed, col_offset)
  * row_flags: NVFP4_AMAX_GIVEN, optionally | NVFP4_SR; col_flags:
- * NVFP4_AMAX_GIVEN, optionally | NVFP4_RHT | NVFP4_SR.  Both amaxes are given
+ * NVFP4_AMAX_GIVEN, optionally | NVFP4_RHT | NVFP4_SR (each SR also with
+ * | NVFP4_OFFSET_DEVICE).  Both amaxes are given
  * (*row_out->amax = max |x|, *col_out->amax = the column operand's amax, e.g.
  * both from one nvfp4_amax call), so nothing needs a workspace.  Shapes:
  * rows % 16 == 0, cols % 16 == 0.  x, the codes and scales buffers 16-byte
@@ -381,7 +388,8 @@ typedef struct nvfp4_mlp_params {
   const float* Wu;
   const float* Wd;
   uint64_t seed;   /* RHT signs and SR key                           */
-  uint64_t step;   /* SR counter offsets 8*step + 0..5 (per tensor)  */
+  uint64_t step;   /* SR counter offsets 8*step + 0..5 (per tensor); a  *
+                    * captured graph keeps it                          */
   uint32_t flags;  /* NVFP4_RHT | NVFP4_AMAX_GIVEN, or 0             */
 } nvfp4_mlp_params;
 

@@ -22,7 +22,7 @@ OK, ERR_INVALID_ARG, ERR_SHAPE, ERR_ALIGN, ERR_ARCH, ERR_WORKSPACE, ERR_CUDA, \
 # enums and flags
 IN_BF16, IN_FP32 = 0, 1
 ROW_1X16, COL_1X16, BLOCK_16X16 = 0, 1, 2
-RHT, SR, EMIT_T, AMAX_GIVEN = 1, 2, 4, 8
+RHT, SR, EMIT_T, AMAX_GIVEN, OFFSET_DEVICE = 1, 2, 4, 8, 32
 D_BF16, D_F32_ACCUM, D_BF16_ADD_C = 0, 1, 2
 MXFP4, MXFP8 = 0, 1
 MX_ROW, MX_COL = 0, 1
@@ -196,10 +196,22 @@ def _workspace(nbytes, device):
     return ws
 
 
-def nvfp4_quantize(x: torch.Tensor, mode: int, flags: int = 0, seed: int = 0, offset: int = 0,
-                   out: QTensor | None = None, workspace: torch.Tensor | None = None,
+def _offset(flags: int, offset: int | torch.Tensor):
+    """Flags and offset argument of a quantiser: a number, or a device counter."""
+    if not isinstance(offset, torch.Tensor):
+        return flags, offset
+    if not (offset.is_cuda and offset.dtype is torch.int64 and offset.numel() == 1):
+        raise ValueError("a device offset must be a 1-element int64 CUDA tensor")
+    return flags | OFFSET_DEVICE, offset.data_ptr()
+
+
+def nvfp4_quantize(x: torch.Tensor, mode: int, flags: int = 0, seed: int = 0,
+                   offset: int | torch.Tensor = 0, out: QTensor | None = None,
+                   workspace: torch.Tensor | None = None,
                    amax: float | torch.Tensor | None = None, stream=None) -> QTensor:
-    """Quantise a 2-D bf16/fp32 CUDA tensor (see nvfp4_quantize in nvfp4.h)."""
+    """Quantise a 2-D bf16/fp32 CUDA tensor (see nvfp4_quantize in nvfp4.h).  An
+    `offset` on the device (a 1-element int64 tensor) is read when the kernel
+    runs, so that replays of a captured graph need not repeat its rounding."""
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D tensor with unit column stride")
     if x.dtype == torch.bfloat16:
@@ -218,6 +230,7 @@ def nvfp4_quantize(x: torch.Tensor, mode: int, flags: int = 0, seed: int = 0, of
     _, _, _, wsb = quantize_sizes(rows, cols, mode, flags)
     if workspace is None and wsb:
         workspace = _workspace(wsb, x.device)
+    flags, offset = _offset(flags, offset)
     _check(lib.nvfp4_quantize(x.data_ptr(), dt, rows, cols, x.stride(0), mode, flags, seed, offset,
                               C.byref(out.desc), _ptr(workspace),
                               0 if workspace is None else workspace.numel(), _stream(stream)),
@@ -248,14 +261,16 @@ def nvfp4_amax(x: torch.Tensor, amax_plain: torch.Tensor | None = None,
 
 
 def nvfp4_quantize_rowcol(x: torch.Tensor, row_flags: int = 0, col_flags: int = 0, seed: int = 0,
-                          row_offset: int = 0, col_offset: int = 0,
+                          row_offset: int | torch.Tensor = 0,
+                          col_offset: int | torch.Tensor = 0,
                           row_out: QTensor | None = None, col_out: QTensor | None = None,
                           amax_row: torch.Tensor | None = None, amax_col: torch.Tensor | None = None,
                           stream=None):
     """Row-wise and column-wise quantisation of a bf16 x from one read (see
     nvfp4_quantize_rowcol in nvfp4.h).  The two amaxes are given: either
     already in row_out.amax / col_out.amax, or as 1-element float32 CUDA
-    tensors amax_row / amax_col (copied there).  Returns (row_out, col_out)."""
+    tensors amax_row / amax_col (copied there).  The offsets may be on the
+    device, as nvfp4_quantize's.  Returns (row_out, col_out)."""
     if x.dim() != 2 or x.stride(1) != 1 or x.dtype != torch.bfloat16:
         raise ValueError("x must be a 2-D bf16 tensor with unit column stride")
     rows, cols = x.shape
@@ -269,6 +284,8 @@ def nvfp4_quantize_rowcol(x: torch.Tensor, row_flags: int = 0, col_flags: int = 
         row_out.amax.copy_(amax_row.reshape(1))
     if amax_col is not None:
         col_out.amax.copy_(amax_col.reshape(1))
+    row_flags, row_offset = _offset(row_flags, row_offset)
+    col_flags, col_offset = _offset(col_flags, col_offset)
     _check(lib.nvfp4_quantize_rowcol(x.data_ptr(), IN_BF16, rows, cols, x.stride(0), row_flags,
                                      col_flags, seed, row_offset, col_offset, C.byref(row_out.desc),
                                      C.byref(col_out.desc), _stream(stream)),
@@ -277,7 +294,7 @@ def nvfp4_quantize_rowcol(x: torch.Tensor, row_flags: int = 0, col_flags: int = 
 
 
 def nvfp4_quantize_noalloc(x: torch.Tensor, mode: int, flags: int = 0, seed: int = 0,
-                           offset: int = 0, out: QTensor | None = None, stream=None) -> QTensor:
+                           offset: int | torch.Tensor = 0, out: QTensor | None = None, stream=None) -> QTensor:
     """nvfp4_quantize without a workspace: scratch lives inside the library
     (see nvfp4_quantize_noalloc in nvfp4.h for who needs this and its limits)."""
     if x.dim() != 2 or x.stride(1) != 1:
@@ -288,6 +305,7 @@ def nvfp4_quantize_noalloc(x: torch.Tensor, mode: int, flags: int = 0, seed: int
     rows, cols = x.shape
     if out is None:
         out = alloc_qtensor(rows, cols, mode, flags, device=x.device)
+    flags, offset = _offset(flags, offset)
     _check(lib.nvfp4_quantize_noalloc(x.data_ptr(), dt, rows, cols, x.stride(0), mode, flags, seed,
                                       offset, C.byref(out.desc), _stream(stream)),
            "nvfp4_quantize_noalloc")

@@ -62,9 +62,9 @@ NVFP4_DEV uint4 philox4x32_10_rk(uint4 c, const PhiloxKeys& rk) {
 
 // Stochastic-rounding words for the 4 consecutive output elements starting at
 // linear index idx4 (a multiple of 4): counter (idx4/4, stream 0, offset).
-NVFP4_DEV uint4 sr_words(const PhiloxKeys& rk, uint64_t offset, uint64_t idx4) {
+NVFP4_DEV uint4 sr_words(const PhiloxKeys& rk, uint32_t offset, uint64_t idx4) {
   const uint64_t g = idx4 >> 2;
-  return philox4x32_10_rk(make_uint4((uint32_t)g, (uint32_t)(g >> 32), 0u, (uint32_t)offset), rk);
+  return philox4x32_10_rk(make_uint4((uint32_t)g, (uint32_t)(g >> 32), 0u, offset), rk);
 }
 
 // 16 RHT sign bits (bit i set -> sign -1): word 0 of counter (0, 0, 1, 0).

@@ -227,6 +227,13 @@ NVFP4_DEV float tensor_s_enc(const QParams& p, float* red) {
   return s_enc;
 }
 
+// The stochastic rounding's offset: the call's own, or with NVFP4_OFFSET_DEVICE
+// what the address in its place holds now.
+NVFP4_DEV uint32_t sr_offset(uint32_t flags, uint64_t offset) {
+  return (uint32_t)(flags & NVFP4_OFFSET_DEVICE ? *reinterpret_cast<const uint64_t*>(offset)
+                                                : offset);
+}
+
 // ---- random Hadamard transform of a block split over a lane pair --------------
 // Transform of a block split over a lane pair (lane^1): this thread holds
 // elements half*8 .. half*8+7.  Stages h = 1, 2, 4 are local; h = 8 pairs
@@ -367,6 +374,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
   float* tab = reinterpret_cast<float*>(smem + L::offTab);
   q_init<G, L>(smem);
   griddep_wait();
+  [[maybe_unused]] const uint32_t offset = SR ? sr_offset(p.flags, p.offset) : 0u;
   const float s_enc = tensor_s_enc(p, reinterpret_cast<float*>(smem + L::offRed));
   fill_enc_table(tab, s_enc);  // ends with a CTA barrier
 
@@ -409,8 +417,8 @@ __global__ void __launch_bounds__(kQThreads, 2)
       uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
       if (SR && ok) {
         const uint64_t idx = (uint64_t)(r * C + c0);
-        w0 = sr_words(p.rk, p.offset, idx);
-        w1 = sr_words(p.rk, p.offset, idx + 4);
+        w0 = sr_words(p.rk, offset, idx);
+        w1 = sr_words(p.rk, offset, idx + 4);
       }
       const uint32_t packed = encode8<SR>(v[i], enc, w0, w1);
       if (ok) *reinterpret_cast<uint32_t*>(p.codes + r * (C / 2) + c0 / 2) = packed;
@@ -430,7 +438,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
 template <bool RHT, bool SR>
 NVFP4_DEV void col_block(float (&v)[16], int ol, int j, bool rows_ok, int64_t c0, int64_t r0,
                          int64_t R, int64_t C, float s_enc, const float* tab,
-                         const PhiloxKeys& rk, uint64_t offset, uint32_t* out_s, uint8_t* atom) {
+                         const PhiloxKeys& rk, uint32_t offset, uint32_t* out_s, uint8_t* atom) {
   const int64_t col = c0 + ol;
   const bool ok = rows_ok && col < C;
   if (RHT) rht16_signed_block(v);
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
   float* tab = reinterpret_cast<float*>(smem + L::offTab);
   q_init<G, L>(smem);
   griddep_wait();
+  [[maybe_unused]] const uint32_t offset = SR ? sr_offset(p.flags, p.offset) : 0u;
   const float s_enc = tensor_s_enc(p, reinterpret_cast<float*>(smem + L::offRed));
   fill_enc_table(tab, s_enc);
 
@@ -518,9 +527,9 @@ __global__ void __launch_bounds__(kQThreads, 2)
     uint32_t* out_s = reinterpret_cast<uint32_t*>(smem + L::offExtra + buf * kBuf);
     uint8_t* atom = smem + L::offExtra + buf * kBuf + kOutBytes;
     const bool rows_ok = r0 + 16 * j < R;
-    col_block<RHT, SR>(va, 2 * cp, j, rows_ok, c0, r0, R, C, s_enc, tab, p.rk, p.offset,
+    col_block<RHT, SR>(va, 2 * cp, j, rows_ok, c0, r0, R, C, s_enc, tab, p.rk, offset,
                        out_s, atom);
-    col_block<RHT, SR>(vb, 2 * cp + 1, j, rows_ok, c0, r0, R, C, s_enc, tab, p.rk, p.offset,
+    col_block<RHT, SR>(vb, 2 * cp + 1, j, rows_ok, c0, r0, R, C, s_enc, tab, p.rk, offset,
                        out_s, atom);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_out + 8 * buf);
@@ -562,6 +571,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
 struct QRowColParams {
   int64_t rows, cols;
   uint64_t seed, row_offset, col_offset;
+  uint32_t row_flags, col_flags;
   uint8_t* row_codes;
   uint8_t* row_scales;
   uint8_t* col_codes;
@@ -594,6 +604,8 @@ __global__ void __launch_bounds__(kQThreads, 2)
   float* tab_r = reinterpret_cast<float*>(smem + L::offExtra + 2 * kBuf);
   q_init<G, L>(smem);
   griddep_wait();
+  const uint32_t row_offset = SRR ? sr_offset(p.row_flags, p.row_offset) : 0u;
+  const uint32_t col_offset = SRC ? sr_offset(p.col_flags, p.col_offset) : 0u;
   const float s_enc_r = per_tensor_s_enc(*p.row_amax), s_enc_c = per_tensor_s_enc(*p.col_amax);
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *p.row_s_dec = __fdiv_rn(1.0f, s_enc_r);
@@ -649,10 +661,10 @@ __global__ void __launch_bounds__(kQThreads, 2)
     uint32_t* out_s = reinterpret_cast<uint32_t*>(smem + L::offExtra + buf * kBuf);
     uint8_t* atom = smem + L::offExtra + buf * kBuf + kOutBytes;
     const bool rows_ok = r0 + 16 * j < R;
-    col_block<RHT, SRC>(va, 2 * cp, j, rows_ok, c0, r0, R, C, s_enc_c, tab_c, p.rk, p.col_offset,
+    col_block<RHT, SRC>(va, 2 * cp, j, rows_ok, c0, r0, R, C, s_enc_c, tab_c, p.rk, col_offset,
                         out_s, atom);
     col_block<RHT, SRC>(vb, 2 * cp + 1, j, rows_ok, c0, r0, R, C, s_enc_c, tab_c, p.rk,
-                        p.col_offset, out_s, atom);
+                        col_offset, out_s, atom);
     // ---- row operand: row r, columns cb .. cb + 31 (two blocks)
     {
       float vr[4][8];
@@ -687,10 +699,10 @@ __global__ void __launch_bounds__(kQThreads, 2)
         uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0, w2 = w0, w3 = w0;
         if (SRR && ok) {
           const uint64_t idx = (uint64_t)(r * C + cb + 16 * b);
-          w0 = sr_words(p.rk, p.row_offset, idx);
-          w1 = sr_words(p.rk, p.row_offset, idx + 4);
-          w2 = sr_words(p.rk, p.row_offset, idx + 8);
-          w3 = sr_words(p.rk, p.row_offset, idx + 12);
+          w0 = sr_words(p.rk, row_offset, idx);
+          w1 = sr_words(p.rk, row_offset, idx + 4);
+          w2 = sr_words(p.rk, row_offset, idx + 8);
+          w3 = sr_words(p.rk, row_offset, idx + 12);
         }
         words[2 * b] = encode8<SRR>(vr[2 * b], enc, w0, w1);
         words[2 * b + 1] = encode8<SRR>(vr[2 * b + 1], enc, w2, w3);
@@ -761,6 +773,7 @@ __global__ void __launch_bounds__(kQThreads, 2)
   float* tab = reinterpret_cast<float*>(smem + L::offTab);
   q_init<G, L>(smem);
   griddep_wait();
+  [[maybe_unused]] const uint32_t offset = SR ? sr_offset(p.flags, p.offset) : 0u;
   const float s_enc = tensor_s_enc(p, reinterpret_cast<float*>(smem + L::offRed));
   fill_enc_table(tab, s_enc);
 
@@ -818,8 +831,8 @@ __global__ void __launch_bounds__(kQThreads, 2)
       uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
       if (SR && ok) {
         const uint64_t idx = (uint64_t)(r * C + c0 + 16 * b + 8 * h);
-        w0 = sr_words(p.rk, p.offset, idx);
-        w1 = sr_words(p.rk, p.offset, idx + 4);
+        w0 = sr_words(p.rk, offset, idx);
+        w1 = sr_words(p.rk, offset, idx + 4);
       }
       packed[b] = encode8<SR>(v[b], enc, w0, w1);
       ok_s[rl16 * kKWords + 2 * b + h] = packed[b];
@@ -1173,6 +1186,13 @@ nvfp4_status launch_quant(const QParams& p, int mode, int sms, cudaStream_t s) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// A device offset (NVFP4_OFFSET_DEVICE) is an address, and belongs to SR.
+bool offset_given(uint32_t flags, uint64_t offset) {
+  return !(flags & NVFP4_OFFSET_DEVICE) || ((flags & NVFP4_SR) && offset);
+}
+bool offset_aligned(uint32_t flags, uint64_t offset) {
+  return !(flags & NVFP4_OFFSET_DEVICE) || offset % 8 == 0;
+}
 
 template <auto KERN>
 nvfp4_status launch_rowcol(const CUtensorMap& tm, const QRowColParams& p, int64_t ntiles, int sms,
@@ -1198,13 +1218,16 @@ nvfp4_status quantize_rowcol_impl(const void* x, int32_t in_dtype, int64_t rows,
   for (const nvfp4_tensor* t : {row_out, col_out})
     if (!t->codes || !t->scales || !t->amax || !t->s_dec) return NVFP4_ERR_INVALID_ARG;
   if (in_dtype != NVFP4_IN_BF16) return NVFP4_ERR_INVALID_ARG;
-  if ((row_flags & ~(uint32_t)(NVFP4_SR | NVFP4_AMAX_GIVEN)) ||
-      (col_flags & ~(uint32_t)(NVFP4_SR | NVFP4_RHT | NVFP4_AMAX_GIVEN)) ||
+  if ((row_flags & ~(uint32_t)(NVFP4_SR | NVFP4_AMAX_GIVEN | NVFP4_OFFSET_DEVICE)) ||
+      (col_flags & ~(uint32_t)(NVFP4_SR | NVFP4_RHT | NVFP4_AMAX_GIVEN | NVFP4_OFFSET_DEVICE)) ||
+      !offset_given(row_flags, row_offset) || !offset_given(col_flags, col_offset) ||
       !(row_flags & NVFP4_AMAX_GIVEN) || !(col_flags & NVFP4_AMAX_GIVEN))
     return NVFP4_ERR_INVALID_ARG;
   if (rows <= 0 || cols <= 0 || ld < cols || rows % 16 || cols % 16) return NVFP4_ERR_SHAPE;
   if (rows > INT32_MAX || cols > INT32_MAX) return NVFP4_ERR_SHAPE;
-  if (!aligned16(x) || (ld * 2) % 16) return NVFP4_ERR_ALIGN;
+  if (!aligned16(x) || (ld * 2) % 16 || !offset_aligned(row_flags, row_offset) ||
+      !offset_aligned(col_flags, col_offset))
+    return NVFP4_ERR_ALIGN;
   for (const nvfp4_tensor* t : {row_out, col_out})
     if (!aligned16(t->codes) || !aligned16(t->scales) ||
         (reinterpret_cast<uintptr_t>(t->amax) & 3u) || (reinterpret_cast<uintptr_t>(t->s_dec) & 3u))
@@ -1217,6 +1240,8 @@ nvfp4_status quantize_rowcol_impl(const void* x, int32_t in_dtype, int64_t rows,
   p.rows = rows;
   p.cols = cols;
   p.seed = seed;
+  p.row_flags = row_flags;
+  p.col_flags = col_flags;
   p.row_offset = row_offset;
   p.col_offset = col_offset;
   p.row_codes = static_cast<uint8_t*>(row_out->codes);
@@ -1412,8 +1437,10 @@ nvfp4_status quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int64_
     return NVFP4_ERR_INVALID_ARG;
   if (in_dtype != NVFP4_IN_BF16 && in_dtype != NVFP4_IN_FP32) return NVFP4_ERR_INVALID_ARG;
   if (mode < NVFP4_ROW_1X16 || mode > NVFP4_BLOCK_16X16) return NVFP4_ERR_INVALID_ARG;
-  if (flags & ~(uint32_t)(NVFP4_RHT | NVFP4_SR | NVFP4_EMIT_T | NVFP4_AMAX_GIVEN))
+  if (flags & ~(uint32_t)(NVFP4_RHT | NVFP4_SR | NVFP4_EMIT_T | NVFP4_AMAX_GIVEN |
+                          NVFP4_OFFSET_DEVICE))
     return NVFP4_ERR_INVALID_ARG;
+  if (!offset_given(flags, offset)) return NVFP4_ERR_INVALID_ARG;
   if ((flags & NVFP4_EMIT_T) && mode != NVFP4_BLOCK_16X16) return NVFP4_ERR_INVALID_ARG;
   if ((flags & NVFP4_RHT) && mode == NVFP4_BLOCK_16X16) return NVFP4_ERR_INVALID_ARG;
   if ((flags & NVFP4_EMIT_T) && (!out->codes_t || !out->scales_t)) return NVFP4_ERR_INVALID_ARG;
@@ -1423,7 +1450,8 @@ nvfp4_status quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int64_
   if (mode == NVFP4_COL_1X16 && rows % 16) return NVFP4_ERR_SHAPE;
   if (mode == NVFP4_BLOCK_16X16 && (rows % 16 || cols % 16)) return NVFP4_ERR_SHAPE;
   const size_t esz = in_dtype == NVFP4_IN_BF16 ? 2 : 4;
-  if (!aligned16(x) || (ld * (int64_t)esz) % 16) return NVFP4_ERR_ALIGN;
+  if (!aligned16(x) || (ld * (int64_t)esz) % 16 || !offset_aligned(flags, offset))
+    return NVFP4_ERR_ALIGN;
   if (!aligned16(out->scales) || ((reinterpret_cast<uintptr_t>(out->codes) & 3u) != 0))
     return NVFP4_ERR_ALIGN;
   if ((flags & NVFP4_EMIT_T) &&

@@ -10,7 +10,9 @@ Every projection of every expert is one grouped product; quantisation follows
 the dense MLP (activations and weights to nearest, gradients stochastically,
 the random Hadamard transform on the weight gradients' operands).  Weight
 gradients are folded into FP32 masters.  Nothing synchronises with the host,
-so a step can be captured as a CUDA graph.
+so a step can be captured as a CUDA graph; its backward then takes the step's
+number from the device, since a captured number, and with it the stochastic
+rounding's random words, would be the same in every replay.
 
 ``python -m nvfp4_block_scaled_03_gb300.moe`` trains a small block for a few
 steps on a GB300 and prints the loss.
@@ -49,13 +51,14 @@ class MoEBlock:
         }
         self.grads = {k: torch.zeros_like(v) for k, v in self.params.items()}
         self.hidden, self.ffn = hidden, ffn
+        self.operand_ids = torch.arange(6, device=device)
 
-    def _both(self, x, sr, step):
+    def _both(self, x, flags=0, offsets=(0, 0)):
         """Row-wise and column-wise operands of x from one read (after its amaxes)."""
         row, col = self._amax(x)
-        flags = nv.SR if sr else 0
-        return nv.nvfp4_quantize_rowcol(x, flags, flags | nv.RHT, seed=self.seed, row_offset=step,
-                                        col_offset=step + 1, amax_row=row, amax_col=col)
+        return nv.nvfp4_quantize_rowcol(x, flags, flags | nv.RHT, seed=self.seed,
+                                        row_offset=offsets[0], col_offset=offsets[1],
+                                        amax_row=row, amax_col=col)
 
     def _amax(self, x):
         row = torch.zeros(1, device=x.device)
@@ -74,7 +77,7 @@ class MoEBlock:
         plan = s["plan"] = nv.nvfp4_route_fwd(s["logits"], self.top, self.mode)
         groups = (plan.sizes, plan.offsets)
         xe = nv.nvfp4_dispatch(s["h"], plan.row, plan.source)
-        qx, s["qx_col"] = self._both(xe, False, 0)
+        qx, s["qx_col"] = self._both(xe)
         for name in ("gate_proj", "up_proj", "down_proj"):
             s[name] = nv.nvfp4_quantize(p[name], nv.BLOCK_16X16, nv.EMIT_T)
         s["G"] = nv.nvfp4_group_gemm(qx, s["gate_proj"], *groups)
@@ -89,11 +92,17 @@ class MoEBlock:
         self.saved = s
         return y
 
-    def backward(self, dy: torch.Tensor, step: int = 0) -> torch.Tensor:
+    def backward(self, dy: torch.Tensor, step: int | torch.Tensor = 0) -> torch.Tensor:
         """dx from dy; the parameters' gradients are added to `self.grads`.
-        `step` picks the random numbers of the stochastic rounding."""
+        `step` picks the random numbers of the stochastic rounding: a number,
+        or, where the call is captured into a graph that is replayed, a
+        1-element int64 tensor on the device that each step advances."""
         p, g, s = self.params, self.grads, self.saved
-        plan, at = s["plan"], 8 * step
+        plan = s["plan"]
+        if isinstance(step, torch.Tensor):
+            at = (8 * step.reshape(1) + self.operand_ids).split(1)
+        else:
+            at = [8 * step + k for k in range(6)]
         groups = (plan.sizes, plan.offsets)
         E, F, D = self.experts, self.ffn, self.hidden
         dx, dz, dw_out, dgate, _ = nv.nvfp4_residual_norm_bwd(
@@ -101,7 +110,7 @@ class MoEBlock:
         g["w_out"] += dw_out
         g["gate"] += dgate
         do, dweight = nv.nvfp4_combine_bwd(dz, s["o"], plan.row, plan.source, plan.weight)
-        qdo, qdo_col = self._both(do, True, at)
+        qdo, qdo_col = self._both(do, nv.SR, at[0:2])
         dH = nv.nvfp4_group_gemm(qdo, s["down_proj"], *groups, b_view=1)
         nv.nvfp4_group_wgrad(qdo_col, s["qh_col"], *groups, out=g["down_proj"].view(E, D, F),
                              d_mode=nv.D_F32_ACCUM)
@@ -110,7 +119,7 @@ class MoEBlock:
         for name, d, row, col, k in (("gate_proj", dG, g_row, g_col, 2),
                                      ("up_proj", dU, u_row, u_col, 4)):
             qd, qd_col = nv.nvfp4_quantize_rowcol(
-                d, nv.SR, nv.SR | nv.RHT, seed=self.seed, row_offset=at + k, col_offset=at + k + 1,
+                d, nv.SR, nv.SR | nv.RHT, seed=self.seed, row_offset=at[k], col_offset=at[k + 1],
                 amax_row=row, amax_col=col)
             dxe = nv.nvfp4_group_gemm(qd, s[name], *groups, b_view=1, C_add=dxe,
                                       d_mode=nv.D_BF16 if dxe is None else nv.D_BF16_ADD_C)
