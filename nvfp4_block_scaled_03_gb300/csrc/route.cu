@@ -102,12 +102,13 @@ NVFP4_DEV float key_value(uint32_t k) {
   return __uint_as_float(WIDE ? b : b & 0xFFFF0000u);
 }
 
-// The tokens of one of `warps` warps of this CTA: [first, last).
+// The tokens of one of `warps` warps of this CTA: [first, last).  Counted from the
+// CTA's first token, which is one: the ends of shares may lie beyond 2^31.
 NVFP4_DEV void warp_tokens(const RouteArgs& a, int warps, int& first, int& last) {
   const int per = (a.per_cta + warps - 1) / warps, c0 = blockIdx.x * a.per_cta;
-  const int end = min(c0 + a.per_cta, a.tokens);
-  first = min(c0 + (int)(threadIdx.x >> 5) * per, end);
-  last = min(first + per, end);
+  const int n = min(a.per_cta, a.tokens - c0), w = (int)(threadIdx.x >> 5) * per;
+  first = c0 + min(w, n);
+  last = c0 + min(w + per, n);
 }
 
 // Experts and weights of B tokens from t on, one warp: to global memory, and
