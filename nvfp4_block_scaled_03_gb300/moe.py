@@ -1,15 +1,19 @@
 """A mixture-of-experts MLP block on the library's calls, forward and backward:
 
     h      = norm(x) w_in                               the block's input
-    plan   = top-k of softmax(h Wr^T)                   the router (bf16)
+    plan   = top-k of softmax(h Wr^T)                   the router
     o      = experts' SwiGLU MLPs over the plan's rows  (NVFP4 products)
     z      = sum over a token's experts of weight * o
     y      = x + z_scale gate (.) norm(z) w_out         the next block's stream
 
 Every projection of every expert is one grouped product; quantisation follows
 the dense MLP (activations and weights to nearest, gradients stochastically,
-the random Hadamard transform on the weight gradients' operands).  Weight
-gradients are folded into FP32 masters.  Nothing synchronises with the host,
+the random Hadamard transform on the weight gradients' operands).  The router's
+products take bf16 operands (h is one; its weights and the logits' gradient are
+rounded to it) and give FP32 logits and an FP32 weight gradient; what it adds to
+h's gradient is added in FP32 to the experts' share, which the combination has
+rounded to bf16, and the sum is rounded to bf16 again, the type in which the
+norm takes it.  Weight gradients are folded into FP32 masters.  Nothing synchronises with the host,
 so a step can be captured as a CUDA graph; its backward then takes the step's
 number from the device, since a captured number, and with it the stochastic
 rounding's random words, would be the same in every replay.
@@ -73,7 +77,7 @@ class MoEBlock:
         s["x"] = x
         _, s["h"] = nv.nvfp4_residual_norm_fwd(x, w_pre=p["w_in"], eps=self.eps)
         s["router"] = p["router"].bfloat16()
-        s["logits"] = s["h"] @ s["router"].t()
+        s["logits"] = torch.mm(s["h"], s["router"].t(), out_dtype=torch.float32)
         plan = s["plan"] = nv.nvfp4_route_fwd(s["logits"], self.top, self.mode)
         groups = (plan.sizes, plan.offsets)
         xe = nv.nvfp4_dispatch(s["h"], plan.row, plan.source)
@@ -126,9 +130,9 @@ class MoEBlock:
             nv.nvfp4_group_wgrad(qd_col, s["qx_col"], *groups, out=g[name].view(E, F, D),
                                  d_mode=nv.D_F32_ACCUM)
         dh = nv.nvfp4_combine(dxe, plan.row)
-        dlogits = nv.nvfp4_route_bwd(s["logits"], plan, dweight, self.mode)
-        g["router"] += (dlogits.t() @ s["h"]).float()
-        dh = torch.addmm(dh, dlogits, s["router"])
+        dlogits = nv.nvfp4_route_bwd(s["logits"], plan, dweight, self.mode).bfloat16()
+        g["router"] += torch.mm(dlogits.t(), s["h"], out_dtype=torch.float32)
+        dh = torch.mm(dlogits, s["router"], out_dtype=torch.float32).add_(dh).bfloat16()
         dx, _, _, _, dw_in = nv.nvfp4_residual_norm_bwd(dx, dh, s["x"], w_pre=p["w_in"],
                                                         eps=self.eps)
         g["w_in"] += dw_in
