@@ -28,8 +28,6 @@ constexpr int kAtom = 64;      // contraction elements per scale atom
 constexpr int kMaxGroups = 512;
 
 struct GroupArgs {
-  const uint8_t* sfa;
-  const uint8_t* sfb;
   const float* sdec_a;
   const float* sdec_b;
   void* D;
@@ -40,7 +38,6 @@ struct GroupArgs {
   int rows;          // rows: rows of A and D; wgrad: the contraction's extent
   int M, N, K;       // wgrad: D_e is [M, N]; rows: N and the contraction K
   int kga, kgb;      // scale atoms per 128-row block of A, of B
-  int nrb_b;         // 128-row blocks of B's scale tensor
   int num_m_blk;     // wgrad: tiles along M
   int num_n_blk;
   int b_row_step;    // rows: B rows from one group to the next (0 with the transposed view)
@@ -909,8 +906,6 @@ nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
   GroupArgs a = {};
-  a.sfa = static_cast<const uint8_t*>(A->scales);
-  a.sfb = static_cast<const uint8_t*>(b_sf);
   a.sdec_a = A->s_dec;
   a.sdec_b = B->s_dec;
   a.D = D;
@@ -924,7 +919,6 @@ nvfp4_status group_gemm_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, int32
   const int64_t b_rows = b_view ? N : groups * N, b_cols = b_view ? groups * K : K;
   a.kga = (int)(K / kAtom);
   a.kgb = (int)(b_cols / kAtom);
-  a.nrb_b = (int)(b_rows / 128);
   a.b_row_step = b_view ? 0 : (int)N;
   a.b_atom_step = b_view ? (int)(K / kAtom) : 0;
   const Operands o = {A->codes, A->scales, b_codes, b_sf, rows, K, b_rows, b_cols, rows};
@@ -954,8 +948,6 @@ nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, cons
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
   GroupArgs a = {};
-  a.sfa = static_cast<const uint8_t*>(A->scales);
-  a.sfb = static_cast<const uint8_t*>(B->scales);
   a.sdec_a = A->s_dec;
   a.sdec_b = B->s_dec;
   a.D = D;
@@ -966,7 +958,6 @@ nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, cons
   a.M = (int)M;
   a.N = (int)N;
   a.kga = a.kgb = (int)(rows / kAtom);
-  a.nrb_b = (int)(N / 128);
   const Operands o = {A->codes, A->scales, B->codes, B->scales, M, rows, N, rows, groups * M};
   // weight gradients are bound by D: both widths take the same time (64 x [1024,
   // 2048] over 32000 rows: 74 us), and the narrow one wastes less of odd widths

@@ -741,9 +741,16 @@ int ctas_per_sm(int threads, uint32_t smem) {
 constexpr int kBwdCtasPerSm = 2;
 
 template <int VPT, bool WIDE, bool RING, int PARTS, bool BACK>
+constexpr auto row_kernel() {
+  if constexpr (BACK)
+    return norm_bwd_kernel<VPT, WIDE, RING, PARTS>;
+  else
+    return norm_fwd_kernel<VPT, WIDE, RING, PARTS>;
+}
+
+template <int VPT, bool WIDE, bool RING, int PARTS, bool BACK>
 cudaError_t launch_rows(const NormArgs& p, int threads, int sms, cudaStream_t stream, int* grid) {
-  constexpr auto kern = BACK ? norm_bwd_kernel<VPT, WIDE, RING, PARTS>
-                             : norm_fwd_kernel<VPT, WIDE, RING, PARTS>;
+  constexpr auto kern = row_kernel<VPT, WIDE, RING, PARTS, BACK>();
   const uint32_t smem = RING                                           ? p.stages * p.stage_bytes
                         : WeightsAt<VPT, RING>::value == kInSmem ? (uint32_t)p.cols * 8
                                                                  : 0u;
