@@ -626,7 +626,9 @@ nvfp4_status nvfp4_group_gemm(const nvfp4_tensor* A, const nvfp4_tensor* B, int3
  * or on neither); the padding rows of those tensors must have been zero.
  *   NVFP4_D_BF16       D bf16 [groups, M, N], zeros for an empty group
  *   NVFP4_D_F32_ACCUM  D fp32 [groups, M, N] += the FP32 product, not rounded
- *                      to bf16 in between (an empty group's D stays as it is)
+ *                      to bf16 in between (an empty group's D stays as it is);
+ *                      one addition an element, in L2, which flushes
+ *                      subnormal operands and results to zero
  * tile: NVFP4_TILE_AUTO, _PAIR_256X256, or with NVFP4_D_BF16 _PAIR_256X384.
  * Shapes: rows, M, N multiples of 128, 1 <= groups <= 512.  One launch. */
 nvfp4_status nvfp4_group_wgrad(const nvfp4_tensor* A, const nvfp4_tensor* B,

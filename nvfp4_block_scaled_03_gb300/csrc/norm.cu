@@ -20,17 +20,19 @@
 // + 2 (z, h) or 3 + 3 streams and are bound by memory, with the arithmetic
 // (about 12 and 25 instructions an element pair) not far behind.
 //
-// A persistent CTA takes `rpc` rows at a time (one from 4097 columns on, whole
-// warps per row), its weights in registers.  Rows arrive by bulk copies in a
-// ring of shared-memory stages, so loads run ahead while a row is reduced; a
-// row is read from its stage once per pass instead of being held in
-// registers, which leaves those to the weights and the column sums.  Long rows
-// (the backward from 8200 columns on, the forward from 16392) are read from
-// global memory in each pass.
+// A persistent CTA takes `rpc` rows at a time, whole warps per row (forward one
+// from 4104 to 16384 columns, backward one from 2056 on), its weights in
+// registers.  Rows arrive by bulk copies in a ring of shared-memory stages, so
+// loads run ahead while a row is reduced; a row is read from its stage once per
+// pass instead of being held in registers, which leaves those to the weights
+// and the column sums.  Long rows (the backward from 8200 columns on, the
+// forward from 16392) are read from global memory in each pass.  From 16392 columns on a thread takes 128 of them,
+// more than its 64 registers hold: 1.1 KB of spills forward, 2.7 KB backward.
 //
 // Measured (us, and the time their bytes take at the copy rate): 16384 x 4096
-// bf16 forward 85 (80), backward 149 (120); FP32 stream, 8191 x 4096 forward
-// 69 (60), backward 100 (90); 16 x 4096 forward 3.4, launch included.  The bf16
+// bf16 forward 84 (80), backward 149 (120); FP32 stream, 8191 x 4096 forward
+// 69 (60), backward 102 (90); 4096 x 16384 bf16 118 (80), 230 (120); 2048 x 32768
+// 241 (80), 780 (120); 16 x 4096 forward 3.9, launch included.  The bf16
 // backward is bound by its arithmetic (0.58 of the issue slots, 16 warps an SM:
 // its column sums and weights fill the registers).
 //
