@@ -2,8 +2,6 @@
 replay rounds with the random numbers of the step that the counter names, as
 the calls with that number do one by one; the call's own number stays the same
 in every replay."""
-import ctypes as C
-
 import pytest
 
 pytestmark = pytest.mark.gpu
