@@ -518,6 +518,72 @@ nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t fl
                             void* workspace, size_t workspace_bytes, nvfp4_stream stream);
 
 /* ---------------------------------------------------------------------- */
+/* Orthogonalised momentum of matrices                                      */
+/* ---------------------------------------------------------------------- */
+/* The optimiser step for weights that are matrices (or a stack of them, such
+ * as the experts' projections): a momentum, whose matrix is replaced by one
+ * with nearly the same singular vectors and singular values near 1, by an
+ * iteration of products (Newton-Schulz).  For each of `batch` matrices
+ * [rows, cols]:
+ *   V <- mu V + G,   U = G + mu V (nesterov) or V
+ *   X <- U / max(||U||_F, eps)
+ *   `steps` times, with the step's (a, b, c):
+ *     A = X X^T,  B = b A + c A A,  X <- a X + B X
+ *     (rows > cols: A = X^T X,  X <- a X + X B, the same polynomial)
+ *   update = X
+ * G the gradient (grad_dtype), V the FP32 momentum, U, X, A and B internal:
+ * the products take f16 operands with what f16 would lose of X and of the
+ * diagonals carried beside them, and FP32 accumulators; the update is within
+ * about 1.5e-3 of that of 64 bits (2-norm of the difference) plus its one
+ * rounding to bf16.  A matrix of zeros gives zeros.  NaN or infinities in a
+ * matrix make its update (and momentum) unspecified, not the others'.  The
+ * entries of X, A and B must stay below 16 in magnitude, which they do for every
+ * input with coefficients that keep X's singular values below 2 and
+ * |b s + c s^2| below 16 on their squares s, as the usual (3.4445, -4.7750,
+ * 2.0315) do. */
+enum { NVFP4_MUON_MAX_STEPS = 32 };
+typedef struct nvfp4_muon_params {
+  int64_t batch, rows, cols;
+  int32_t grad_dtype; /* nvfp4_in_dtype                                    */
+  int32_t nesterov;   /* 0 or 1                                            */
+  int32_t steps;      /* 1 .. NVFP4_MUON_MAX_STEPS                         */
+  float mu;           /* momentum                                          */
+  float eps;          /* > 0                                               */
+  const float* coefs; /* host, [steps][3]; read before the call returns    */
+} nvfp4_muon_params;
+
+/* *workspace_bytes (may be NULL) = what nvfp4_muon_update needs: about 6 bytes
+ * an element and 4 min(rows, cols)^2 a matrix.  NVFP4_ERR_SHAPE unless
+ * 1 <= batch <= 65535, rows, cols >= 1, rows cols < 2^31 and
+ * min(rows, cols) <= 32768. */
+nvfp4_status nvfp4_muon_sizes(int64_t batch, int64_t rows, int64_t cols,
+                              size_t* workspace_bytes);
+
+/* grad [batch, rows, cols] (zeroed with NVFP4_ZERO_GRAD in flags), momentum float
+ * [batch, rows, cols] (read and written), update bf16 [batch, rows, cols]; all
+ * contiguous, 16-byte aligned, not overlapping.  Any rows and cols; rows of a
+ * multiple of 8 elements take the fast loads and stores.  The result is the same
+ * on every call.  workspace: device, 16-byte aligned, at least
+ * nvfp4_muon_sizes gives; contents on return unspecified.  2 + 3 steps launches
+ * on `stream`, nothing allocated.  Returns NVFP4_ERR_INVALID_ARG (NULL pointers,
+ * overlaps, unknown flags or types, steps, mu, eps or coefs out of range),
+ * _SHAPE, _ALIGN, _WORKSPACE, _ARCH, _CUDA. */
+nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad, float* momentum,
+                               void* update, uint32_t flags, void* workspace,
+                               size_t workspace_bytes, nvfp4_stream stream);
+
+/* Applies an update to an FP32 master weight, elementwise in binary32:
+ *   W[i]  = (1 - lr decay) W[i] - (lr scale) update[i]
+ *   *amax = max_i |W[i]|  of the updated W, when amax is not NULL, as
+ *           nvfp4_sgd_step gives it (NaN is left out, as there).
+ * The factors are computed in binary64 and rounded once.  update bf16 [n], W
+ * float [n], both 16-byte aligned, not overlapping; n > 0.  lr, scale, decay
+ * finite.  workspace: as nvfp4_sgd_step.  One read of both, one write of W. */
+nvfp4_status nvfp4_muon_apply(float* W, const void* update, int64_t n, float lr, float scale,
+                              float decay, float* amax, void* workspace, size_t workspace_bytes,
+                              nvfp4_stream stream);
+
+/* ---------------------------------------------------------------------- */
 /* Mixture of experts: routing, grouped products, norms                     */
 /* ---------------------------------------------------------------------- */
 /* The pages describe a dense MLP; these calls build the mixture-of-experts

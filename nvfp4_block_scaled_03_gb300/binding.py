@@ -51,6 +51,13 @@ class NormParams(C.Structure):
                 ("z_scale", C.c_float)]
 
 
+class MuonParams(C.Structure):
+    """Mirror of ``nvfp4_muon_params``."""
+    _fields_ = [("batch", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
+                ("grad_dtype", C.c_int32), ("nesterov", C.c_int32), ("steps", C.c_int32),
+                ("mu", C.c_float), ("eps", C.c_float), ("coefs", C.POINTER(C.c_float))]
+
+
 class MlpParams(C.Structure):
     """Mirror of ``nvfp4_mlp_params``."""
     _fields_ = [("M", C.c_int64), ("D", C.c_int64), ("F", C.c_int64), ("Wg", C.c_void_p),
@@ -96,6 +103,10 @@ def _load():
         "nvfp4_mlp_tensor": ([i64, i64, i64, vp, vp, i32, P(vp), P(i64), P(i64)], C.c_int),
         "nvfp4_mlp_operand": ([i64, i64, i64, vp, vp, i32, P(Tensor)], C.c_int),
         "nvfp4_sgd_step": ([vp, vp, i64, C.c_float, u32, vp, vp, sz, vp], C.c_int),
+        "nvfp4_muon_sizes": ([i64, i64, i64, P(sz)], C.c_int),
+        "nvfp4_muon_update": ([P(MuonParams), vp, vp, vp, u32, vp, sz, vp], C.c_int),
+        "nvfp4_muon_apply": ([vp, vp, i64, C.c_float, C.c_float, C.c_float, vp, vp, sz, vp],
+                             C.c_int),
         "nvfp4_route_sizes": ([i64, i64, i32, P(i64), P(sz)], C.c_int),
         "nvfp4_route_fwd": ([vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                             C.c_int),
@@ -564,6 +575,120 @@ def _scratch(nbytes, t):
     allocator each time: one that a later, larger call replaced would still be
     written by the graphs that captured it."""
     return torch.empty(max(nbytes, 16), dtype=_U8, device=t.device)
+
+
+def _on_device(call):
+    """As _on_stream, for a call whose first tensor may lie on another device
+    than the current one: the call then runs there, on that device's current
+    stream."""
+    inner = _on_stream(call)
+
+    @functools.wraps(call)
+    def run(first, *args, **kwargs):
+        if not (isinstance(first, torch.Tensor) and first.is_cuda):
+            raise ValueError(f"{call.__name__}: the first argument must be a CUDA tensor")
+        if first.get_device() == torch.cuda.current_device():
+            return inner(first, *args, **kwargs)
+        with torch.cuda.device(first.device):
+            return inner(first, *args, **kwargs)
+    return run
+
+
+def _together(first, *others):
+    """Refuses tensors of several devices."""
+    for t in others:
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError("tensors of one call must lie on one device")
+
+
+# ---- orthogonalised momentum ---------------------------------------------------
+MUON_COEFS = (3.4445, -4.7750, 2.0315)
+MUON_MAX_STEPS = 32
+
+
+def muon_sizes(batch, rows, cols) -> int:
+    """Workspace bytes of nvfp4_muon_update."""
+    w = C.c_size_t()
+    _check(lib.nvfp4_muon_sizes(batch, rows, cols, w), "nvfp4_muon_sizes")
+    return w.value
+
+
+@functools.lru_cache(maxsize=64)
+def _coefs(coefs, steps):
+    """[steps][3] for the library: one triple for every step, or one for each."""
+    if not 1 <= steps <= MUON_MAX_STEPS:
+        raise ValueError(f"steps must be 1 to {MUON_MAX_STEPS}")
+    rows = [coefs] * steps if len(coefs) == 3 and not hasattr(coefs[0], "__len__") else coefs
+    if len(rows) != steps or any(len(r) != 3 for r in rows):
+        raise ValueError("coefs must be one triple, or one for each step")
+    flat = [float(v) for r in rows for v in r]
+    return (C.c_float * len(flat))(*flat)
+
+
+@_on_device
+def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.95,
+                      nesterov: bool = True, steps: int = 5, coefs=MUON_COEFS, eps: float = 1e-7,
+                      out: torch.Tensor | None = None, zero_grad: bool = False,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The orthogonalised momentum of a matrix, or of each of a stack of them:
+    grad [..., rows, cols] (bf16 or fp32) is taken into the fp32 `momentum`, in
+    place; returns the update in bf16 (see nvfp4_muon_update in nvfp4.h).  `coefs`:
+    the polynomial's (a, b, c), or one such triple for each step."""
+    kind = _DTYPES.get(grad.dtype)
+    if kind is None:
+        raise TypeError(f"grad must be bf16 or fp32, got {grad.dtype}")
+    shape = grad.shape
+    if len(shape) < 2 or grad.numel() == 0:
+        raise ValueError("grad must be a matrix or a stack of matrices, not empty")
+    _cuda(grad, grad.dtype, "grad")
+    _cuda(momentum, _F32, "momentum", shape)
+    if out is None:
+        out = torch.empty(shape, dtype=_BF16, device=grad.device)
+    else:
+        _cuda(out, _BF16, "out", shape)
+    rows, cols = shape[-2], shape[-1]
+    batch = grad.numel() // (rows * cols)
+    if workspace is None:
+        workspace = _scratch(muon_sizes(batch, rows, cols), grad)
+    else:
+        _cuda(workspace, _U8, "workspace")
+    _together(grad, momentum, out, workspace)
+    if not hasattr(coefs, "__hash__") or coefs.__hash__ is None:
+        coefs = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefs)
+    p = MuonParams(batch, rows, cols, kind, 1 if nesterov else 0, steps, mu, eps,
+                   _coefs(coefs, steps))
+    st = lib.nvfp4_muon_update(p, grad.data_ptr(), momentum.data_ptr(), out.data_ptr(),
+                               ZERO_GRAD if zero_grad else 0, workspace.data_ptr(),
+                               workspace.numel(), _current(grad))
+    if st:
+        raise NVFP4Error(st, "nvfp4_muon_update")
+    return out
+
+
+@_on_device
+def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: float = 1.0,
+                     decay: float = 0.0, amax: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """W = (1 - lr decay) W - lr scale update on an fp32 master weight, in place
+    (see nvfp4_muon_apply in nvfp4.h); returns max |W| of the result, a 1-element
+    tensor that its quantisation takes."""
+    _cuda(W, _F32, "W")
+    _cuda(update, _BF16, "update", W.shape)
+    if amax is None:
+        amax = torch.empty(1, dtype=_F32, device=W.device)
+    else:
+        _cuda(amax, _F32, "amax", (1,))
+    if workspace is None:
+        workspace = _scratch(4096, W)
+    else:
+        _cuda(workspace, _U8, "workspace")
+    _together(W, update, amax, workspace)
+    st = lib.nvfp4_muon_apply(W.data_ptr(), update.data_ptr(), W.numel(), lr, scale, decay,
+                              amax.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                              _current(W))
+    if st:
+        raise NVFP4Error(st, "nvfp4_muon_apply")
+    return amax
 
 
 def operand(codes: torch.Tensor, scales: torch.Tensor, s_dec: torch.Tensor, rows: int,

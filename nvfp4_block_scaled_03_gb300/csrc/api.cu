@@ -63,16 +63,18 @@ nvfp4_status nvfp4_device_check(int device) {
 nvfp4_status nvfp4_check_device_errors(nvfp4_stream stream) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  unsigned int gcode = 0, qcode = 0, ecode = 0, ncode = 0;
+  unsigned int gcode = 0, qcode = 0, ecode = 0, ncode = 0, mcode = 0;
   nvfp4_status st = gemm_read_error(&gcode);
   if (st != NVFP4_OK) return st;
   st = group_read_error(&ecode);
   if (st != NVFP4_OK) return st;
   st = norm_read_error(&ncode);
   if (st != NVFP4_OK) return st;
+  st = muon_read_error(&mcode);
+  if (st != NVFP4_OK) return st;
   st = quant_read_error(&qcode);
   if (st != NVFP4_OK) return st;
-  return (gcode || ecode || ncode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
+  return (gcode || ecode || ncode || mcode || qcode) ? NVFP4_ERR_DEVICE_TIMEOUT : NVFP4_OK;
 }
 
 nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
@@ -90,6 +92,8 @@ nvfp4_status nvfp4_debug_inject(uint32_t stall_mask, uint64_t wait_limit_ns) {
   const unsigned int gemm = ((stall_mask & NVFP4_STALL_GEMM) ? 1u : 0u) |
                             ((stall_mask & NVFP4_QUIT_GEMM) ? 2u : 0u);
   st = group_set_injection(gemm, ns);
+  if (st != NVFP4_OK) return st;
+  st = muon_set_injection(gemm, ns);
   if (st != NVFP4_OK) return st;
   return gemm_set_injection(gemm, ns);
 }

@@ -122,6 +122,10 @@ nvfp4_status group_wgrad_impl(const nvfp4_tensor* A, const nvfp4_tensor* B, cons
 nvfp4_status group_read_error(unsigned int* code);
 nvfp4_status group_set_injection(unsigned int stall, unsigned long long wait_ns);
 
+// The products of nvfp4_muon_update (muon.cu), likewise.
+nvfp4_status muon_read_error(unsigned int* code);
+nvfp4_status muon_set_injection(unsigned int stall, unsigned long long wait_ns);
+
 // The most SMs that workspaces sized without a device allow for.
 constexpr int kMaxSms = 160;
 

@@ -76,6 +76,64 @@ __global__ void __launch_bounds__(kThreads) sgd_amax_finalize_kernel(const float
   if (threadIdx.x == 0) *amax = m;
 }
 
+// W = keep W - step update (bf16), 8 elements a thread, two chunks in flight (four
+// gain nothing); the elements behind the last chunk are the last CTA's.
+NVFP4_DEV float apply1(float w, float u, float keep, float step) {
+  return fmaf(-step, u, __fmul_rn(keep, w));
+}
+
+template <bool AMAX>
+__global__ void __launch_bounds__(kThreads) muon_apply_kernel(float* __restrict__ W,
+                                                              const uint16_t* __restrict__ U,
+                                                              int64_t n, float keep, float step,
+                                                              float* partials) {
+  __shared__ float red[kThreads / 32];
+  constexpr int kChunks = 2;
+  const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * kThreads;
+  float m = 0.0f;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n8; i += kChunks * stride) {
+    float4 w[kChunks][2];
+    uint4 u[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int64_t q = i + c * stride;
+      if (q < n8) {
+        w[c][0] = reinterpret_cast<const float4*>(W)[2 * q];
+        w[c][1] = reinterpret_cast<const float4*>(W)[2 * q + 1];
+        u[c] = reinterpret_cast<const uint4*>(U)[q];
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      const int64_t q = i + c * stride;
+      if (q >= n8) continue;
+      const uint32_t b[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t lo = b[2 * k], hi = b[2 * k + 1];
+        const float4 v = w[c][k];
+        const float4 r = make_float4(apply1(v.x, __uint_as_float(lo << 16), keep, step),
+                                     apply1(v.y, __uint_as_float(lo & 0xFFFF0000u), keep, step),
+                                     apply1(v.z, __uint_as_float(hi << 16), keep, step),
+                                     apply1(v.w, __uint_as_float(hi & 0xFFFF0000u), keep, step));
+        reinterpret_cast<float4*>(W)[2 * q + k] = r;
+        if (AMAX)
+          m = fmaxf(m, fmaxf(fmaxf(fabsf(r.x), fabsf(r.y)), fmaxf(fabsf(r.z), fabsf(r.w))));
+      }
+    }
+  }
+  const int64_t t = n8 * 8 + threadIdx.x;
+  if (blockIdx.x == gridDim.x - 1 && t < n) {
+    const float r = apply1(W[t], __uint_as_float((uint32_t)U[t] << 16), keep, step);
+    W[t] = r;
+    if (AMAX) m = fmaxf(m, fabsf(r));
+  }
+  if (AMAX) {
+    m = block_max(m, red);
+    if (threadIdx.x == 0) partials[blockIdx.x] = m;
+  }
+}
+
 // CTAs of a persistent launch: as many as are resident at once (looked up
 // once per kernel and device), at most one partial slot each, at most one
 // per kThreads chunks.
@@ -141,4 +199,34 @@ extern "C" nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, 
   }
   return zero ? launch_sgd<true, false>(W, G, n4, lr, nullptr, dev.sm_count, &grid, s)
               : launch_sgd<false, false>(W, G, n4, lr, nullptr, dev.sm_count, &grid, s);
+}
+
+extern "C" nvfp4_status nvfp4_muon_apply(float* W, const void* update, int64_t n, float lr,
+                                         float scale, float decay, float* amax, void* workspace,
+                                         size_t workspace_bytes, nvfp4_stream stream) {
+  if (!W || !update || !std::isfinite(lr) || !std::isfinite(scale) || !std::isfinite(decay))
+    return NVFP4_ERR_INVALID_ARG;
+  if (n <= 0 || n > INT64_MAX / 16) return NVFP4_ERR_SHAPE;
+  const uintptr_t wb = reinterpret_cast<uintptr_t>(W), ub = reinterpret_cast<uintptr_t>(update);
+  if (wb < ub + (uintptr_t)n * 2 && ub < wb + (uintptr_t)n * 4) return NVFP4_ERR_INVALID_ARG;
+  if (!a16(W) || !a16(update) || (reinterpret_cast<uintptr_t>(amax) & 3u)) return NVFP4_ERR_ALIGN;
+  if (amax && (!workspace || workspace_bytes < kQuantWorkspaceBytes || !a16(workspace)))
+    return NVFP4_ERR_WORKSPACE;
+  DeviceInfo dev;
+  const nvfp4_status st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const float keep = (float)(1.0 - (double)lr * decay), step = (float)((double)lr * scale);
+  const uint16_t* u = static_cast<const uint16_t*>(update);
+  if (!amax) {
+    const int grid = sgd_grid<muon_apply_kernel<false>>(n / 8, dev.sm_count);
+    muon_apply_kernel<false><<<grid, kThreads, 0, s>>>(W, u, n, keep, step, nullptr);
+    return cuda_status(cudaGetLastError());
+  }
+  float* partials = static_cast<float*>(workspace);
+  const int grid = sgd_grid<muon_apply_kernel<true>>(n / 8, dev.sm_count);
+  muon_apply_kernel<true><<<grid, kThreads, 0, s>>>(W, u, n, keep, step, partials);
+  if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
+  sgd_amax_finalize_kernel<<<1, kThreads, 0, s>>>(partials, grid, amax);
+  return cuda_status(cudaGetLastError());
 }
