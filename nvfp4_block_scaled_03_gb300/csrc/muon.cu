@@ -162,7 +162,9 @@ NVFP4_DEV void box_transpose(uint32_t from, uint32_t to, int lane) {
 }
 
 // Tile t of a matrix: by rows of the lower triangle where the result is
-// symmetric, else with the rows running fastest, so that neighbours share B.
+// symmetric, else with the matrix's smaller side running fastest: tiles at work
+// together then read X, the operand that L2 may not hold, once (14336 x 4096: an
+// update 375 us the other way round, 488 ns a stage).
 template <int KIND>
 NVFP4_DEV void tile_of(int t, const NsArgs& a, int& tm, int& tn) {
   if (KIND <= kPoly) {
@@ -171,8 +173,9 @@ NVFP4_DEV void tile_of(int t, const NsArgs& a, int& tm, int& tn) {
     while (tm * (tm + 1) / 2 > t) --tm;
     tn = t - tm * (tm + 1) / 2;
   } else {
-    tn = t / a.tiles_m;
-    tm = t - tn * a.tiles_m;
+    const int fast = min(a.tiles_m, a.tiles_n), slow = t / fast;
+    tm = a.tiles_m > a.tiles_n ? slow : t - slow * fast;
+    tn = a.tiles_m > a.tiles_n ? t - slow * fast : slow;
   }
 }
 
