@@ -645,6 +645,62 @@ nvfp4_status nvfp4_route_bwd(const void* logits, int32_t in_dtype, int64_t token
                              const int32_t* expert, const float* weight, const float* dweight,
                              void* dlogits, nvfp4_stream stream);
 
+/* The same plan by scores, with a bias for balance and groups of experts.  For
+ * each token, over the experts whose logit is not -inf or NaN (+inf counts as the
+ * largest finite value):
+ *   s_e = sigmoid(l_e), or softmax(l)_e
+ *   a group's worth is the sum of the group_top largest s_e + bias_e among its
+ *     experts (of one, where it has one); the groups_kept groups of the largest
+ *     worth are kept
+ *   the `top` experts of the largest s_e + bias_e in them are chosen, the largest
+ *     first
+ *   weight_i = scale s_i / (renormalise: sum of the chosen s; else 1)
+ * The bias decides the choice alone.  Everything is compared as 64 bits have it,
+ * equals by the lowest index; without a bias experts are compared by their
+ * logits.  Groups are consecutive experts, all of one size.  Empty slots, plan and
+ * workspace as nvfp4_route_fwd; launches too.  bias: device float [experts], finite,
+ * or NULL.
+ * NVFP4_ERR_SHAPE unless nvfp4_route_sizes accepts the sizes, groups is a power of
+ * two up to 32 that divides experts, 1 <= groups_kept <= groups, group_top is 1 or
+ * 2, and the kept groups have `top` experts; NVFP4_ERR_INVALID_ARG unless scale is
+ * finite and above 0.  The rest as nvfp4_route_fwd. */
+enum { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
+typedef struct nvfp4_route_params {
+  int64_t tokens, experts, ld;
+  int32_t in_dtype;    /* nvfp4_in_dtype of the logits (and their gradient)  */
+  int32_t top;
+  int32_t score;       /* NVFP4_SCORE_*                                      */
+  int32_t renormalise; /* 0 or 1                                             */
+  int32_t groups, groups_kept, group_top;
+  float scale;
+} nvfp4_route_params;
+nvfp4_status nvfp4_route_scored_fwd(const nvfp4_route_params* p, const void* logits,
+                                    const float* bias, int32_t* expert, float* weight,
+                                    int32_t* sizes, int32_t* offsets, int32_t* row,
+                                    int32_t* source, void* workspace, size_t workspace_bytes,
+                                    nvfp4_stream stream);
+
+/* dlogits [tokens, experts] (contiguous, the logits' type) from dweight [tokens,
+ * top], over a token's slots i, j, with v = weight / scale:
+ *   softmax, renormalised   dl_i = w_i sum_j v_j (dw_i - dw_j)
+ *   softmax                 the same plus the unchosen experts' share, who get
+ *                           -s_e sum_j w_j dw_j
+ *   sigmoid, renormalised   dl_i = w_i (1 - s_i) sum_j v_j (dw_i - dw_j)
+ *   sigmoid                 dl_i = w_i (1 - s_i) dw_i
+ * and zero elsewhere.  expert, weight: as nvfp4_route_scored_fwd wrote them for the
+ * same logits and parameters (those of the groups are not read, but checked).  One
+ * launch. */
+nvfp4_status nvfp4_route_scored_bwd(const nvfp4_route_params* p, const void* logits,
+                                    const int32_t* expert, const float* weight,
+                                    const float* dweight, void* dlogits, nvfp4_stream stream);
+
+/* bias_e += rate sign(mean of the loads - sizes[e]), the loads a plan's sizes
+ * [experts] or the sum of several plans': experts with more than their share lose
+ * rate, the others gain it, and one at the mean keeps its bias.  1 <= experts <=
+ * 512.  One launch. */
+nvfp4_status nvfp4_route_balance(const int32_t* sizes, int64_t experts, float rate, float* bias,
+                                 nvfp4_stream stream);
+
 /* xe [rows, cols] bf16: row row[t, j] is x[t], x bf16 [tokens, cols]; rows whose
  * source is -1 are zero.  cols % 8 == 0, all tensors contiguous and 16-byte
  * aligned.  Entries of `row` outside [0, rows) are skipped.  The gradient is

@@ -51,6 +51,14 @@ class NormParams(C.Structure):
                 ("z_scale", C.c_float)]
 
 
+class RouteParams(C.Structure):
+    """Mirror of ``nvfp4_route_params``."""
+    _fields_ = [("tokens", C.c_int64), ("experts", C.c_int64), ("ld", C.c_int64),
+                ("in_dtype", C.c_int32), ("top", C.c_int32), ("score", C.c_int32),
+                ("renormalise", C.c_int32), ("groups", C.c_int32), ("groups_kept", C.c_int32),
+                ("group_top", C.c_int32), ("scale", C.c_float)]
+
+
 class MuonParams(C.Structure):
     """Mirror of ``nvfp4_muon_params``."""
     _fields_ = [("batch", C.c_int64), ("rows", C.c_int64), ("cols", C.c_int64),
@@ -111,6 +119,10 @@ def _load():
         "nvfp4_route_fwd": ([vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                             C.c_int),
         "nvfp4_route_bwd": ([vp, i32, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp], C.c_int),
+        "nvfp4_route_scored_fwd": ([P(RouteParams), vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                                   C.c_int),
+        "nvfp4_route_scored_bwd": ([P(RouteParams), vp, vp, vp, vp, vp, vp], C.c_int),
+        "nvfp4_route_balance": ([vp, i64, C.c_float, vp, vp], C.c_int),
         "nvfp4_dispatch": ([vp, vp, vp, i64, i64, i32, i64, vp, vp], C.c_int),
         "nvfp4_combine": ([vp, vp, vp, i64, i64, i32, i64, vp, vp], C.c_int),
         "nvfp4_combine_bwd": ([vp, vp, vp, vp, vp, i64, i64, i32, i64, vp, vp, vp], C.c_int),
@@ -540,6 +552,7 @@ def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool 
 # These calls are made once per layer and token at a server, so their checks
 # are kept to a few attribute reads, and messages are only built to be raised.
 ROUTE_ALL, ROUTE_CHOSEN = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 GATE_NONE, GATE_CHANNEL, GATE_ROW = 0, 1, 2
 _DTYPES = {torch.bfloat16: IN_BF16, torch.float32: IN_FP32}
 _BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
@@ -766,13 +779,8 @@ def _logits(logits):
     return kind, tokens, experts, logits.stride(0) if tokens > 1 else experts
 
 
-@_on_stream
-def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
-                    plan: RoutePlan | None = None,
-                    workspace: torch.Tensor | None = None) -> RoutePlan:
-    """Choose each token's `top` experts and order the rows by expert (see
-    nvfp4_route_fwd in nvfp4.h)."""
-    kind, tokens, experts, ld = _logits(logits)
+def _plan_buffers(tokens, experts, top, plan, workspace, logits):
+    """The plan and the workspace of a routing call, checked or new."""
     rows, nbytes = route_sizes(tokens, experts, top)
     if plan is None:
         plan = _alloc_plan(tokens, experts, top, rows, logits.device)
@@ -787,6 +795,17 @@ def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
         workspace = _scratch(nbytes, logits)
     else:
         _cuda(workspace, _U8, "workspace")
+    return plan, workspace
+
+
+@_on_stream
+def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
+                    plan: RoutePlan | None = None,
+                    workspace: torch.Tensor | None = None) -> RoutePlan:
+    """Choose each token's `top` experts and order the rows by expert (see
+    nvfp4_route_fwd in nvfp4.h)."""
+    kind, tokens, experts, ld = _logits(logits)
+    plan, workspace = _plan_buffers(tokens, experts, top, plan, workspace, logits)
     st = lib.nvfp4_route_fwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
                              plan.expert.data_ptr(), plan.weight.data_ptr(),
                              plan.sizes.data_ptr(), plan.offsets.data_ptr(), plan.row.data_ptr(),
@@ -817,6 +836,74 @@ def nvfp4_route_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor
     if st:
         raise NVFP4Error(st, "nvfp4_route_bwd")
     return dlogits
+
+
+@_on_device
+def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SIGMOID,
+                           bias: torch.Tensor | None = None, groups: int = 1,
+                           groups_kept: int | None = None, group_top: int = 2,
+                           renormalise: bool = True, scale: float = 1.0,
+                           plan: RoutePlan | None = None,
+                           workspace: torch.Tensor | None = None) -> RoutePlan:
+    """Choose each token's `top` experts by their scores plus a bias, among the best
+    groups of experts, and order the rows by expert (see nvfp4_route_scored_fwd in
+    nvfp4.h).  groups_kept None: all of them."""
+    kind, tokens, experts, ld = _logits(logits)
+    plan, workspace = _plan_buffers(tokens, experts, top, plan, workspace, logits)
+    if bias is not None:
+        _cuda(bias, _F32, "bias", (experts,))
+    _together(logits, bias, plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row,
+              plan.source, workspace)
+    p = RouteParams(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, groups,
+                    groups if groups_kept is None else groups_kept, group_top, scale)
+    st = lib.nvfp4_route_scored_fwd(p, logits.data_ptr(), _ptr(bias), plan.expert.data_ptr(),
+                                    plan.weight.data_ptr(), plan.sizes.data_ptr(),
+                                    plan.offsets.data_ptr(), plan.row.data_ptr(),
+                                    plan.source.data_ptr(), workspace.data_ptr(),
+                                    workspace.numel(), _current(logits))
+    if st:
+        raise NVFP4Error(st, "nvfp4_route_scored_fwd")
+    return plan
+
+
+@_on_device
+def nvfp4_route_scored_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor,
+                           score: int = SCORE_SIGMOID, renormalise: bool = True,
+                           scale: float = 1.0,
+                           dlogits: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient from that of the weights of nvfp4_route_scored_fwd."""
+    kind, tokens, experts, ld = _logits(logits)
+    top = plan.expert.shape[1]
+    _cuda(plan.expert, _I32, "expert", (tokens, top))
+    _cuda(plan.weight, _F32, "weight", (tokens, top))
+    _cuda(dweight, _F32, "dweight", (tokens, top))
+    if dlogits is None:
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+    else:
+        _cuda(dlogits, logits.dtype, "dlogits", (tokens, experts))
+    _together(logits, plan.expert, plan.weight, dweight, dlogits)
+    p = RouteParams(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, 1, 1, 1, scale)
+    st = lib.nvfp4_route_scored_bwd(p, logits.data_ptr(), plan.expert.data_ptr(),
+                                    plan.weight.data_ptr(), dweight.data_ptr(), dlogits.data_ptr(),
+                                    _current(logits))
+    if st:
+        raise NVFP4Error(st, "nvfp4_route_scored_bwd")
+    return dlogits
+
+
+@_on_device
+def nvfp4_route_balance(sizes: torch.Tensor, bias: torch.Tensor, rate: float) -> torch.Tensor:
+    """bias += rate sign(mean load - load) in place, from the loads of a plan (or
+    the sum of several plans'): see nvfp4_route_balance in nvfp4.h; returns bias."""
+    experts = sizes.numel()
+    _cuda(sizes, _I32, "sizes", (experts,))
+    _cuda(bias, _F32, "bias", (experts,))
+    _together(sizes, bias)
+    st = lib.nvfp4_route_balance(sizes.data_ptr(), experts, rate, bias.data_ptr(),
+                                 _current(sizes))
+    if st:
+        raise NVFP4Error(st, "nvfp4_route_balance")
+    return bias
 
 
 def _rows2d(t, name):

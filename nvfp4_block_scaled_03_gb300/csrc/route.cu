@@ -21,8 +21,16 @@
 // every CTA: 4096 tokens of 512 experts took 43 us that way.)  No atomic
 // decides an order: the plan is the same every time.  Few tokens take one CTA
 // and one launch for all of it.
+//
+// Scored choice (nvfp4_route_scored_fwd): by s + bias with s the softmax or the
+// sigmoid of the logits, among the best groups of experts, as 64 bits order them.
+// A warp computes the keys in FP32 and looks at the gaps between those that it
+// puts in an order; a token with a gap that the rounding could have turned round
+// (about one in a thousand) is done again in FP64, whose rate here would make it
+// the bound for all of them.  Without a bias the logits' own order decides.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 
 #include "common.cuh"
 #include "internal.h"
@@ -54,9 +62,16 @@ struct RouteArgs {
   int64_t rows;     // entries of source
   int32_t* counts;  // [CTAs + 1][experts], after the second kernel running sums
   int ctas;
+  // scored choice
+  const float* bias;
+  int score, renorm;
+  int groups, kept, group_top;
+  int group_size, lanes, per;  // of a group: experts, lanes that hold them, experts of a lane
+  float scale;
   // backward
   const float* dweight;
   void* dlogits;
+  float inv_scale;
 };
 
 template <bool WIDE>
@@ -174,8 +189,291 @@ NVFP4_DEV void choose_tokens(const RouteArgs& a, int t, int* hist) {
   }
 }
 
-// Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
+// ---- scored choice -----------------------------------------------------------------
+// A group of experts takes a.lanes lanes, a.per experts each (all of them where there
+// is one group), so lanes and their experts rise together.
+struct Share {
+  int first, count;
+};
+NVFP4_DEV Share lane_share(const RouteArgs& a, int lane) {
+  const int g = lane / a.lanes, at = (lane - g * a.lanes) * a.per;
+  return {g * a.group_size + at, min(a.per, a.group_size - at)};
+}
+
+// A logit as the choice sees it: -inf for what is never chosen, +inf as the
+// largest finite value.
+template <bool WIDE>
+NVFP4_DEV float open_logit(float v) {
+  return v > -INFINITY ? fminf(v, WIDE ? 3.402823466e38f : 3.3895314e38f) : -INFINITY;
+}
+
+// Unsigned order of the floats, 0 for -inf and NaN; +-0 are equal.
+NVFP4_DEV uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+NVFP4_DEV double shfl_xor_double(double v, int o) {
+  return __hiloint2double(__shfl_xor_sync(0xFFFFFFFFu, __double2hiint(v), o),
+                          __shfl_xor_sync(0xFFFFFFFFu, __double2loint(v), o));
+}
+NVFP4_DEV double shfl_double(double v, int l) {
+  return __hiloint2double(__shfl_sync(0xFFFFFFFFu, __double2hiint(v), l),
+                          __shfl_sync(0xFFFFFFFFu, __double2loint(v), l));
+}
+
+// The expert of slot `lane` (-1: none) of token t, in FP64.
 template <int NI, bool WIDE>
+__device__ __noinline__ int choose_exact(const RouteArgs& a, int64_t t) {
+  const int lane = threadIdx.x & 31;
+  const double none = -__longlong_as_double(0x7FF0000000000000ll);
+  const Share mine = lane_share(a, lane);
+  float l[NI], most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    l[i] = i < mine.count ? open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + mine.first + i))
+                          : -INFINITY;
+    most = fmaxf(most, l[i]);
+  }
+  most = warp_max(most);
+  double key[NI], all = 0.0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const bool open = l[i] > -INFINITY;
+    if (a.score == NVFP4_SCORE_SIGMOID)
+      key[i] = open ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
+    else
+      key[i] = open ? exp((double)l[i] - (double)most) : 0.0;
+    all += key[i];
+  }
+  if (a.score == NVFP4_SCORE_SOFTMAX) {
+    for (int o = 16; o; o >>= 1) all += shfl_xor_double(all, o);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) key[i] = all > 0.0 ? key[i] / all : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const bool open = l[i] > -INFINITY;
+    if (a.bias && open) key[i] += (double)a.bias[mine.first + i];
+    if (!open || !(key[i] > none)) {
+      key[i] = none;
+      l[i] = -INFINITY;
+    }
+  }
+  if (a.groups > 1) {
+    // the two best of the group; by one alone and without a bias the logits decide
+    const bool raw = !a.bias && a.group_top == 1;
+    double best = none, next = none;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const double v = raw ? (double)l[i] : key[i];
+      next = fmax(next, fmin(best, v));
+      best = fmax(best, v);
+    }
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      const double b = shfl_xor_double(best, o), n = shfl_xor_double(next, o);
+      next = fmax(fmax(next, n), fmin(best, b));
+      best = fmax(best, b);
+    }
+    const double worth = best + (a.group_top == 2 && next > none ? next : 0.0);
+    const int g = lane / a.lanes;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const double w = shfl_double(worth, h * a.lanes);
+      rank += w > worth || (w == worth && h < g);
+    }
+    if (rank >= a.kept) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        key[i] = none;
+        l[i] = -INFINITY;
+      }
+    }
+  }
+  if (!a.bias)
+#pragma unroll
+    for (int i = 0; i < NI; ++i) key[i] = (double)l[i];
+  int expert = -1;
+  for (int j = 0; j < a.top; ++j) {
+    double best = none;
+    int e = INT_MAX;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        e = mine.first + i;
+      }
+    for (int o = 16; o; o >>= 1) {
+      const double b = shfl_xor_double(best, o);
+      const int f = __shfl_xor_sync(0xFFFFFFFFu, e, o);
+      if (b > best || (b == best && f < e)) {
+        best = b;
+        e = f;
+      }
+    }
+    if (e == INT_MAX) break;
+    if (lane == j) expert = e;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (mine.first + i == e) key[i] = none;
+  }
+  return expert;
+}
+
+// The weight of slot `lane` from its logit l (-inf: none).  A sigmoid's share is
+// taken of e^l where all are far below what FP32 holds.  all: the softmax's
+// denominator about `most`, where the weights are parts of all experts.
+NVFP4_DEV float slot_weight(const RouteArgs& a, float l, float most, float all) {
+  const bool some = l > -INFINITY;
+  if (a.score == NVFP4_SCORE_SOFTMAX && !a.renorm)
+    return some ? a.scale * (expf(l - most) / all) : 0.0f;
+  float u;
+  if (a.renorm) {
+    const float top = warp_max(l);
+    if (a.score == NVFP4_SCORE_SIGMOID && top > -60.0f)
+      u = 1.0f / (1.0f + expf(-l));
+    else
+      u = expf(l - top);
+    u = some ? u : 0.0f;
+    const float total = warp_sum(u);
+    return some ? a.scale * (u / total) : 0.0f;
+  }
+  return some ? a.scale * (1.0f / (1.0f + expf(-l))) : 0.0f;
+}
+
+// Experts and weights of token t by their scores, one warp.  bias: of this lane's
+// experts.
+template <int NI, bool WIDE>
+NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
+                             const float (&bias)[NI], int* hist) {
+  const int lane = threadIdx.x & 31;
+  float v[NI], l_most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    v[i] = i < mine.count ? open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + mine.first + i))
+                          : -INFINITY;
+    l_most = fmaxf(l_most, v[i]);
+  }
+  const bool softmax = a.score == NVFP4_SCORE_SOFTMAX;
+  float all = 1.0f, inv = 1.0f;
+  if (softmax) {
+    l_most = fmaxf(warp_max(l_most), -3.402823466e38f);
+    if (a.bias || !a.renorm) {
+      all = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) all += expf(v[i] - l_most);
+      all = warp_sum(all);
+      inv = all > 0.0f ? 1.0f / all : 0.0f;
+    }
+  }
+  // keys, and how near two may be to be told apart: the scores are good to 3e-7
+  // (the softmax's to 2e-6 of the largest), a sum to half a step more
+  uint32_t key[NI];
+  const float near0 = softmax ? 5e-6f * inv : 1e-6f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    float k = v[i];
+    if (a.bias) {
+      const float s = softmax ? expf(v[i] - l_most) * inv
+                              : __fdividef(1.0f, 1.0f + __expf(fminf(-v[i], 80.0f)));
+      k = v[i] > -INFINITY ? s + bias[i] : -INFINITY;
+    }
+    key[i] = order_key(k);
+  }
+  bool doubt = false;
+  if (a.groups > 1) {
+    uint32_t best = 0u, next = 0u;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      next = max(next, min(best, key[i]));
+      best = max(best, key[i]);
+    }
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      const uint32_t n = __shfl_xor_sync(0xFFFFFFFFu, next, o);
+      next = max(max(next, n), min(best, b));
+      best = max(best, b);
+    }
+    float worth = key_value<true>(max(best, 1u)), size = fabsf(worth), near = 0.0f;
+    if (a.group_top == 2) {
+      const float second = key_value<true>(max(next, 1u));
+      if (a.bias) {
+        worth = next ? worth + second : worth;
+        size += next ? fabsf(second) : 0.0f;
+      } else if (softmax) {
+        worth = expf(worth - l_most) + (next ? expf(second - l_most) : 0.0f);
+        near = 1e-5f * worth;
+      } else {
+        worth = 1.0f / (1.0f + expf(-worth)) + (next ? 1.0f / (1.0f + expf(-second)) : 0.0f);
+        near = 2e-6f * worth;
+      }
+    }
+    if (a.bias) near = 2.0f * near0 + 1e-6f * size;
+    const uint32_t w = best ? order_key(worth) : 0u;
+    const int g = lane / a.lanes;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+      const uint32_t u = __shfl_sync(0xFFFFFFFFu, w, h * a.lanes);
+      rank += u > w || (u == w && h < g);
+    }
+    const bool keep = rank < a.kept;
+    if (a.bias || a.group_top == 2) {
+      const uint32_t in = __reduce_min_sync(0xFFFFFFFFu, keep ? w : 0xFFFFFFFFu);
+      const uint32_t out = __reduce_max_sync(0xFFFFFFFFu, keep ? 0u : w);
+      const float margin = __uint_as_float(
+          __reduce_max_sync(0xFFFFFFFFu, __float_as_uint((w == in || w == out) ? near : 0.0f)));
+      doubt = out != 0u && key_value<true>(in) - key_value<true>(out) <= margin;
+    }
+    if (!keep)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) key[i] = 0u;
+  }
+  int expert = -1;
+  float last = INFINITY;
+  int last_e = -1;
+  // with a bias one round more, for the gap behind the last slot
+  const int rounds = a.bias ? a.top + 1 : a.top;
+  for (int j = 0; j < rounds && !doubt; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) best = max(best, key[i]);
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (m == 0u) break;
+    int at = 0;
+#pragma unroll
+    for (int i = NI - 1; i >= 0; --i) at = key[i] == m ? i : at;
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+    const int e = __shfl_sync(0xFFFFFFFFu, mine.first + at, from);
+    if (a.bias) {
+      const float k = key_value<true>(m);
+      if (last - k <= near0 * (softmax ? 1.0f : fmaxf(1.0f, fabsf(k))) + 5e-7f * fabsf(k)) {
+        // equal logits with equal biases are equal in any arithmetic
+        const float p = load_logit<WIDE>(a.logits, t * a.ld + last_e);
+        const float q = load_logit<WIDE>(a.logits, t * a.ld + e);
+        doubt = !(p == q && a.bias[last_e] == a.bias[e]);
+      }
+      last = k;
+      last_e = e;
+    }
+    if (lane == j && j < a.top) expert = e;
+    if (lane == from)
+#pragma unroll
+      for (int i = 0; i < NI; ++i) key[i] = i == at ? 0u : key[i];
+  }
+  if (doubt) expert = choose_exact<NI, WIDE>(a, t);
+  float l = -INFINITY;
+  if (expert >= 0) l = open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + expert));
+  const float weight = slot_weight(a, l, l_most, all);
+  if (lane < a.top) {
+    a.expert[t * a.top + lane] = expert;
+    a.weight[t * a.top + lane] = weight;
+    if (expert >= 0) atomicAdd(&hist[expert], 1);
+  }
+}
+
+// Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
+template <int NI, bool WIDE, bool SCORED>
 NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) hist[e] = 0;
   for (int64_t r = (int64_t)blockIdx.x * kChooseThreads + threadIdx.x; r < a.rows;
@@ -184,9 +482,18 @@ NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
   __syncthreads();
   int t, t1;
   warp_tokens(a, kChooseWarps, t, t1);
-  if (NI <= 8)  // more would not leave registers for two tokens
-    for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
-  for (; t < t1; ++t) choose_tokens<NI, WIDE, 1>(a, t, hist);
+  if constexpr (SCORED) {
+    const Share mine = lane_share(a, threadIdx.x & 31);
+    float bias[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      bias[i] = a.bias && i < mine.count ? a.bias[mine.first + i] : 0.0f;
+    for (; t < t1; ++t) choose_scored<NI, WIDE>(a, t, mine, bias, hist);
+  } else {
+    if (NI <= 8)  // more would not leave registers for two tokens
+      for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
+    for (; t < t1; ++t) choose_tokens<NI, WIDE, 1>(a, t, hist);
+  }
   __syncthreads();
 }
 
@@ -264,11 +571,11 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
   }
 }
 
-template <int NI, bool WIDE>
+template <int NI, bool WIDE, bool SCORED>
 __global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
   griddep_wait();
-  choose<NI, WIDE>(a, hist);
+  choose<NI, WIDE, SCORED>(a, hist);
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads)
     a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
@@ -328,11 +635,11 @@ __global__ void __launch_bounds__(kThreads) route_assign_kernel(const RouteArgs 
   assign(a, s.before, s.total, s.offset, s.base);
 }
 
-template <int NI, bool WIDE>
+template <int NI, bool WIDE, bool SCORED>
 __global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
-  choose<NI, WIDE>(a, s.total);
+  choose<NI, WIDE, SCORED>(a, s.total);
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) s.before[e] = 0;
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);
@@ -342,6 +649,9 @@ __global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const Route
 // over all experts the unchosen, whose weights have no gradient, add their
 // share of probability times dw_i, and themselves get -p sum_j w_j dw_j.  The
 // differences keep the result exact where one weight is near 1.
+// With a scale c the other weights count as w_j / c; a sigmoid's logits get their
+// share times 1 - s_i, and nothing of the others' where the weights are not
+// renormalised: w_i (1 - s_i) dw_i.
 // A token's row lies in shared memory: the lanes of its slots put theirs
 // into it.
 template <int NI, bool WIDE>
@@ -364,10 +674,16 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) 
     }
   }
   float apart = 0.0f;
-  for (int j = 0; j < a.top; ++j)
-    apart += __shfl_sync(0xFFFFFFFFu, w, j) * (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
+  if (a.renorm || a.score == NVFP4_SCORE_SOFTMAX)
+    for (int j = 0; j < a.top; ++j)
+      apart += (__shfl_sync(0xFFFFFFFFu, w, j) * a.inv_scale) *
+               (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
+  else
+    apart = dw;
+  if (a.score == NVFP4_SCORE_SIGMOID && e >= 0)
+    apart *= 1.0f / (1.0f + expf(load_logit<WIDE>(a.logits, t * a.ld + e)));
   float other = 0.0f;  // what an unchosen expert's probability is multiplied by
-  if (a.mode == NVFP4_ROUTE_ALL) {
+  if (a.score == NVFP4_SCORE_SOFTMAX && !a.renorm) {
     other = -warp_sum(w * dw);
     float v[NI];
     uint32_t key[NI], best = 0u;
@@ -411,6 +727,25 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) 
         static_cast<__nv_bfloat16*>(a.dlogits)[t * a.experts + c] = __float2bfloat16_rn(p[c]);
     }
   }
+}
+
+// bias_e += rate sign(mean load - load_e), compared as total - load_e experts.
+__global__ void __launch_bounds__(kMaxExperts) route_balance_kernel(const int32_t* sizes, int experts,
+                                                                    float rate, float* bias) {
+  __shared__ long long part[kMaxExperts / 32];
+  griddep_wait();
+  const int e = threadIdx.x;
+  const long long size = e < experts ? sizes[e] : 0;
+  long long total = size;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  if ((e & 31) == 0) part[e >> 5] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kMaxExperts / 32; ++w) total += part[w];
+  const long long gap = total - size * experts;
+  if (e < experts && gap) bias[e] += gap > 0 ? rate : -rate;
 }
 
 // ---- rows to the experts and back ------------------------------------------------
@@ -595,10 +930,12 @@ nvfp4_status check_route(int64_t tokens, int64_t experts, int32_t top) {
   return NVFP4_OK;
 }
 
-template <int NI, bool WIDE>
+template <int NI, bool WIDE, bool SCORED>
 cudaError_t launch_route(RouteArgs& a, int ctas, cudaStream_t stream) {
-  if (ctas == 1) return launch_pdl(route_small_kernel<NI, WIDE>, 1, kChooseThreads, 0, stream, a);
-  const cudaError_t e = launch_pdl(route_choose_kernel<NI, WIDE>, ctas, kChooseThreads, 0, stream, a);
+  if (ctas == 1)
+    return launch_pdl(route_small_kernel<NI, WIDE, SCORED>, 1, kChooseThreads, 0, stream, a);
+  const cudaError_t e =
+      launch_pdl(route_choose_kernel<NI, WIDE, SCORED>, ctas, kChooseThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   const cudaError_t f = launch_pdl(route_scan_kernel, (a.experts + 31) / 32, 1024, 0, stream, a);
   if (f != cudaSuccess) return f;
@@ -611,13 +948,24 @@ cudaError_t launch_route_bwd(RouteArgs& a, cudaStream_t stream) {
   return launch_pdl(route_bwd_kernel<NI, WIDE>, dim3((unsigned)ctas), kThreads, 0, stream, a);
 }
 
-// Calls F<NI, WIDE> for a number of experts.
-#define NVFP4_ROUTE_CALL(F, experts, wide, ...)                                        \
-  ((experts) <= 32    ? ((wide) ? F<1, true>(__VA_ARGS__) : F<1, false>(__VA_ARGS__))  \
-   : (experts) <= 64  ? ((wide) ? F<2, true>(__VA_ARGS__) : F<2, false>(__VA_ARGS__))  \
-   : (experts) <= 128 ? ((wide) ? F<4, true>(__VA_ARGS__) : F<4, false>(__VA_ARGS__))  \
-   : (experts) <= 256 ? ((wide) ? F<8, true>(__VA_ARGS__) : F<8, false>(__VA_ARGS__))  \
-                      : ((wide) ? F<16, true>(__VA_ARGS__) : F<16, false>(__VA_ARGS__)))
+// The routing and its backward for the least NI that holds a number of experts in
+// 32 lanes.
+template <bool WIDE, bool SCORED>
+cudaError_t call_route(int64_t experts, RouteArgs& a, int ctas, cudaStream_t s) {
+  return experts <= 32    ? launch_route<1, WIDE, SCORED>(a, ctas, s)
+         : experts <= 64  ? launch_route<2, WIDE, SCORED>(a, ctas, s)
+         : experts <= 128 ? launch_route<4, WIDE, SCORED>(a, ctas, s)
+         : experts <= 256 ? launch_route<8, WIDE, SCORED>(a, ctas, s)
+                          : launch_route<16, WIDE, SCORED>(a, ctas, s);
+}
+template <bool WIDE>
+cudaError_t call_route_bwd(int64_t experts, RouteArgs& a, cudaStream_t s) {
+  return experts <= 32    ? launch_route_bwd<1, WIDE>(a, s)
+         : experts <= 64  ? launch_route_bwd<2, WIDE>(a, s)
+         : experts <= 128 ? launch_route_bwd<4, WIDE>(a, s)
+         : experts <= 256 ? launch_route_bwd<8, WIDE>(a, s)
+                          : launch_route_bwd<16, WIDE>(a, s);
+}
 
 nvfp4_status check_move(int64_t tokens, int64_t cols, int32_t top, int64_t rows) {
   if (tokens <= 0 || cols <= 0 || cols % 8 || cols > INT32_MAX / 2 || top <= 0 || top > kMaxTop ||
@@ -660,21 +1008,21 @@ nvfp4_status route_sizes_impl(int64_t tokens, int64_t experts, int32_t top, int6
   return NVFP4_OK;
 }
 
-nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
-                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
-                            int32_t* expert, float* weight, int32_t* sizes, int32_t* offsets,
-                            int32_t* row, int32_t* source, void* workspace,
-                            size_t workspace_bytes, cudaStream_t stream) {
+// What the two forms of the routing share behind their own checks.
+static nvfp4_status route_fwd(const void* logits, int32_t in_dtype, int64_t tokens, int64_t experts,
+                              int64_t ld, int32_t top, int32_t* expert, float* weight,
+                              int32_t* sizes, int32_t* offsets, int32_t* row, int32_t* source,
+                              void* workspace, size_t workspace_bytes, RouteArgs a, bool scored,
+                              cudaStream_t stream) {
   if (!logits || !expert || !weight || !sizes || !offsets || !row || !source)
     return NVFP4_ERR_INVALID_ARG;
   if (in_dtype != NVFP4_IN_BF16 && in_dtype != NVFP4_IN_FP32) return NVFP4_ERR_INVALID_ARG;
-  if (mode != NVFP4_ROUTE_ALL && mode != NVFP4_ROUTE_CHOSEN) return NVFP4_ERR_INVALID_ARG;
   nvfp4_status st = check_route(tokens, experts, top);
   if (st != NVFP4_OK) return st;
   if (ld < experts) return NVFP4_ERR_SHAPE;
   const bool wide = in_dtype == NVFP4_IN_FP32;
   if ((reinterpret_cast<uintptr_t>(logits) & (wide ? 3u : 1u)) || !a4(expert) || !a4(weight) ||
-      !a4(sizes) || !a4(offsets) || !a4(row) || !a4(source))
+      !a4(sizes) || !a4(offsets) || !a4(row) || !a4(source) || !a4(a.bias))
     return NVFP4_ERR_ALIGN;
   if (!workspace || !a4(workspace) ||
       workspace_bytes < (size_t)(kMaxSms + 1) * experts * sizeof(int32_t))
@@ -682,13 +1030,11 @@ nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens
   DeviceInfo dev;
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
-  RouteArgs a = {};
   a.logits = logits;
   a.ld = ld;
   a.tokens = (int)tokens;
   a.experts = (int)experts;
   a.top = top;
-  a.mode = mode;
   a.expert = expert;
   a.weight = weight;
   a.sizes = sizes;
@@ -700,16 +1046,20 @@ nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens
   int ctas = route_ctas(tokens, dev.sm_count);
   a.per_cta = (int)((tokens + ctas - 1) / ctas);
   ctas = a.ctas = (int)((tokens + a.per_cta - 1) / a.per_cta);
-  return cuda_status(NVFP4_ROUTE_CALL(launch_route, experts, wide, a, ctas, stream));
+  if (!scored)
+    return cuda_status(wide ? call_route<true, false>(experts, a, ctas, stream)
+                            : call_route<false, false>(experts, a, ctas, stream));
+  // a lane's experts decide how many registers hold them
+  return cuda_status(wide ? call_route<true, true>(32 * a.per, a, ctas, stream)
+                          : call_route<false, true>(32 * a.per, a, ctas, stream));
 }
 
-nvfp4_status route_bwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
-                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
-                            const int32_t* expert, const float* weight, const float* dweight,
-                            void* dlogits, cudaStream_t stream) {
+static nvfp4_status route_bwd(const void* logits, int32_t in_dtype, int64_t tokens, int64_t experts,
+                              int64_t ld, int32_t top, const int32_t* expert, const float* weight,
+                              const float* dweight, void* dlogits, RouteArgs a,
+                              cudaStream_t stream) {
   if (!logits || !expert || !weight || !dweight || !dlogits) return NVFP4_ERR_INVALID_ARG;
   if (in_dtype != NVFP4_IN_BF16 && in_dtype != NVFP4_IN_FP32) return NVFP4_ERR_INVALID_ARG;
-  if (mode != NVFP4_ROUTE_ALL && mode != NVFP4_ROUTE_CHOSEN) return NVFP4_ERR_INVALID_ARG;
   nvfp4_status st = check_route(tokens, experts, top);
   if (st != NVFP4_OK) return st;
   if (ld < experts) return NVFP4_ERR_SHAPE;
@@ -721,19 +1071,115 @@ nvfp4_status route_bwd_impl(const void* logits, int32_t in_dtype, int64_t tokens
   DeviceInfo dev;
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
-  RouteArgs a = {};
   a.logits = logits;
   a.ld = ld;
   a.tokens = (int)tokens;
   a.experts = (int)experts;
   a.top = top;
-  a.mode = mode;
   a.expert = const_cast<int32_t*>(expert);
   a.weight = const_cast<float*>(weight);
   a.dweight = dweight;
   a.dlogits = dlogits;
-  return cuda_status(NVFP4_ROUTE_CALL(launch_route_bwd, experts, wide, a, stream));
+  return cuda_status(wide ? call_route_bwd<true>(experts, a, stream)
+                          : call_route_bwd<false>(experts, a, stream));
 }
+
+static RouteArgs plain_route(int32_t mode) {
+  RouteArgs a = {};
+  a.mode = mode;
+  a.score = NVFP4_SCORE_SOFTMAX;
+  a.renorm = mode == NVFP4_ROUTE_CHOSEN;
+  a.inv_scale = 1.0f;
+  return a;
+}
+
+nvfp4_status route_fwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
+                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                            int32_t* expert, float* weight, int32_t* sizes, int32_t* offsets,
+                            int32_t* row, int32_t* source, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream) {
+  if (mode != NVFP4_ROUTE_ALL && mode != NVFP4_ROUTE_CHOSEN) return NVFP4_ERR_INVALID_ARG;
+  return route_fwd(logits, in_dtype, tokens, experts, ld, top, expert, weight, sizes, offsets, row,
+                   source, workspace, workspace_bytes, plain_route(mode), false, stream);
+}
+
+nvfp4_status route_bwd_impl(const void* logits, int32_t in_dtype, int64_t tokens,
+                            int64_t experts, int64_t ld, int32_t top, int32_t mode,
+                            const int32_t* expert, const float* weight, const float* dweight,
+                            void* dlogits, cudaStream_t stream) {
+  if (mode != NVFP4_ROUTE_ALL && mode != NVFP4_ROUTE_CHOSEN) return NVFP4_ERR_INVALID_ARG;
+  return route_bwd(logits, in_dtype, tokens, experts, ld, top, expert, weight, dweight, dlogits,
+                   plain_route(mode), stream);
+}
+
+// The arguments of a scored choice; a group takes a power of two of the lanes.
+static nvfp4_status scored_args(const nvfp4_route_params* p, const float* bias, RouteArgs* a) {
+  if (!p) return NVFP4_ERR_INVALID_ARG;
+  if ((p->score != NVFP4_SCORE_SOFTMAX && p->score != NVFP4_SCORE_SIGMOID) ||
+      p->renormalise < 0 || p->renormalise > 1 || !(p->scale > 0.0f) || !std::isfinite(p->scale))
+    return NVFP4_ERR_INVALID_ARG;
+  const nvfp4_status st = check_route(p->tokens, p->experts, p->top);
+  if (st != NVFP4_OK) return st;
+  if (p->groups < 1 || p->groups > 32 || (p->groups & (p->groups - 1)) ||
+      p->experts % p->groups || p->groups_kept < 1 || p->groups_kept > p->groups ||
+      p->group_top < 1 || p->group_top > 2 || p->top > p->groups_kept * (p->experts / p->groups))
+    return NVFP4_ERR_SHAPE;
+  *a = {};
+  a->bias = bias;
+  a->score = p->score;
+  a->renorm = p->renormalise;
+  a->groups = p->groups;
+  a->kept = p->groups_kept;
+  a->group_top = p->group_top;
+  a->group_size = (int)(p->experts / p->groups);
+  a->lanes = 32 / p->groups;
+  a->per = (a->group_size + a->lanes - 1) / a->lanes;
+  a->scale = p->scale;
+  a->inv_scale = 1.0f / p->scale;
+  return NVFP4_OK;
+}
+
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" nvfp4_status nvfp4_route_scored_fwd(const nvfp4_route_params* p, const void* logits,
+                                               const float* bias, int32_t* expert, float* weight,
+                                               int32_t* sizes, int32_t* offsets, int32_t* row,
+                                               int32_t* source, void* workspace,
+                                               size_t workspace_bytes, nvfp4_stream stream) {
+  RouteArgs a;
+  const nvfp4_status st = scored_args(p, bias, &a);
+  if (st != NVFP4_OK) return st;
+  return route_fwd(logits, p->in_dtype, p->tokens, p->experts, p->ld, p->top, expert, weight, sizes,
+                   offsets, row, source, workspace, workspace_bytes, a, true,
+                   static_cast<cudaStream_t>(stream));
+}
+
+extern "C" nvfp4_status nvfp4_route_scored_bwd(const nvfp4_route_params* p, const void* logits,
+                                               const int32_t* expert, const float* weight,
+                                               const float* dweight, void* dlogits,
+                                               nvfp4_stream stream) {
+  RouteArgs a;
+  const nvfp4_status st = scored_args(p, nullptr, &a);
+  if (st != NVFP4_OK) return st;
+  return route_bwd(logits, p->in_dtype, p->tokens, p->experts, p->ld, p->top, expert, weight,
+                   dweight, dlogits, a, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" nvfp4_status nvfp4_route_balance(const int32_t* sizes, int64_t experts, float rate,
+                                            float* bias, nvfp4_stream stream) {
+  if (!sizes || !bias || !std::isfinite(rate)) return NVFP4_ERR_INVALID_ARG;
+  if (experts < 1 || experts > kMaxExperts) return NVFP4_ERR_SHAPE;
+  if (!a4(sizes) || !a4(bias)) return NVFP4_ERR_ALIGN;
+  DeviceInfo dev;
+  const nvfp4_status st = current_device(&dev);
+  if (st != NVFP4_OK) return st;
+  return cuda_status(launch_pdl(route_balance_kernel, 1, kMaxExperts, 0,
+                                static_cast<cudaStream_t>(stream), sizes, (int)experts, rate, bias));
+}
+
+namespace nvfp4 {
 
 nvfp4_status dispatch_impl(const void* x, const int32_t* row, const int32_t* source,
                            int64_t tokens, int64_t cols, int32_t top, int64_t rows, void* xe,
