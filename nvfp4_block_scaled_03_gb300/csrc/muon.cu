@@ -28,14 +28,11 @@
 // in bf16 3e-1); rounding it to bf16 costs 1.7e-3.
 #include <cmath>
 
-#include "gemm_common.cuh"
-
-#include <cuda_fp16.h>
+#include "muon_common.cuh"
 
 namespace nvfp4 {
 namespace {
 
-constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
 constexpr int kTile = 256;  // rows and columns of a CTA pair's tile
 constexpr int kBK = 64;     // contraction elements of a stage, 128 bytes
 
@@ -63,24 +60,8 @@ struct NsArgs {
 // A warp goes on only together: its lanes may give up at a wait one by one.
 NVFP4_DEV bool all_waited(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 
-// MN-major operand tile: boxes of 64 (along M or N) x 64 (along K), a row of
-// 128 bytes for each k with the 128-byte swizzle, 8 rows (1024 bytes) a swizzle
-// atom; the next 64 of M or N lie a box further.
+// An MN-major operand lies in boxes of 64 (along M or N) x 64 (along K).
 constexpr uint32_t kBoxMN = 64 * kBK * 2;
-NVFP4_DEV uint64_t smem_desc_mn(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(kBoxMN >> 4) << 16;  // leading byte offset: the next 64 of M or N
-  d |= (uint64_t)(1024 >> 4) << 32;    // stride byte offset: the next 8 of K
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;              // SWIZZLE_128B
-  return d;
-}
-
-// Instruction descriptor for kind::f16: f16 A and B, FP32 accumulators.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 
 NVFP4_DEV void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                uint32_t accumulate) {
@@ -114,14 +95,6 @@ NVFP4_DEV void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int
           reinterpret_cast<uint64_t>(map)),
       "r"(src), "r"(x), "r"(y), "r"(z)
       : "memory");
-}
-
-NVFP4_DEV uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-NVFP4_DEV float2 unpack_f16x2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 // A 32 x 32 box of 16-bit values in shared memory, rows of 64 bytes with the
@@ -330,8 +303,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NsLayout<KIND>::kThr
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j) {
             if (16 * j >= left) break;
-            const uint64_t ad = AMN ? smem_desc_mn(sa + 2048 * j) : smem_desc_sw128(sa + 32 * j);
-            const uint64_t bd = BMN ? smem_desc_mn(sb + 2048 * j) : smem_desc_sw128(sb + 32 * j);
+            const uint64_t ad = AMN ? smem_desc_mn(sa + 2048 * j, kBoxMN) : smem_desc_sw128(sa + 32 * j);
+            const uint64_t bd = BMN ? smem_desc_mn(sb + 2048 * j, kBoxMN) : smem_desc_sw128(sb + 32 * j);
             tc_mma_pair_f16(tmem + b * kTile, ad, bd, idesc, kb | j ? 1u : 0u);
           }
           st_shared_u8(inject + warp, 1u);
@@ -556,19 +529,6 @@ struct MomentumArgs {
   int nesterov, zero;
 };
 
-template <bool WIDE>
-NVFP4_DEV float grad_at(const void* g, int64_t i) {
-  if (WIDE) return static_cast<const float*>(g)[i];
-  return __uint_as_float((uint32_t) static_cast<const uint16_t*>(g)[i] << 16);
-}
-template <bool WIDE>
-NVFP4_DEV float4 grad4_at(const void* g, int64_t i) {
-  if (WIDE) return *reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
-  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + i);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                     __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
-}
-
 NVFP4_DEV float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
@@ -746,11 +706,10 @@ struct Layout {
   int64_t ldx, ldm, dstride;
   size_t x_bytes, g_bytes, d_bytes;
   size_t total;
+  bool panel;
 };
 constexpr int kMaxParts = 1024;
 constexpr int64_t kMaxSide = 1 << 20;
-
-size_t up(size_t v) { return (v + 1023) / 1024 * 1024; }
 
 nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
   if (batch <= 0 || rows <= 0 || cols <= 0 || batch > 65535 || rows > kMaxSide || cols > kMaxSide)
@@ -763,10 +722,13 @@ nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
   l->dstride = (l->m + 31) / 32 * 32;
   const int64_t tm = (l->m + 255) / 256, tn = (l->n + 255) / 256;
   if (tm * tn * batch > INT32_MAX / 2) return NVFP4_ERR_SHAPE;
-  l->x_bytes = up((size_t)batch * rows * l->ldx * 2);
-  l->g_bytes = up((size_t)batch * l->m * l->ldm * 2);
-  l->d_bytes = up((size_t)batch * l->dstride * 4);
-  l->total = 3 * l->x_bytes + 2 * l->g_bytes + 2 * l->d_bytes + up((size_t)batch * kMaxParts * 4);
+  l->x_bytes = up1k((size_t)batch * rows * l->ldx * 2);
+  l->g_bytes = up1k((size_t)batch * l->m * l->ldm * 2);
+  l->d_bytes = up1k((size_t)batch * l->dstride * 4);
+  l->panel = muon_panel_fits(rows, cols);
+  l->total = l->panel ? muon_panel_workspace(rows, cols)
+                      : 3 * l->x_bytes + 2 * l->g_bytes + 2 * l->d_bytes +
+                            up1k((size_t)batch * kMaxParts * 4);
   return NVFP4_OK;
 }
 
@@ -781,7 +743,7 @@ nvfp4_status muon_set_injection(unsigned int stall, unsigned long long wait_ns) 
   if (cudaMemcpyToSymbol(g_gemm_stall, &stall, sizeof(stall)) != cudaSuccess ||
       cudaMemcpyToSymbol(g_gemm_wait_ns, &wait_ns, sizeof(wait_ns)) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  return NVFP4_OK;
+  return muon_panel_set_injection(stall, wait_ns);
 }
 
 nvfp4_status muon_read_error(unsigned int* code) {
@@ -789,8 +751,10 @@ nvfp4_status muon_read_error(unsigned int* code) {
   if (cudaMemcpyFromSymbol(&v, g_gemm_error, sizeof(v)) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (v && cudaMemcpyToSymbol(g_gemm_error, &zero, sizeof(zero)) != cudaSuccess)
     return NVFP4_ERR_CUDA;
-  *code = v;
-  return NVFP4_OK;
+  unsigned int panel = 0;
+  const nvfp4_status st = muon_panel_read_error(&panel);
+  *code = v ? v : panel;
+  return st;
 }
 
 }  // namespace nvfp4
@@ -833,6 +797,9 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   st = current_device(&dev);
   if (st != NVFP4_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (l.panel)
+    return muon_panel({p, grad, momentum, static_cast<__nv_bfloat16*>(update), wide,
+                       (flags & NVFP4_ZERO_GRAD) != 0, workspace, dev.sm_count, s});
 
   uint8_t* w = static_cast<uint8_t*>(workspace);
   void* hi[2] = {w, w + l.x_bytes};
