@@ -33,43 +33,68 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kTile = 256;  // rows and columns of a CTA pair's tile
 constexpr int kBK = 64;     // contraction elements of a stage, 128 bytes
-
-// What a product computes and what becomes of it.
-enum {
-  kGram = 0,    // E, D of X X^T; symmetric
-  kPoly = 1,    // F, D' from E E; symmetric
-  kUpdate = 2,  // X' = (a + d') X + F X
-  kFinal = 3    // the same, stored as bf16
-};
-
-struct NsArgs {
-  int m, n, k;             // the product's rows, columns and contraction
-  int tiles_m, tiles_n;
-  int tiles_per, tiles;    // of a matrix, of all
-  float a, b, c;
-  int by_col;              // update: d' belongs to the columns (tall matrices)
-  const float* din;        // poly: d; update: d'
-  float* dout;             // gram: d; poly: d'
-  int64_t dstride;         // from one matrix's diagonal to the next's
-  __nv_bfloat16* out;      // final
-  int out_boxes;           // final: rows are whole multiples of 16 bytes
-};
 
 // A warp goes on only together: its lanes may give up at a wait one by one.
 NVFP4_DEV bool all_waited(bool ok) { return __all_sync(0xFFFFFFFFu, ok); }
 
+// One lane of a converged warp, the same every time.  A role's warp runs its loop
+// together and has this lane issue what one thread issues: its operands are uniform
+// then, and a stage costs its producer and its MMA thread 150 cycles, 500 with the
+// whole loop in one lane's branch.
+NVFP4_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // An MN-major operand lies in boxes of 64 (along M or N) x 64 (along K).
 constexpr uint32_t kBoxMN = 64 * kBK * 2;
 
-NVFP4_DEV void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                               uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// One product over a stack of matrices, and what becomes of it.  With r a result of
+// the tensor cores, x what the chunk brings in (nothing, E, or X's two halves) and d
+// the diagonal's entries of its row and column, all of them are
+//   v = (p + q (d_i + d_j)) x + s r
+// and on a symmetric product's diagonal  p d_i + q d_i^2 + t r, which goes to dout:
+//   E, D of X X^T       p = q = 0, s = 2^-12, t = 2^-24
+//   F, D' from E E      p = b, q = c, s = c 2^-12, t = c 2^-24
+//   X' = (a + d') X + F X   p = a, q = 1, s = 2^-12, d' of the rows or the columns
+// (One formula, and one code for all of them: where a launch goes through every kind
+// of product, code of their own for each, 20 KB a kind, came anew from memory at each.)
+struct NsArgs {
+  int m, n, k;             // its rows, columns and contraction
+  int tiles_m, tiles_n;
+  int tiles_per, tiles;    // of a matrix, of all
+  int a_mn, b_mn;          // operands whose contraction does not lie along their rows
+  int symmetric;
+  int loads;               // boxes that a chunk brings in
+  int by_row, by_col;      // whose diagonal entries count
+  int final;               // the result is stored as bf16, not as f16 (and lo)
+  float p, q, s, t;
+  const float* din;
+  float* dout;
+  int64_t dstride;         // from one matrix's diagonal to the next's
+  __nv_bfloat16* out;      // final
+  int out_boxes;           // final: rows are whole multiples of 16 bytes
+};
+struct NsMaps {
+  const CUtensorMap *a, *b, *in0, *in1, *out0, *out1;
+};
+
+NVFP4_DEV void tc_mma_f16(bool pair, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                          uint32_t idesc, uint32_t accumulate) {
+  if (pair)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 NVFP4_DEV void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster,
@@ -96,6 +121,8 @@ NVFP4_DEV void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x, int
       "r"(src), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// Between what the generic proxy sees and what tensor copies read or wrote.
+NVFP4_DEV void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // A 32 x 32 box of 16-bit values in shared memory, rows of 64 bytes with the
 // 64-byte swizzle: 16-byte piece p of row r.
@@ -134,41 +161,26 @@ NVFP4_DEV void box_transpose(uint32_t from, uint32_t to, int lane) {
   }
 }
 
-// Tile t of a matrix: by rows of the lower triangle where the result is
-// symmetric, else with the matrix's smaller side running fastest: tiles at work
-// together then read X, the operand that L2 may not hold, once (14336 x 4096: an
-// update 375 us the other way round, 488 ns a stage).
-template <int KIND>
-NVFP4_DEV void tile_of(int t, const NsArgs& a, int& tm, int& tn) {
-  if (KIND <= kPoly) {
-    tm = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-    while ((tm + 1) * (tm + 2) / 2 <= t) ++tm;
-    while (tm * (tm + 1) / 2 > t) --tm;
-    tn = t - tm * (tm + 1) / 2;
-  } else {
-    const int fast = min(a.tiles_m, a.tiles_n), slow = t / fast;
-    tm = a.tiles_m > a.tiles_n ? slow : t - slow * fast;
-    tn = a.tiles_m > a.tiles_n ? t - slow * fast : slow;
-  }
-}
-
 // =============================================================================
-// CTA-pair kernel: persistent pairs, tiles of 256 x 256, contraction 64 a stage
-// (tcgen05 cta_group::2 kind::f16, K = 16 an instruction).  CTA r loads rows
-// [128 r, 128 r + 128) of A and of B; two accumulators in tensor memory, so a
-// tile's epilogue runs under the next one's MMAs.  8 epilogue warps of each CTA
-// take 32 rows x 32 columns at a time through a slot of two boxes: what the
-// chunk needs (E, or X's two halves) comes in ahead by tensor loads, the results
-// go out of the same boxes by tensor stores.  Of a symmetric product the tiles
-// on and below the diagonal are computed, and the others are their transposes,
-// through ldmatrix and stmatrix.  Rows, columns and contraction behind a
-// matrix's end are filled with zeros by the loads and left out by the stores.
+// The products.  Tiles of 128 rows x BN columns of a CTA, or of 256 x BN of a CTA
+// pair (tcgen05 cta_group::2: CTA r loads rows [128 r, 128 r + 128) of A and its half
+// of B's), contraction 64 a stage (kind::f16, K = 16 an instruction).  A TMA
+// producer, an MMA thread and 8 epilogue warps in each CTA, which walks its tiles;
+// two accumulators in tensor memory, so a tile's epilogue runs under the next one's
+// MMAs.  An epilogue warp takes 32 rows x 32 columns at a time through a slot of two
+// boxes: what the chunk needs (E, or X's two halves) comes in ahead by tensor loads,
+// the results go out of the same boxes by tensor stores.  Of a symmetric product the
+// tiles that reach the diagonal or lie below it are computed, their boxes below the
+// diagonal stored twice, the second time transposed (ldmatrix and stmatrix).  Rows,
+// columns and contraction behind a matrix's end are filled with zeros by the loads and
+// left out by the stores.
 // =============================================================================
-template <int KIND>
+template <bool PAIR, int BN, int STAGES, int SLOTS>
 struct NsLayout {
-  static constexpr int kStages = KIND == kGram ? 5 : 4;
-  static constexpr int kSlots = KIND == kGram ? 2 : 3;  // of an epilogue warp
-  static constexpr uint32_t kA = 128 * kBK * 2, kB = kA;
+  static constexpr bool kPair = PAIR;
+  static constexpr int kBN = BN, kBM = PAIR ? 256 : 128, kStages = STAGES, kSlots = SLOTS;
+  static constexpr int kRowsB = PAIR ? BN / 2 : BN;  // of B that a CTA loads
+  static constexpr uint32_t kA = 128 * kBK * 2, kB = kRowsB * kBK * 2;
   static constexpr uint32_t kBox = 32 * 64, kSlot = 2 * kBox;
   static constexpr uint32_t offA = 0, offB = offA + kStages * kA;
   static constexpr uint32_t offSlots = offB + kStages * kB;
@@ -177,336 +189,454 @@ struct NsLayout {
   // where pair_leave looks for it; then one per epilogue warp and slot
   static constexpr uint32_t kAccBar = 2 * kStages, kDrainBar = 4 * kStages + 2;
   static constexpr uint32_t kSlotBar = kDrainBar + 3;
-  static constexpr uint32_t offMisc = offBar + (kSlotBar + 8 * kSlots) * 8;
+  // between the products of one launch: the warps are done, and may go on
+  static constexpr uint32_t kDoneBar = kSlotBar + 8 * kSlots, kGoBar = kDoneBar + 1;
+  static constexpr uint32_t offMisc = offBar + (kGoBar + 1 + (kGoBar + 1) % 2) * 8;
   static constexpr uint32_t kAlloc = offMisc + 16 + 1024;
   static constexpr int kThreads = 384;
+  static constexpr int kChunks = BN / 64;  // of an epilogue warp
   static_assert(kAlloc <= 232448, "shared memory overflow");
   static_assert(offSlots % 1024 == 0 && kAccBar + 4 <= kDrainBar, "layout");
+  static_assert(2 * BN <= (int)kTmemCols, "tensor memory overflow");
 };
 
-template <int KIND, bool AMN, bool BMN>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NsLayout<KIND>::kThreads, 1)
+// A CTA's place and what its roles share.
+template <class L>
+struct Ns {
+  uint8_t* smem;
+  uint32_t base, bar0, tmem;
+  volatile int* abort_flag;
+  uint32_t peer_abort, rank;
+  int warp, lane, unit, units;
+
+  NVFP4_DEV uint32_t full_bar(uint32_t s) const { return bar0 + 8u * s; }
+  NVFP4_DEV uint32_t empty_bar(uint32_t s) const { return bar0 + 8u * (L::kStages + s); }
+  NVFP4_DEV uint32_t acc_full(uint32_t b) const { return bar0 + 8u * (L::kAccBar + b); }
+  NVFP4_DEV uint32_t acc_empty(uint32_t b) const { return bar0 + 8u * (L::kAccBar + 2 + b); }
+  NVFP4_DEV uint32_t fills() const { return base + L::offMisc + 8; }
+  NVFP4_DEV uint32_t inject() const { return base + L::offMisc + 12; }
+  NVFP4_DEV bool wait(uint32_t bar, uint32_t parity, unsigned int code) const {
+    return L::kPair ? wait_bounded_pair(bar, parity, abort_flag, peer_abort, code)
+                    : wait_bounded(bar, parity, abort_flag, code);
+  }
+  NVFP4_DEV void commit(uint32_t bar) const {
+    if (L::kPair)
+      tc_commit_pair(bar, (uint16_t)3);
+    else
+      tc_commit(bar);
+  }
+};
+
+// Barriers, tensor memory; ends with all of the cluster's CTAs set up.
+template <class L>
+NVFP4_DEV Ns<L> ns_enter() {
+  extern __shared__ uint8_t smem_raw[];
+  Ns<L> c;
+  c.smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                      ~uintptr_t(1023));
+  c.base = smem_u32(c.smem);
+  c.bar0 = c.base + L::offBar;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(c.smem + L::offMisc);
+  c.abort_flag = reinterpret_cast<volatile int*>(c.smem + L::offMisc + 4);
+  c.rank = L::kPair ? cluster_ctarank() : 0;
+  c.peer_abort = L::kPair ? mapa_shared(c.base + L::offMisc + 4, c.rank ^ 1u) : 0;
+  c.warp = threadIdx.x >> 5;
+  c.lane = threadIdx.x & 31;
+  c.unit = L::kPair ? blockIdx.x / 2 : blockIdx.x;
+  c.units = L::kPair ? gridDim.x / 2 : gridDim.x;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      mbar_init(c.full_bar(s), 1);
+      mbar_init(c.empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(c.acc_full(b), 1);
+      mbar_init(c.acc_empty(b), L::kPair ? 16 : 8);  // 8 epilogue warps in each CTA
+    }
+    mbar_init(c.bar0 + 8u * L::kDrainBar, 1);
+    mbar_init(c.bar0 + 8u * (L::kDrainBar + 1), 1);
+    for (int w = 0; w < 8 * L::kSlots; ++w) mbar_init(c.bar0 + 8u * (L::kSlotBar + w), 1);
+    mbar_init(c.bar0 + 8u * L::kDoneBar, 8);
+    mbar_init(c.bar0 + 8u * L::kGoBar, 1);
+    *c.abort_flag = 0;
+    st_shared_u32(c.fills(), 0);
+    st_shared_u32(c.inject(), injected());
+    fence_mbar_init();
+  }
+  if (c.warp == 1) {
+    if (L::kPair) {
+      tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (L::kPair) cluster_sync();
+  tc_fence_after();
+  c.tmem = *tmem_slot;
+  return c;
+}
+
+// The end: what a CTA that has given up left in flight finishes before its memory goes.
+template <class L>
+NVFP4_DEV void ns_leave(const Ns<L>& c) {
+  tc_fence_before();
+  __syncthreads();
+  // the MMAs, by the lane that issued them
+  if (*c.abort_flag && c.warp == 1 && (ld_shared_u32(c.inject()) >> 8 & 0xFFu) && elect_one()) {
+    const uint32_t bar = c.bar0 + 8u * (L::kDrainBar + 1);
+    if (L::kPair)
+      tc_commit_pair(bar, (uint16_t)(1u << c.rank));
+    else
+      tc_commit(bar);
+    wait_drain(bar, 0);
+  }
+  if (L::kPair) {
+    pair_leave<L, L::kStages, 2, false>(L::kA + L::kB);
+  } else {
+    if (*c.abort_flag && threadIdx.x == 0)
+      drain_stages<L::kStages>(c.bar0, ld_shared_u32(c.fills()));
+    __syncthreads();
+  }
+  if (c.warp == 1) {
+    tc_fence_after();
+    if (L::kPair)
+      tmem_dealloc_pair(ld_shared_u32(c.base + L::offMisc), kTmemCols);
+    else
+      tmem_dealloc(ld_shared_u32(c.base + L::offMisc), kTmemCols);
+  }
+}
+
+// Tile t of a matrix.  A symmetric product's: row by row, those that begin left of the
+// row's end.  Else with the matrix's smaller side running fastest: tiles at work
+// together then read X, the operand that L2 may not hold, once (14336 x 4096: an
+// update 375 us the other way round, 330 this).
+template <class L>
+NVFP4_DEV void tile_of(int t, const NsArgs& a, int& tm, int& tn) {
+  if (a.symmetric) {
+    constexpr int kPer = L::kBM / L::kBN;  // more tiles in each row; the last may be short
+    tm = (int)((sqrtf(8.0f / kPer * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (kPer * ((tm + 1) * (tm + 2) / 2) <= t) ++tm;
+    while (kPer * (tm * (tm + 1) / 2) > t) --tm;
+    tn = t - kPer * (tm * (tm + 1) / 2);
+  } else {
+    const int fast = min(a.tiles_m, a.tiles_n), slow = t / fast;
+    tm = a.tiles_m > a.tiles_n ? slow : t - slow * fast;
+    tn = a.tiles_m > a.tiles_n ? t - slow * fast : slow;
+  }
+}
+
+struct Pipe {
+  uint32_t s = 0, ph = 0;  // stage, and its phase
+  uint32_t it = 0;         // tiles done (which accumulator), producer: stages filled
+};
+
+// The producer's warp.
+template <class L>
+NVFP4_DEV bool ns_produce(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Pipe& p) {
+  const int num_kb = (a.k + kBK - 1) / kBK;
+  for (int tile = c.unit; tile < a.tiles; tile += c.units) {
+    const int z = tile / a.tiles_per;
+    int tm, tn;
+    tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
+    const int a0 = tm * L::kBM + (int)c.rank * 128;
+    const int b0 = tn * L::kBN + (int)c.rank * L::kRowsB;
+    for (int kb = 0; kb < num_kb; ++kb) {
+      if (!all_waited(c.wait(c.empty_bar(p.s), p.ph ^ 1u, 0x71u))) return false;
+      ++p.it;
+      if (elect_one()) {
+        const uint32_t sa = c.base + L::offA + p.s * L::kA, sb = c.base + L::offB + p.s * L::kB;
+        const int k = kb * kBK;
+        if (L::kPair) {
+          const uint32_t fb = mapa_shared(c.full_bar(p.s), 0);
+          if (c.rank == 0) mbar_arrive_expect_tx(c.full_bar(p.s), 2 * (L::kA + L::kB));
+          if (a.a_mn)
+            for (int i = 0; i < 2; ++i)
+              tma_load_3d_pair(sa + i * kBoxMN, maps.a, fb, a0 + 64 * i, k, z);
+          else
+            tma_load_3d_pair(sa, maps.a, fb, k, a0, z);
+          if (a.b_mn)
+            for (int i = 0; i < L::kRowsB / 64; ++i)
+              tma_load_3d_pair(sb + i * kBoxMN, maps.b, fb, b0 + 64 * i, k, z);
+          else
+            tma_load_3d_pair(sb, maps.b, fb, k, b0, z);
+        } else {
+          const uint32_t fb = c.full_bar(p.s);
+          mbar_arrive_expect_tx(fb, L::kA + L::kB);
+          if (a.a_mn)
+            for (int i = 0; i < 2; ++i)
+              tma_load_3d(sa + i * kBoxMN, maps.a, fb, a0 + 64 * i, k, z);
+          else
+            tma_load_3d(sa, maps.a, fb, k, a0, z);
+          if (a.b_mn)
+            for (int i = 0; i < L::kRowsB / 64; ++i)
+              tma_load_3d(sb + i * kBoxMN, maps.b, fb, b0 + 64 * i, k, z);
+          else
+            tma_load_3d(sb, maps.b, fb, k, b0, z);
+        }
+      }
+      __syncwarp();
+      if (++p.s == L::kStages) {
+        p.s = 0;
+        p.ph ^= 1u;
+      }
+    }
+  }
+  return true;
+}
+
+// The MMA warp (of a pair: the first CTA's).
+template <class L>
+NVFP4_DEV bool ns_multiply(const Ns<L>& c, const NsArgs& a, Pipe& p) {
+  const int num_kb = (a.k + kBK - 1) / kBK;
+  const uint32_t idesc = idesc_f16(L::kBM, L::kBN, a.a_mn, a.b_mn);
+  // a step of 16 lies 32 bytes on in K-major operands, 16 rows in others
+  const uint64_t as = a.a_mn ? 2048 >> 4 : 32 >> 4, bs = a.b_mn ? 2048 >> 4 : 32 >> 4;
+  for (int tile = c.unit; tile < a.tiles; tile += c.units, ++p.it) {
+    const uint32_t b = p.it & 1u;
+    if (!all_waited(c.wait(c.acc_empty(b), ((p.it >> 1) & 1u) ^ 1u, 0x72u))) return false;
+    tc_fence_after();
+    for (int kb = 0; kb < num_kb; ++kb) {
+      if (!all_waited(c.wait(c.full_bar(p.s), p.ph, 0x74u))) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t sa = c.base + L::offA + p.s * L::kA, sb = c.base + L::offB + p.s * L::kB;
+        const int left = a.k - kb * kBK;
+        const uint64_t ad = a.a_mn ? smem_desc_mn(sa, kBoxMN) : smem_desc_sw128(sa);
+        const uint64_t bd = a.b_mn ? smem_desc_mn(sb, kBoxMN) : smem_desc_sw128(sb);
+#pragma unroll
+        for (int j = 0; j < kBK / 16; ++j) {
+          if (16 * j >= left) break;
+          tc_mma_f16(L::kPair, c.tmem + b * L::kBN, ad + j * as, bd + j * bs, idesc,
+                     kb | j ? 1u : 0u);
+        }
+        if (kb == 0) st_shared_u8(c.inject() + 1, 1u);
+        c.commit(c.empty_bar(p.s));
+        if (kb == num_kb - 1) c.commit(c.acc_full(b));
+      }
+      __syncwarp();
+      if (++p.s == L::kStages) {
+        p.s = 0;
+        p.ph ^= 1u;
+      }
+    }
+  }
+  return true;
+}
+
+// An epilogue warp's position: its next tile's accumulator, chunks sent for and done.
+struct Chunks {
+  uint32_t it = 0, loaded = 0, used = 0;
+};
+
+template <class L>
+NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Chunks& p) {
+  const int ew = c.warp - 4, q = c.warp & 3, h = ew >> 2, lane = c.lane;
+  uint8_t* slots = c.smem + L::offSlots + ew * (L::kSlots * L::kSlot);
+  const uint32_t slot_bar = c.bar0 + 8u * (L::kSlotBar + ew * L::kSlots);
+  // where this warp's chunks of a tile lie, and how many there are
+  auto place = [&](int tile, int& x, int& y, int& z) {
+    z = tile / a.tiles_per;
+    int tm, tn;
+    tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
+    y = tm * L::kBM + (int)c.rank * 128 + q * 32;
+    x = tn * L::kBN + h * (L::kBN / 2);
+    if (y >= a.m || x >= a.n) return 0;
+    const int end = a.symmetric ? min(a.n, y + 32) : a.n;  // up to the diagonal
+    return max(0, min(L::kChunks, (end - x + 31) / 32));
+  };
+  // the loads run up to kSlots - 1 chunks ahead, over the tiles
+  int ltile = a.loads ? c.unit : a.tiles, lc = 0, lcount = 0, lx, ly, lz;
+  if (ltile < a.tiles) lcount = place(ltile, lx, ly, lz);
+  auto load_next = [&]() {
+    while (ltile < a.tiles && lc >= lcount) {
+      ltile += c.units;
+      lc = 0;
+      if (ltile < a.tiles) lcount = place(ltile, lx, ly, lz);
+    }
+    if (ltile >= a.tiles) return;
+    if (lane == 0) {
+      const uint32_t s = p.loaded % L::kSlots, bar = slot_bar + 8u * s;
+      const uint32_t to = smem_u32(slots + s * L::kSlot);
+      mbar_arrive_expect_tx(bar, a.loads * L::kBox);
+      tma_load_3d(to, maps.in0, bar, lx + lc * 32, ly, lz);
+      if (a.loads > 1) tma_load_3d(to + L::kBox, maps.in1, bar, lx + lc * 32, ly, lz);
+    }
+    ++p.loaded;
+    ++lc;
+  };
+#pragma unroll 1
+  for (int i = 0; i < L::kSlots - 1; ++i) load_next();
+  uint32_t stores = 0;  // chunks without loads
+#pragma unroll 1
+  for (int tile = c.unit; tile < a.tiles; tile += c.units, ++p.it) {
+    const uint32_t b = p.it & 1u;
+    int x0, y, z;
+    const int count = place(tile, x0, y, z);
+    const float* din = a.din + (int64_t)z * a.dstride;
+    const int row = y + lane;
+    // the diagonal's entries: this row's, and of the chunk's columns the lane's
+    const float di = a.by_row && row < a.m ? __ldcg(din + row) : 0.0f;
+    float dj = a.by_col && count > 0 ? __ldcg(din + x0 + lane) : 0.0f;
+    if (!all_waited(c.wait(c.acc_full(b), (p.it >> 1) & 1u, 0x73u))) return false;
+    tc_fence_after();
+#pragma unroll 1
+    for (int ch = 0; ch < count; ++ch) {
+      const uint32_t s = (p.used + stores) % L::kSlots;
+      uint8_t* box = slots + s * L::kSlot;
+      const int x = x0 + ch * 32;
+      // the slot that the next load takes is free once its stores have read it
+      if (lane == 0) {
+        if (a.loads)
+          bulk_wait_group_read<0>();
+        else
+          bulk_wait_group_read<L::kSlots - 1>();
+      }
+      __syncwarp();
+      load_next();
+      uint32_t r[32];
+      tmem_ld32(c.tmem + ((uint32_t)(q * 32) << 16) + b * L::kBN +
+                    (uint32_t)(h * (L::kBN / 2) + ch * 32),
+                r);
+      uint32_t in0[16] = {}, in1[16] = {};
+      if (a.loads) {
+        if (!all_waited(c.wait(slot_bar + 8u * s, (p.used / L::kSlots) & 1u, 0x75u))) return false;
+        box_get(box, lane, in0);
+        if (a.loads > 1) box_get(box + L::kBox, lane, in1);
+        ++p.used;
+      } else {
+        ++stores;
+      }
+      tmem_ld_wait();
+      const float base = fmaf(a.q, di, a.p);
+      float v[32];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float2 x0f = unpack_f16x2(in0[e]), x1f = unpack_f16x2(in1[e]);
+        const float f0 = fmaf(a.q, __shfl_sync(0xFFFFFFFFu, dj, 2 * e), base);
+        const float f1 = fmaf(a.q, __shfl_sync(0xFFFFFFFFu, dj, 2 * e + 1), base);
+        v[2 * e] = fmaf(f0, x0f.x + x1f.x, __uint_as_float(r[2 * e]) * a.s);
+        v[2 * e + 1] = fmaf(f1, x0f.y + x1f.y, __uint_as_float(r[2 * e + 1]) * a.s);
+      }
+      if (a.by_col && ch + 1 < count) dj = __ldcg(din + x + 32 + lane);
+      if (a.symmetric && x == y) {
+        float d = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          d = e == lane ? __uint_as_float(r[e]) : d;
+          v[e] = e == lane ? 0.0f : v[e];
+        }
+        if (row < a.m)
+          a.dout[(int64_t)z * a.dstride + row] = fmaf(base, di, a.t * d);
+      }
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        w[e] = a.final ? pack_bf16x2(v[2 * e] * kUnscale, v[2 * e + 1] * kUnscale)
+                       : pack_f16x2(v[2 * e], v[2 * e + 1]);
+      __syncwarp();
+      box_put(box, lane, w);
+      const bool mirror = a.symmetric && x < y, both = a.loads > 1 && !a.final;
+      if (both) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 hi = unpack_f16x2(w[e]);
+          w[e] = pack_f16x2(v[2 * e] - hi.x, v[2 * e + 1] - hi.y);
+        }
+        box_put(box + L::kBox, lane, w);
+      }
+      __syncwarp();
+      if (mirror) {
+        box_transpose(smem_u32(box), smem_u32(box + L::kBox), lane);
+        __syncwarp();
+      }
+      if (a.final && !a.out_boxes) {
+        // rows of the result that do not start on 16 bytes: a row at a time
+        const int rows = min(32, a.m - y);
+        for (int i = 0; i < rows; ++i) {
+          const uint16_t u = *reinterpret_cast<const uint16_t*>(box + box_piece(i, lane >> 3) +
+                                                                (lane & 7) * 2);
+          if (x + lane < a.n)
+            reinterpret_cast<uint16_t*>(a.out)[((int64_t)z * a.m + y + i) * a.n + x + lane] = u;
+        }
+        __syncwarp();
+      } else {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(maps.out0, smem_u32(box), x, y, z);
+          if (mirror) tma_store_3d(maps.out0, smem_u32(box + L::kBox), y, x, z);
+          if (both) tma_store_3d(maps.out1, smem_u32(box + L::kBox), x, y, z);
+          bulk_commit_group();
+        }
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (L::kPair)
+        mbar_arrive_cluster_relaxed(mapa_shared(c.acc_empty(b), 0));
+      else
+        mbar_arrive(c.acc_empty(b));
+    }
+  }
+  return true;
+}
+
+// The coefficients of a step's product k (0: X X^T, 1: E E, 2: the update).
+__host__ __device__ inline void set_coefs(NsArgs& n, int k, const float* abc, bool last) {
+  n.p = k == 0 ? 0.0f : k == 1 ? abc[1] : abc[0];
+  n.q = k == 0 ? 0.0f : k == 1 ? abc[2] : 1.0f;
+  n.s = k == 1 ? abc[2] * kUnscale : kUnscale;
+  n.t = n.s * kUnscale;
+  n.final = k == 2 && last;
+}
+
+// The chunks that a warp that has given up sent for land before the block ends.
+template <class L>
+NVFP4_DEV void drain_chunks(const Ns<L>& c, Chunks& p) {
+  const uint32_t slot_bar = c.bar0 + 8u * (L::kSlotBar + (c.warp - 4) * L::kSlots);
+  for (; (int32_t)(p.loaded - p.used) > 0; ++p.used)
+    wait_drain(slot_bar + 8u * (p.used % L::kSlots), (p.used / L::kSlots) & 1u);
+}
+
+// ---- a launch for each product: large matrices ---------------------------------------
+// LOADS: the epilogue brings something in.
+template <bool LOADS>
+using PairLayout = NsLayout<true, 256, LOADS ? 4 : 5, LOADS ? 3 : 2>;
+
+template <bool LOADS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<LOADS>::kThreads, 1)
     ns_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmIn0,
                    const __grid_constant__ CUtensorMap tmIn1,
                    const __grid_constant__ CUtensorMap tmOut0,
                    const __grid_constant__ CUtensorMap tmOut1, const NsArgs args) {
-  using L = NsLayout<KIND>;
-  constexpr int S = L::kStages;
-  constexpr bool kSym = KIND <= kPoly;
-  constexpr int kLoads = KIND == kGram ? 0 : KIND == kPoly ? 1 : 2;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bar0 = sbase + L::offBar;
-  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (S + s); };
-  auto acc_full = [&](uint32_t b) { return bar0 + 8u * (L::kAccBar + b); };
-  auto acc_empty = [&](uint32_t b) { return bar0 + 8u * (L::kAccBar + 2 + b); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::offMisc);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::offMisc + 4);
-  const uint32_t rank = cluster_ctarank();
-  const bool leader = rank == 0;
-  const uint32_t peer_abort = mapa_shared(smem_u32(smem + L::offMisc + 4), rank ^ 1u);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int unit = blockIdx.x / 2, num_units = gridDim.x / 2;
-  const uint32_t fills = sbase + L::offMisc + 8, inject = fills + 4;
-
+  using L = PairLayout<LOADS>;
+  const Ns<L> c = ns_enter<L>();
+  const NsMaps maps = {&tmA, &tmB, &tmIn0, &tmIn1, &tmOut0, &tmOut1};
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(acc_full(b), 1);
-      mbar_init(acc_empty(b), 16);  // 8 epilogue warps in each CTA
-    }
-    mbar_init(bar0 + 8u * L::kDrainBar, 1);
-    for (int w = 0; w < 8 * L::kSlots; ++w) mbar_init(bar0 + 8u * (L::kSlotBar + w), 1);
-    *abort_flag = 0;
-    st_shared_u32(inject, injected());
-    fence_mbar_init();
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
   }
-  if (warp == 1) {
-    tmem_alloc_pair(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
-  tc_fence_after();
   griddep_wait();
-  const uint32_t tmem = *tmem_slot;
-  const int num_kb = (args.k + kBK - 1) / kBK;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      prefetch_tmap(&tmA);
-      prefetch_tmap(&tmB);
-      uint32_t s = 0, ph = 0, count = 0;
-      bool ok = !(ld_shared_u32(inject) & kStall);
-      for (int tile = unit; ok && tile < args.tiles; tile += num_units) {
-        const int z = tile / args.tiles_per;
-        int tm, tn;
-        tile_of<KIND>(tile - z * args.tiles_per, args, tm, tn);
-        const int a0 = tm * kTile + (int)rank * 128, b0 = tn * kTile + (int)rank * 128;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bounded_pair(empty_bar(s), ph ^ 1u, abort_flag, peer_abort, 0x71u)) {
-            ok = false;
-            break;
-          }
-          ++count;
-          const uint32_t fb = mapa_shared(full_bar(s), 0);
-          const uint32_t sa = sbase + L::offA + s * L::kA, sb = sbase + L::offB + s * L::kB;
-          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * (L::kA + L::kB));
-          if (AMN) {
-            tma_load_3d_pair(sa, &tmA, fb, a0, kb * kBK, z);
-            tma_load_3d_pair(sa + kBoxMN, &tmA, fb, a0 + 64, kb * kBK, z);
-          } else {
-            tma_load_3d_pair(sa, &tmA, fb, kb * kBK, a0, z);
-          }
-          if (BMN) {
-            tma_load_3d_pair(sb, &tmB, fb, b0, kb * kBK, z);
-            tma_load_3d_pair(sb + kBoxMN, &tmB, fb, b0 + 64, kb * kBK, z);
-          } else {
-            tma_load_3d_pair(sb, &tmB, fb, kb * kBK, b0, z);
-          }
-          if (++s == S) { s = 0; ph ^= 1u; }
-        }
-      }
-      st_shared_u32(fills, count);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      // ---------------------------------------------------------------- MMA
-      constexpr uint32_t idesc = idesc_f16(256, kTile, AMN, BMN);
-      uint32_t s = 0, ph = 0, it = 0;
-      bool ok = !quits_pair(ld_shared_u32(inject), abort_flag, peer_abort);
-      for (int tile = unit; ok && tile < args.tiles; tile += num_units, ++it) {
-        const uint32_t b = it & 1u;
-        if (!wait_bounded_pair(acc_empty(b), ((it >> 1) & 1u) ^ 1u, abort_flag, peer_abort,
-                               0x72u)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (!wait_bounded_pair(full_bar(s), ph, abort_flag, peer_abort, 0x74u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = sbase + L::offA + s * L::kA, sb = sbase + L::offB + s * L::kB;
-          const int left = args.k - kb * kBK;
-#pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) {
-            if (16 * j >= left) break;
-            const uint64_t ad = AMN ? smem_desc_mn(sa + 2048 * j, kBoxMN) : smem_desc_sw128(sa + 32 * j);
-            const uint64_t bd = BMN ? smem_desc_mn(sb + 2048 * j, kBoxMN) : smem_desc_sw128(sb + 32 * j);
-            tc_mma_pair_f16(tmem + b * kTile, ad, bd, idesc, kb | j ? 1u : 0u);
-          }
-          st_shared_u8(inject + warp, 1u);
-          tc_commit_pair(empty_bar(s), (uint16_t)3);
-          if (++s == S) { s = 0; ph ^= 1u; }
-        }
-        if (!ok) break;
-        tc_commit_pair(acc_full(b), (uint16_t)3);
-      }
-    }
-  } else if (warp >= 4) {
-    // -------------------------------------------------------------- epilogue
-    const int ew = warp - 4, q = warp & 3, h = ew >> 2;
-    uint8_t* slots = smem + L::offSlots + ew * (L::kSlots * L::kSlot);
-    const uint32_t slot_bar = bar0 + 8u * (L::kSlotBar + ew * L::kSlots);
-    if (lane == 0) {
-      prefetch_tmap(&tmOut0);
-      prefetch_tmap(&tmOut1);
-    }
-    // where this warp's chunks of a tile lie, and how many there are
-    auto place = [&](int tile, int& x, int& y, int& z, int& tm, int& tn) {
-      z = tile / args.tiles_per;
-      tile_of<KIND>(tile - z * args.tiles_per, args, tm, tn);
-      y = tm * kTile + (int)rank * 128 + q * 32;
-      x = tn * kTile + h * 128;
-      return y < args.m && x < args.n ? min(4, (args.n - x + 31) / 32) : 0;
-    };
-    // the loads run up to kSlots - 1 chunks ahead, over the tiles
-    int ltile = unit, lc = 0;
-    uint32_t loaded = 0;
-    bool lmore = kLoads > 0;
-    auto load_next = [&]() {
-      if (!lmore) return;
-      int x, y, z, tm, tn, count = 0;
-      while (ltile < args.tiles && lc >= (count = place(ltile, x, y, z, tm, tn))) {
-        ltile += num_units;
-        lc = 0;
-      }
-      if (ltile >= args.tiles) {
-        lmore = false;
-        return;
-      }
-      if (lane == 0) {
-        const uint32_t s = loaded % L::kSlots, bar = slot_bar + 8u * s;
-        const uint32_t to = smem_u32(slots + s * L::kSlot);
-        mbar_arrive_expect_tx(bar, kLoads * L::kBox);
-        tma_load_3d(to, &tmIn0, bar, x + lc * 32, y, z);
-        if (kLoads > 1) tma_load_3d(to + L::kBox, &tmIn1, bar, x + lc * 32, y, z);
-      }
-      ++loaded;
-      ++lc;
-    };
-    for (int i = 0; i < L::kSlots - 1; ++i) load_next();
-    uint32_t it = 0, used = 0;
-    bool ok = true;
-    for (int tile = unit; ok && tile < args.tiles; tile += num_units, ++it) {
-      const uint32_t b = it & 1u;
-      int x0, y, z, tm, tn;
-      const int count = place(tile, x0, y, z, tm, tn);
-      if (!all_waited(wait_bounded_pair(acc_full(b), (it >> 1) & 1u, abort_flag, peer_abort,
-                                        0x73u))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const bool mirror = kSym && tm != tn;
-      const float* din = args.din + (int64_t)z * args.dstride;
-      const int row = y + lane;
-      float di = 0.0f;
-      if ((KIND == kPoly || (KIND >= kUpdate && !args.by_col)) && row < args.m) di = din[row];
-      for (int c = 0; c < count; ++c, ++used) {
-        const uint32_t s = used % L::kSlots;
-        uint8_t* box = slots + s * L::kSlot;
-        const int x = x0 + c * 32;
-        // the slot of the chunk before last is free once its stores have read it
-        if (lane == 0) {
-          if (kLoads)
-            bulk_wait_group_read<0>();
-          else
-            bulk_wait_group_read<L::kSlots - 1>();
-        }
-        __syncwarp();
-        load_next();
-        uint32_t r[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + b * kTile + (uint32_t)(h * 128 + c * 32), r);
-        uint32_t in0[16], in1[16];
-        if (kLoads) {
-          if (!all_waited(wait_bounded_pair(slot_bar + 8u * s, (used / L::kSlots) & 1u, abort_flag,
-                                            peer_abort, 0x75u))) {
-            ok = false;
-            break;
-          }
-          box_get(box, lane, in0);
-          if (kLoads > 1) box_get(box + L::kBox, lane, in1);
-        }
-        tmem_ld_wait();
-        uint32_t w0[16], w1[16];
-        float v[32];
-        if constexpr (KIND == kGram) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * kUnscale;
-          if (x == y) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e == lane) {
-                if (row < args.m) args.dout[(int64_t)z * args.dstride + row] = v[e] * kUnscale;
-                v[e] = 0.0f;
-              }
-          }
-        } else if constexpr (KIND == kPoly) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 f = unpack_f16x2(in0[e]);
-            const float2 dj = *reinterpret_cast<const float2*>(din + x + 2 * e);
-            v[2 * e] = args.b * f.x +
-                       args.c * (__uint_as_float(r[2 * e]) * kUnscale + (di + dj.x) * f.x);
-            v[2 * e + 1] = args.b * f.y +
-                           args.c * (__uint_as_float(r[2 * e + 1]) * kUnscale + (di + dj.y) * f.y);
-          }
-          if (x == y) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (e == lane) {
-                const float sq = __uint_as_float(r[e]) * (kUnscale * kUnscale);
-                if (row < args.m)
-                  args.dout[(int64_t)z * args.dstride + row] = args.b * di + args.c * (di * di + sq);
-                v[e] = 0.0f;
-              }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 hi = unpack_f16x2(in0[e]), lo = unpack_f16x2(in1[e]);
-            float2 d = make_float2(di, di);
-            if (args.by_col) d = *reinterpret_cast<const float2*>(din + x + 2 * e);
-            v[2 * e] = (args.a + d.x) * (hi.x + lo.x) + __uint_as_float(r[2 * e]) * kUnscale;
-            v[2 * e + 1] =
-                (args.a + d.y) * (hi.y + lo.y) + __uint_as_float(r[2 * e + 1]) * kUnscale;
-          }
-        }
-        if constexpr (KIND == kFinal) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            w0[e] = pack_bf16x2(v[2 * e] * kUnscale, v[2 * e + 1] * kUnscale);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) w0[e] = pack_f16x2(v[2 * e], v[2 * e + 1]);
-        }
-        if constexpr (KIND == kUpdate) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 hi = unpack_f16x2(w0[e]);
-            w1[e] = pack_f16x2(v[2 * e] - hi.x, v[2 * e + 1] - hi.y);
-          }
-        }
-        __syncwarp();
-        box_put(box, lane, w0);
-        if (KIND == kUpdate) box_put(box + L::kBox, lane, w1);
-        __syncwarp();
-        if (mirror) {
-          box_transpose(smem_u32(box), smem_u32(box + L::kBox), lane);
-          __syncwarp();
-        }
-        if (KIND == kFinal && !args.out_boxes) {
-          // rows of the result that do not start on 16 bytes: a row at a time
-          const int rows = min(32, args.m - y);
-          for (int i = 0; i < rows; ++i) {
-            const uint16_t u = *reinterpret_cast<const uint16_t*>(box + box_piece(i, lane >> 3) +
-                                                                  (lane & 7) * 2);
-            if (x + lane < args.n)
-              reinterpret_cast<uint16_t*>(args.out)[((int64_t)z * args.m + y + i) * args.n + x +
-                                                    lane] = u;
-          }
-          __syncwarp();
-        } else {
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&tmOut0, smem_u32(box), x, y, z);
-            if (mirror) tma_store_3d(&tmOut0, smem_u32(box + L::kBox), y, x, z);
-            if (KIND == kUpdate) tma_store_3d(&tmOut1, smem_u32(box + L::kBox), x, y, z);
-            bulk_commit_group();
-          }
-        }
-      }
-      if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(acc_empty(b), 0));
-    }
-    // given up: the chunks sent for have landed before the block ends
-    for (; kLoads && used < loaded; ++used)
-      wait_drain(slot_bar + 8u * (used % L::kSlots), (used / L::kSlots) & 1u);
-    if (lane == 0) bulk_wait_group<0>();
+  if (c.warp == 0) {
+    Pipe p;
+    if (!(ld_shared_u32(c.inject()) & kStall)) ns_produce(c, args, maps, p);
+    if (c.lane == 0) st_shared_u32(c.fills(), p.it);
+  } else if (c.warp == 1) {
+    Pipe p;
+    if (c.rank == 0 && all_waited(!quits_pair(ld_shared_u32(c.inject()), c.abort_flag, c.peer_abort)))
+      ns_multiply(c, args, p);
+  } else if (c.warp >= 4) {
+    Chunks p;
+    if (!ns_finish(c, args, maps, p)) drain_chunks(c, p);
+    if (c.lane == 0) bulk_wait_group<0>();
   }
-
-  tc_fence_before();
-  pair_leave<L, S, 2, false>(L::kA + L::kB);
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc_pair(ld_shared_u32(sbase + L::offMisc), kTmemCols);
-  }
+  ns_leave(c);
 }
 
 // ---- momentum and start ----------------------------------------------------------
@@ -515,6 +645,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NsLayout<KIND>::kThr
 // fixed order), the second computes U again from V and G, scales it and writes
 // its two halves.
 constexpr int kEwThreads = 256, kEwUnroll = 4;
+
+constexpr size_t kBarBytes = 1024;
+constexpr int kMaxParts = 1024;
+constexpr int kWholeTiles = 2;
 
 struct MomentumArgs {
   void* grad;
@@ -532,26 +666,28 @@ struct MomentumArgs {
 NVFP4_DEV float block_sum(float v, float* red) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  __syncthreads();
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kEwThreads / 32; ++w) s += red[w];
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) s += red[w];
   return s;
 }
 
-// VEC: a matrix has a multiple of 4 elements.
+NVFP4_DEV float4 fma4(float m, const float4 v, const float4 g) {
+  return make_float4(fmaf(m, v.x, g.x), fmaf(m, v.y, g.y), fmaf(m, v.z, g.z), fmaf(m, v.w, g.w));
+}
+
+// Part `part` of matrix `mat`.  VEC: a matrix has a multiple of 4 elements.
 template <bool WIDE, bool VEC>
-__global__ void __launch_bounds__(kEwThreads) momentum_kernel(const MomentumArgs a) {
-  __shared__ float red[kEwThreads / 32];
-  griddep_wait();
-  const int64_t base = (int64_t)blockIdx.y * a.size;
-  const int64_t stride = (int64_t)gridDim.x * kEwThreads;
+NVFP4_DEV void momentum_part(const MomentumArgs& a, int mat, int part, float* red) {
+  const int64_t base = (int64_t)mat * a.size;
+  const int64_t first = (int64_t)part * blockDim.x + threadIdx.x;
+  const int64_t stride = (int64_t)a.parts * blockDim.x;
   float sum = 0.0f;
   if (VEC) {
     const int64_t n4 = a.size / 4;
-    for (int64_t i = (int64_t)blockIdx.x * kEwThreads + threadIdx.x; i < n4;
-         i += kEwUnroll * stride) {
+    for (int64_t i = first; i < n4; i += kEwUnroll * stride) {
       float4 g[kEwUnroll], v[kEwUnroll];
 #pragma unroll
       for (int u = 0; u < kEwUnroll; ++u) {
@@ -563,24 +699,15 @@ __global__ void __launch_bounds__(kEwThreads) momentum_kernel(const MomentumArgs
       }
 #pragma unroll
       for (int u = 0; u < kEwUnroll; ++u) {
-        const int64_t at = base + 4 * (i + u * stride);
         if (i + u * stride >= n4) continue;
-        v[u].x = fmaf(a.mu, v[u].x, g[u].x);
-        v[u].y = fmaf(a.mu, v[u].y, g[u].y);
-        v[u].z = fmaf(a.mu, v[u].z, g[u].z);
-        v[u].w = fmaf(a.mu, v[u].w, g[u].w);
-        *reinterpret_cast<float4*>(a.momentum + at) = v[u];
-        if (a.nesterov) {
-          v[u].x = fmaf(a.mu, v[u].x, g[u].x);
-          v[u].y = fmaf(a.mu, v[u].y, g[u].y);
-          v[u].z = fmaf(a.mu, v[u].z, g[u].z);
-          v[u].w = fmaf(a.mu, v[u].w, g[u].w);
-        }
+        v[u] = fma4(a.mu, v[u], g[u]);
+        *reinterpret_cast<float4*>(a.momentum + base + 4 * (i + u * stride)) = v[u];
+        if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
         sum += (v[u].x * v[u].x + v[u].y * v[u].y) + (v[u].z * v[u].z + v[u].w * v[u].w);
       }
     }
   } else {
-    for (int64_t i = (int64_t)blockIdx.x * kEwThreads + threadIdx.x; i < a.size; i += stride) {
+    for (int64_t i = first; i < a.size; i += stride) {
       const float g = grad_at<WIDE>(a.grad, base + i);
       float v = fmaf(a.mu, a.momentum[base + i], g);
       a.momentum[base + i] = v;
@@ -589,24 +716,22 @@ __global__ void __launch_bounds__(kEwThreads) momentum_kernel(const MomentumArgs
     }
   }
   const float s = block_sum(sum, red);
-  if (threadIdx.x == 0) a.partial[(int64_t)blockIdx.y * a.parts + blockIdx.x] = s;
+  if (threadIdx.x == 0) a.partial[(int64_t)mat * a.parts + part] = s;
 }
 
 // VEC: rows of a multiple of 8 elements, so hi and lo are laid out as the matrix.
 template <bool WIDE, bool VEC>
-__global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a) {
-  __shared__ float red[kEwThreads / 32];
-  griddep_wait();
+NVFP4_DEV void start_part(const MomentumArgs& a, int mat, int part, float* red) {
   float sum = 0.0f;
-  for (int p = threadIdx.x; p < a.parts; p += kEwThreads)
-    sum += a.partial[(int64_t)blockIdx.y * a.parts + p];
+  for (int p = threadIdx.x; p < a.parts; p += blockDim.x)
+    sum += __ldcg(a.partial + (int64_t)mat * a.parts + p);
   const float scale = kScale / fmaxf(sqrtf(block_sum(sum, red)), a.eps);
-  const int64_t base = (int64_t)blockIdx.y * a.size, to = (int64_t)blockIdx.y * a.padded;
-  const int64_t stride = (int64_t)gridDim.x * kEwThreads;
+  const int64_t base = (int64_t)mat * a.size, to = (int64_t)mat * a.padded;
+  const int64_t first = (int64_t)part * blockDim.x + threadIdx.x;
+  const int64_t stride = (int64_t)a.parts * blockDim.x;
   if (VEC) {
     const int64_t n4 = a.size / 4;
-    for (int64_t i = (int64_t)blockIdx.x * kEwThreads + threadIdx.x; i < n4;
-         i += kEwUnroll * stride) {
+    for (int64_t i = first; i < n4; i += kEwUnroll * stride) {
       float4 g[kEwUnroll], v[kEwUnroll];
 #pragma unroll
       for (int u = 0; u < kEwUnroll; ++u) {
@@ -620,12 +745,7 @@ __global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a)
       for (int u = 0; u < kEwUnroll; ++u) {
         const int64_t e = 4 * (i + u * stride);
         if (i + u * stride >= n4) continue;
-        if (a.nesterov) {
-          v[u].x = fmaf(a.mu, v[u].x, g[u].x);
-          v[u].y = fmaf(a.mu, v[u].y, g[u].y);
-          v[u].z = fmaf(a.mu, v[u].z, g[u].z);
-          v[u].w = fmaf(a.mu, v[u].w, g[u].w);
-        }
+        if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
         v[u].x *= scale;
         v[u].y *= scale;
         v[u].z *= scale;
@@ -647,7 +767,7 @@ __global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a)
       }
     }
   } else {
-    for (int64_t i = (int64_t)blockIdx.x * kEwThreads + threadIdx.x; i < a.size; i += stride) {
+    for (int64_t i = first; i < a.size; i += stride) {
       float v = a.momentum[base + i];
       if (a.nesterov) v = fmaf(a.mu, v, grad_at<WIDE>(a.grad, base + i));
       v *= scale;
@@ -664,6 +784,180 @@ __global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a)
       }
     }
   }
+}
+
+template <bool WIDE, bool VEC>
+__global__ void __launch_bounds__(kEwThreads) momentum_kernel(const MomentumArgs a) {
+  __shared__ float red[kEwThreads / 32];
+  griddep_wait();
+  momentum_part<WIDE, VEC>(a, blockIdx.y, blockIdx.x, red);
+}
+template <bool WIDE, bool VEC>
+__global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a) {
+  __shared__ float red[kEwThreads / 32];
+  griddep_wait();
+  start_part<WIDE, VEC>(a, blockIdx.y, blockIdx.x, red);
+}
+
+// ---- one launch for all of it: matrices of some hundred rows and columns -----------
+// The CTAs, one an SM, go through momentum, start and the products of every step
+// together; between two products they meet at a counter: a CTA's epilogue warps tell
+// its producer that their stores have been written, which counts up for all of them,
+// waits for the other CTAs and lets them go on.  (Counted by every warp, 1216 additions
+// to one word took longer than the products.)  A launch each costs 12 us a product here,
+// most of it ends and beginnings.
+struct WholeArgs {
+  MomentumArgs e;
+  NsArgs gram, poly, update;  // without coefficients
+  unsigned int* bars;  // two counters, zero at the start
+  int batch, steps, vec1, vec2;
+  float coefs[3 * NVFP4_MUON_MAX_STEPS];
+};
+struct WholeMaps {
+  CUtensorMap gram_a[2], gram_b[2], poly_a, poly_b, upd_a[2], upd_b[2];
+  CUtensorMap x[2], lo, e, f, out;
+};
+
+// One thread waits until a counter has come to `target`, or gives up.
+NVFP4_DEV bool count_wait(const unsigned int* bar, unsigned int target, volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_gemm_wait_ns);
+  while (true) {
+    unsigned int v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
+    if ((int)(v - target) >= 0) break;
+    if (*abort_flag) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      *abort_flag = 1;
+      atomicCAS(&g_gemm_error, 0u, 0x76u);
+      return false;
+    }
+  }
+  fence_proxy_async();
+  return true;
+}
+NVFP4_DEV void count_up(unsigned int* bar) {
+  __threadfence();
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
+}
+
+// All CTAs' threads meet (before the roles part); false when the wait ran out.
+template <class L>
+NVFP4_DEV bool whole_barrier(const Ns<L>& c, const WholeArgs& a, unsigned int target) {
+  fence_proxy_async();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (!(injected() & kQuit) || blockIdx.x) count_up(a.bars);
+    count_wait(a.bars, target, c.abort_flag);
+  }
+  __syncthreads();
+  return *c.abort_flag == 0;
+}
+
+template <int BN>
+using WholeLayout = NsLayout<false, BN, BN == 64 ? 6 : 4, BN == 64 ? 2 : 3>;
+
+template <int BN, bool WIDE>
+__global__ void __launch_bounds__(WholeLayout<BN>::kThreads, 1)
+    whole_kernel(const __grid_constant__ WholeMaps maps, const __grid_constant__ WholeArgs a) {
+  using L = WholeLayout<BN>;
+  __shared__ float red[L::kThreads / 32];
+  const Ns<L> c = ns_enter<L>();
+  if (threadIdx.x < sizeof(WholeMaps) / sizeof(CUtensorMap))
+    prefetch_tmap(reinterpret_cast<const CUtensorMap*>(&maps) + threadIdx.x);
+  const int items = a.batch * a.e.parts;
+  for (int w = blockIdx.x; w < items; w += gridDim.x) {
+    const int mat = w / a.e.parts, part = w - mat * a.e.parts;
+    if (a.vec1)
+      momentum_part<WIDE, true>(a.e, mat, part, red);
+    else
+      momentum_part<WIDE, false>(a.e, mat, part, red);
+  }
+  bool ok = whole_barrier(c, a, gridDim.x);
+  if (ok) {
+    for (int w = blockIdx.x; w < items; w += gridDim.x) {
+      const int mat = w / a.e.parts, part = w - mat * a.e.parts;
+      if (a.vec2)
+        start_part<WIDE, true>(a.e, mat, part, red);
+      else
+        start_part<WIDE, false>(a.e, mat, part, red);
+    }
+    ok = whole_barrier(c, a, 2 * gridDim.x);
+  }
+  unsigned int* bar = a.bars + 32;
+  const uint32_t done_bar = c.bar0 + 8u * L::kDoneBar, go_bar = c.bar0 + 8u * L::kGoBar;
+  if (!ok) {
+  } else if (c.warp == 0) {
+    Pipe p;
+    unsigned int products = 0;  // behind
+    // the product before is done, in all CTAs
+    auto meet = [&]() {
+      bool k = c.wait(done_bar, products & 1u, 0x77u);
+      ++products;
+      if (c.lane == 0 && k) {
+        count_up(bar);
+        k = count_wait(bar, products * gridDim.x, c.abort_flag);
+        if (k) mbar_arrive(go_bar);
+      }
+      k = all_waited(k);
+      fence_proxy_async();
+      return k;
+    };
+    fence_proxy_async();
+    ok = !(ld_shared_u32(c.inject()) & kStall);
+    for (int step = 0; ok && step < a.steps; ++step) {
+      const int x = step & 1;
+      const NsMaps g = {&maps.gram_a[x], &maps.gram_b[x]}, q = {&maps.poly_a, &maps.poly_b},
+                   u = {&maps.upd_a[x], &maps.upd_b[x]};
+#pragma unroll 1
+      for (int k = 0; ok && k < 3; ++k)
+        ok = (step + k == 0 || meet()) &&
+             ns_produce(c, k == 0 ? a.gram : k == 1 ? a.poly : a.update,
+                        k == 0 ? g : k == 1 ? q : u, p);
+    }
+    if (c.lane == 0) st_shared_u32(c.fills(), p.it);
+  } else if (c.warp == 1) {
+    Pipe p;
+    ok = all_waited(!quits(ld_shared_u32(c.inject()), c.abort_flag));
+#pragma unroll 1
+    for (int i = 0; ok && i < 3 * a.steps; ++i)
+      ok = ns_multiply(c, i % 3 == 0 ? a.gram : i % 3 == 1 ? a.poly : a.update, p);
+  } else if (c.warp >= 4) {
+    Chunks p;
+    uint32_t products = 0;
+    // a product's end for this warp: its stores have been written, and it says so
+    auto next = [&]() {
+      __syncwarp();
+      if (c.lane == 0) {
+        bulk_wait_group<0>();
+        fence_proxy_async();
+        mbar_arrive(done_bar);
+      }
+    };
+    auto meet = [&]() {
+      const bool k = all_waited(c.wait(go_bar, products & 1u, 0x78u));
+      ++products;
+      fence_proxy_async();
+      return k;
+    };
+    fence_proxy_async();
+#pragma unroll 1
+    for (int i = 0; ok && i < 3 * a.steps; ++i) {
+      const int step = i / 3, k = i - 3 * step, x = step & 1;
+      const bool last = step == a.steps - 1;
+      NsArgs n = k == 0 ? a.gram : k == 1 ? a.poly : a.update;
+      set_coefs(n, k, a.coefs + 3 * step, last);
+      NsMaps t = {};
+      t.in0 = k == 1 ? &maps.e : &maps.x[x];
+      t.in1 = t.out1 = &maps.lo;
+      t.out0 = k == 0 ? &maps.e : k == 1 ? &maps.f : last ? &maps.out : &maps.x[x ^ 1];
+      ok = (i == 0 || meet()) && ns_finish(c, n, t, p);
+      if (ok && i < 3 * a.steps - 1) next();
+    }
+    if (!ok) drain_chunks(c, p);
+    if (c.lane == 0) bulk_wait_group<0>();
+  }
+  ns_leave(c);
 }
 
 // ---- host side -----------------------------------------------------------------
@@ -683,21 +977,57 @@ bool make_map(CUtensorMap* map, const void* base, int64_t batch, int64_t rows, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int KIND, bool AMN, bool BMN>
+// How a product's tiles lie.
+void set_tiles(NsArgs& a, int64_t batch, int bm, int bn) {
+  a.tiles_m = (a.m + bm - 1) / bm;
+  a.tiles_n = (a.n + bn - 1) / bn;
+  const int per = bm / bn;  // a row's tiles up to the diagonal rise by these; past the
+  a.tiles_per = a.symmetric  // matrix's end there may be some, which have no chunks
+                    ? per * (a.tiles_m * (a.tiles_m + 1) / 2)
+                    : a.tiles_m * a.tiles_n;
+  a.tiles = (int)(a.tiles_per * batch);
+}
+
+template <bool LOADS>
 nvfp4_status launch_ns(const CUtensorMap& ma, const CUtensorMap& mb, const CUtensorMap& in0,
                        const CUtensorMap& in1, const CUtensorMap& out0, const CUtensorMap& out1,
                        NsArgs a, int64_t batch, int sms, cudaStream_t stream) {
-  using L = NsLayout<KIND>;
+  using L = PairLayout<LOADS>;
   static GemmLaunchState ls;
-  auto kern = ns_pair_kernel<KIND, AMN, BMN>;
+  auto kern = ns_pair_kernel<LOADS>;
   const int units = gemm_setup(ls, kern, L::kAlloc, L::kThreads, 0, 2, sms);
   if (units <= 0) return NVFP4_ERR_CUDA;
-  a.tiles_m = (a.m + kTile - 1) / kTile;
-  a.tiles_n = (a.n + kTile - 1) / kTile;
-  a.tiles_per = KIND <= kPoly ? a.tiles_m * (a.tiles_m + 1) / 2 : a.tiles_m * a.tiles_n;
-  a.tiles = (int)(a.tiles_per * batch);
+  set_tiles(a, batch, L::kBM, L::kBN);
   return cuda_status(launch_pdl(kern, 2 * std::min(units, a.tiles), L::kThreads, L::kAlloc, stream,
                                 ma, mb, in0, in1, out0, out1, a));
+}
+
+template <int BN, bool WIDE>
+nvfp4_status launch_whole(const WholeMaps& maps, WholeArgs& a, int sms, cudaStream_t stream) {
+  using L = WholeLayout<BN>;
+  static GemmLaunchState ls;
+  auto kern = whole_kernel<BN, WIDE>;
+  if (gemm_setup(ls, kern, L::kAlloc, L::kThreads, 0, 1, sms) <= 0) return NVFP4_ERR_CUDA;
+  set_tiles(a.gram, a.batch, L::kBM, BN);
+  set_tiles(a.poly, a.batch, L::kBM, BN);
+  set_tiles(a.update, a.batch, L::kBM, BN);
+  if (cudaMemsetAsync(a.bars, 0, kBarBytes, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  // no more CTAs than have a tile, or a share of the momentum
+  const int64_t share = (a.e.size * a.batch + 8191) / 8192;
+  const int ctas = (int)std::min<int64_t>(
+      sms, std::max<int64_t>({share, a.poly.tiles, a.update.tiles}));
+  a.e.parts = (int)std::min<int64_t>(kMaxParts, std::max<int64_t>(1, ctas / a.batch));
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, kern, maps, a));
 }
 
 // Where the parts of a workspace lie.
@@ -708,7 +1038,6 @@ struct Layout {
   size_t total;
   bool panel;
 };
-constexpr int kMaxParts = 1024;
 constexpr int64_t kMaxSide = 1 << 20;
 
 nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
@@ -728,8 +1057,18 @@ nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
   l->panel = muon_panel_fits(rows, cols);
   l->total = l->panel ? muon_panel_workspace(rows, cols)
                       : 3 * l->x_bytes + 2 * l->g_bytes + 2 * l->d_bytes +
-                            up1k((size_t)batch * kMaxParts * 4);
+                            up1k((size_t)batch * kMaxParts * 4) + kBarBytes;
   return NVFP4_OK;
+}
+
+// Whether one launch does it all: as long as the tiles of 128 x 128 of an update are
+// few.
+bool takes_whole(const Layout& l, int64_t batch, int sms) {
+  return ((l.m + 127) / 128) * ((l.n + 127) / 128) * batch <= kWholeTiles * sms;
+}
+// Its tiles' width.
+int whole_width(const Layout& l, int64_t batch, int sms) {
+  return ((l.m + 127) / 128) * ((l.n + 63) / 64) * batch <= sms ? 64 : 128;
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -823,77 +1162,106 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   e.eps = p->eps;
   e.nesterov = p->nesterov;
   e.zero = (flags & NVFP4_ZERO_GRAD) != 0;
+  const bool tall = p->rows > p->cols, whole = takes_whole(l, p->batch, dev.sm_count);
+  const int bn = whole ? whole_width(l, p->batch, dev.sm_count) : 256;
+  const int b_rows = whole ? bn : 128;  // rows of B that a CTA loads at a time
+  const bool vec1 = e.size % 4 == 0, vec2 = p->cols % 8 == 0;
+  WholeMaps t;
+  bool ok = true;
+  const int64_t mm = l.m;
+  for (int i = 0; i < 2; ++i) {
+    auto x = [&](CUtensorMap* map, int box_cols, int box_rows) {
+      ok = ok && make_map(map, hi[i], p->batch, p->rows, p->cols, l.ldx, box_cols, box_rows);
+    };
+    x(&t.gram_a[i], 64, tall ? 64 : 128);
+    x(&t.gram_b[i], 64, tall ? 64 : b_rows);
+    x(&t.x[i], 32, 32);
+    if (tall) {
+      x(&t.upd_a[i], 64, 128);
+      ok = ok && make_map(&t.upd_b[i], F, p->batch, mm, mm, l.ldm, 64, b_rows);
+    } else {
+      ok = ok && make_map(&t.upd_a[i], F, p->batch, mm, mm, l.ldm, 64, 128);
+      x(&t.upd_b[i], 64, 64);
+    }
+  }
+  ok = ok && make_map(&t.poly_a, E, p->batch, mm, mm, l.ldm, 64, 128) &&
+       make_map(&t.poly_b, E, p->batch, mm, mm, l.ldm, 64, b_rows) &&
+       make_map(&t.e, E, p->batch, mm, mm, l.ldm, 32, 32) &&
+       make_map(&t.f, F, p->batch, mm, mm, l.ldm, 32, 32) &&
+       make_map(&t.lo, lo, p->batch, p->rows, p->cols, l.ldx, 32, 32);
+  if (vec2)
+    ok = ok && make_map(&t.out, update, p->batch, p->rows, p->cols, p->cols, 32, 32, true);
+  else
+    t.out = t.lo;  // not read
+  if (!ok) return NVFP4_ERR_CUDA;
+
+  NsArgs gram = {}, poly, upd;
+  gram.m = gram.n = (int)l.m;
+  gram.k = (int)l.n;
+  gram.a_mn = gram.b_mn = tall;
+  gram.symmetric = 1;
+  gram.din = gram.dout = d;
+  gram.dstride = l.dstride;
+  poly = gram;
+  poly.k = (int)l.m;
+  poly.a_mn = poly.b_mn = 0;
+  poly.loads = poly.by_row = poly.by_col = 1;
+  poly.dout = db;
+  upd = poly;
+  upd.m = (int)p->rows;
+  upd.n = (int)p->cols;
+  upd.b_mn = !tall;
+  upd.symmetric = 0;
+  upd.loads = 2;
+  upd.by_row = !tall;
+  upd.by_col = tall;
+  upd.din = db;
+  upd.out = static_cast<__nv_bfloat16*>(update);
+  upd.out_boxes = vec2;
+
+  if (whole) {
+    WholeArgs a = {};
+    a.e = e;
+    a.gram = gram;
+    a.poly = poly;
+    a.update = upd;
+    a.bars = reinterpret_cast<unsigned int*>(w + l.total - kBarBytes);
+    a.batch = (int)p->batch;
+    a.steps = p->steps;
+    a.vec1 = vec1;
+    a.vec2 = vec2;
+    std::copy(p->coefs, p->coefs + 3 * p->steps, a.coefs);
+    if (bn == 64)
+      return wide ? launch_whole<64, true>(t, a, dev.sm_count, s)
+                  : launch_whole<64, false>(t, a, dev.sm_count, s);
+    return wide ? launch_whole<128, true>(t, a, dev.sm_count, s)
+                : launch_whole<128, false>(t, a, dev.sm_count, s);
+  }
+
   const int64_t want = std::max<int64_t>(1, (e.size + kEwThreads * 16 - 1) / (kEwThreads * 16));
   const int64_t fit = std::max<int64_t>(1, (int64_t)dev.sm_count * 8 / p->batch);
   e.parts = (int)std::min<int64_t>({want, fit, kMaxParts});
   const dim3 grid((unsigned)e.parts, (unsigned)p->batch);
-  const bool vec1 = e.size % 4 == 0, vec2 = p->cols % 8 == 0;
   auto k1 = wide ? (vec1 ? momentum_kernel<true, true> : momentum_kernel<true, false>)
                  : (vec1 ? momentum_kernel<false, true> : momentum_kernel<false, false>);
   auto k2 = wide ? (vec2 ? start_kernel<true, true> : start_kernel<true, false>)
                  : (vec2 ? start_kernel<false, true> : start_kernel<false, false>);
   if (launch_pdl(k1, grid, kEwThreads, 0, s, e) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (launch_pdl(k2, grid, kEwThreads, 0, s, e) != cudaSuccess) return NVFP4_ERR_CUDA;
-
-  const bool tall = p->rows > p->cols;
-  CUtensorMap xk[2], xmn[2], xbox[2], lobox, ek, fk, ebox, fbox, obox;
-  bool ok = true;
-  for (int i = 0; i < 2; ++i) {
-    ok = ok && make_map(&xk[i], hi[i], p->batch, p->rows, p->cols, l.ldx, 64, 128);
-    ok = ok && make_map(&xmn[i], hi[i], p->batch, p->rows, p->cols, l.ldx, 64, 64);
-    ok = ok && make_map(&xbox[i], hi[i], p->batch, p->rows, p->cols, l.ldx, 32, 32);
-  }
-  ok = ok && make_map(&lobox, lo, p->batch, p->rows, p->cols, l.ldx, 32, 32);
-  ok = ok && make_map(&ek, E, p->batch, l.m, l.m, l.ldm, 64, 128);
-  ok = ok && make_map(&fk, F, p->batch, l.m, l.m, l.ldm, 64, 128);
-  ok = ok && make_map(&ebox, E, p->batch, l.m, l.m, l.ldm, 32, 32);
-  ok = ok && make_map(&fbox, F, p->batch, l.m, l.m, l.ldm, 32, 32);
-  const bool out_boxes = p->cols % 8 == 0;
-  if (out_boxes)
-    ok = ok && make_map(&obox, update, p->batch, p->rows, p->cols, p->cols, 32, 32, true);
-  else
-    obox = lobox;  // not read
-  if (!ok) return NVFP4_ERR_CUDA;
-
   for (int i = 0; i < p->steps; ++i) {
     const int x = i & 1;
-    NsArgs a = {};
-    a.a = p->coefs[3 * i];
-    a.b = p->coefs[3 * i + 1];
-    a.c = p->coefs[3 * i + 2];
-    a.dstride = l.dstride;
-    a.m = a.n = (int)l.m;
-    a.k = (int)l.n;
-    a.din = d;
-    a.dout = d;
-    st = tall ? launch_ns<kGram, true, true>(xmn[x], xmn[x], ebox, ebox, ebox, ebox, a, p->batch,
-                                             dev.sm_count, s)
-              : launch_ns<kGram, false, false>(xk[x], xk[x], ebox, ebox, ebox, ebox, a, p->batch,
-                                               dev.sm_count, s);
-    if (st != NVFP4_OK) return st;
-    a.k = (int)l.m;
-    a.din = d;
-    a.dout = db;
-    st = launch_ns<kPoly, false, false>(ek, ek, ebox, ebox, fbox, fbox, a, p->batch, dev.sm_count,
-                                        s);
-    if (st != NVFP4_OK) return st;
-    a.m = (int)p->rows;
-    a.n = (int)p->cols;
-    a.din = db;
-    a.by_col = tall;
-    a.out = static_cast<__nv_bfloat16*>(update);
-    a.out_boxes = out_boxes;
     const bool last = i == p->steps - 1;
-    if (tall)
-      st = last ? launch_ns<kFinal, false, false>(xk[x], fk, xbox[x], lobox, obox, obox, a,
-                                                  p->batch, dev.sm_count, s)
-                : launch_ns<kUpdate, false, false>(xk[x], fk, xbox[x], lobox, xbox[x ^ 1], lobox, a,
-                                                   p->batch, dev.sm_count, s);
-    else
-      st = last ? launch_ns<kFinal, false, true>(fk, xmn[x], xbox[x], lobox, obox, obox, a,
-                                                 p->batch, dev.sm_count, s)
-                : launch_ns<kUpdate, false, true>(fk, xmn[x], xbox[x], lobox, xbox[x ^ 1], lobox, a,
-                                                  p->batch, dev.sm_count, s);
+    const float* abc = p->coefs + 3 * i;
+    set_coefs(gram, 0, abc, last);
+    set_coefs(poly, 1, abc, last);
+    set_coefs(upd, 2, abc, last);
+    st = launch_ns<false>(t.gram_a[x], t.gram_b[x], t.e, t.e, t.e, t.e, gram, p->batch,
+                          dev.sm_count, s);
+    if (st != NVFP4_OK) return st;
+    st = launch_ns<true>(t.poly_a, t.poly_b, t.e, t.e, t.f, t.f, poly, p->batch, dev.sm_count, s);
+    if (st != NVFP4_OK) return st;
+    st = launch_ns<true>(t.upd_a[x], t.upd_b[x], t.x[x], t.lo, last ? t.out : t.x[x ^ 1], t.lo, upd,
+                         p->batch, dev.sm_count, s);
     if (st != NVFP4_OK) return st;
   }
   return NVFP4_OK;
