@@ -334,14 +334,20 @@ struct Pipe {
   uint32_t it = 0;         // tiles done (which accumulator), producer: stages filled
 };
 
-// The producer's warp.
-template <class L>
-NVFP4_DEV bool ns_produce(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Pipe& p) {
+// The producer's warp.  `begin` waits for what the product reads, once the first tile
+// is known; false: given up.
+template <class L, class B>
+NVFP4_DEV bool ns_produce(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Pipe& p, B begin) {
   const int num_kb = (a.k + kBK - 1) / kBK;
-  for (int tile = c.unit; tile < a.tiles; tile += c.units) {
-    const int z = tile / a.tiles_per;
-    int tm, tn;
+  int tile = c.unit, z = 0, tm = 0, tn = 0;
+  auto find = [&]() {
+    if (tile >= a.tiles) return;
+    z = tile / a.tiles_per;
     tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
+  };
+  find();
+  if (!begin()) return false;
+  for (; tile < a.tiles; tile += c.units, find()) {
     const int a0 = tm * L::kBM + (int)c.rank * 128;
     const int b0 = tn * L::kBN + (int)c.rank * L::kRowsB;
     for (int kb = 0; kb < num_kb; ++kb) {
@@ -432,8 +438,8 @@ struct Chunks {
   uint32_t it = 0, loaded = 0, used = 0;
 };
 
-template <class L>
-NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Chunks& p) {
+template <class L, class B>
+NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Chunks& p, B begin) {
   const int ew = c.warp - 4, q = c.warp & 3, h = ew >> 2, lane = c.lane;
   uint8_t* slots = c.smem + L::offSlots + ew * (L::kSlots * L::kSlot);
   const uint32_t slot_bar = c.bar0 + 8u * (L::kSlotBar + ew * L::kSlots);
@@ -449,8 +455,10 @@ NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Ch
     return max(0, min(L::kChunks, (end - x + 31) / 32));
   };
   // the loads run up to kSlots - 1 chunks ahead, over the tiles
-  int ltile = a.loads ? c.unit : a.tiles, lc = 0, lcount = 0, lx, ly, lz;
-  if (ltile < a.tiles) lcount = place(ltile, lx, ly, lz);
+  int ltile = a.loads ? c.unit : a.tiles, lc = 0, lcount = 0, lx = 0, ly = 0, lz = 0;
+  int x0 = 0, y = 0, z = 0, count = 0;
+  if (c.unit < a.tiles) count = place(c.unit, x0, y, z);
+  if (a.loads) lx = x0, ly = y, lz = z, lcount = count;
   auto load_next = [&]() {
     while (ltile < a.tiles && lc >= lcount) {
       ltile += c.units;
@@ -468,14 +476,14 @@ NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Ch
     ++p.loaded;
     ++lc;
   };
+  if (!begin()) return false;
 #pragma unroll 1
   for (int i = 0; i < L::kSlots - 1; ++i) load_next();
   uint32_t stores = 0;  // chunks without loads
 #pragma unroll 1
   for (int tile = c.unit; tile < a.tiles; tile += c.units, ++p.it) {
     const uint32_t b = p.it & 1u;
-    int x0, y, z;
-    const int count = place(tile, x0, y, z);
+    if (tile != c.unit) count = place(tile, x0, y, z);
     const float* din = a.din + (int64_t)z * a.dstride;
     const int row = y + lane;
     // the diagonal's entries: this row's, and of the chunk's columns the lane's
@@ -625,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<LOADS>::k
   griddep_wait();
   if (c.warp == 0) {
     Pipe p;
-    if (!(ld_shared_u32(c.inject()) & kStall)) ns_produce(c, args, maps, p);
+    if (!(ld_shared_u32(c.inject()) & kStall)) ns_produce(c, args, maps, p, [] { return true; });
     if (c.lane == 0) st_shared_u32(c.fills(), p.it);
   } else if (c.warp == 1) {
     Pipe p;
@@ -633,7 +641,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<LOADS>::k
       ns_multiply(c, args, p);
   } else if (c.warp >= 4) {
     Chunks p;
-    if (!ns_finish(c, args, maps, p)) drain_chunks(c, p);
+    if (!ns_finish(c, args, maps, p, [] { return true; })) drain_chunks(c, p);
     if (c.lane == 0) bulk_wait_group<0>();
   }
   ns_leave(c);
@@ -837,7 +845,6 @@ NVFP4_DEV bool count_wait(const unsigned int* bar, unsigned int target, volatile
   return true;
 }
 NVFP4_DEV void count_up(unsigned int* bar) {
-  __threadfence();
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar) : "memory");
 }
 
@@ -847,7 +854,7 @@ NVFP4_DEV bool whole_barrier(const Ns<L>& c, const WholeArgs& a, unsigned int ta
   fence_proxy_async();
   __syncthreads();
   if (threadIdx.x == 0) {
-    if (!(injected() & kQuit) || blockIdx.x) count_up(a.bars);
+    count_up(a.bars);
     count_wait(a.bars, target, c.abort_flag);
   }
   __syncthreads();
@@ -911,9 +918,9 @@ __global__ void __launch_bounds__(WholeLayout<BN>::kThreads, 1)
                    u = {&maps.upd_a[x], &maps.upd_b[x]};
 #pragma unroll 1
       for (int k = 0; ok && k < 3; ++k)
-        ok = (step + k == 0 || meet()) &&
-             ns_produce(c, k == 0 ? a.gram : k == 1 ? a.poly : a.update,
-                        k == 0 ? g : k == 1 ? q : u, p);
+        ok = ns_produce(c, k == 0 ? a.gram : k == 1 ? a.poly : a.update,
+                        k == 0 ? g : k == 1 ? q : u, p,
+                        [&] { return step + k == 0 || meet(); });
     }
     if (c.lane == 0) st_shared_u32(c.fills(), p.it);
   } else if (c.warp == 1) {
@@ -951,7 +958,7 @@ __global__ void __launch_bounds__(WholeLayout<BN>::kThreads, 1)
       t.in0 = k == 1 ? &maps.e : &maps.x[x];
       t.in1 = t.out1 = &maps.lo;
       t.out0 = k == 0 ? &maps.e : k == 1 ? &maps.f : last ? &maps.out : &maps.x[x ^ 1];
-      ok = (i == 0 || meet()) && ns_finish(c, n, t, p);
+      ok = ns_finish(c, n, t, p, [&] { return i == 0 || meet(); });
       if (ok && i < 3 * a.steps - 1) next();
     }
     if (!ok) drain_chunks(c, p);

@@ -1,7 +1,8 @@
 """A mixture-of-experts MLP block on the library's calls, forward and backward:
 
     h      = norm(x) w_in                               the block's input
-    plan   = top-k of softmax(h Wr^T)                   the router
+    plan   = top-k of softmax(h Wr^T)                   the router (or by scores with a
+                                                        bias for balance, in groups)
     o      = experts' SwiGLU MLPs over the plan's rows  (NVFP4 products)
     z      = sum over a token's experts of weight * o
     y      = x + z_scale gate (.) norm(z) w_out         the next block's stream
@@ -18,10 +19,16 @@ so a step can be captured as a CUDA graph; its backward then takes the step's
 number from the device, since a captured number, and with it the stochastic
 rounding's random words, would be the same in every replay.
 
+The masters take plain SGD (`sgd`), or the matrices, each expert's by itself, the
+orthogonalised momentum and the vectors SGD (`muon`), whose last pass gives the
+weights' amaxes to the next forward's quantisation.
+
 ``python -m nvfp4_block_scaled_03_gb300.moe`` trains a small block for a few
 steps on a GB300 and prints the loss.
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -30,15 +37,26 @@ from . import binding as nv
 
 class MoEBlock:
     """`experts` SwiGLU experts of width `ffn` behind a top-`top` router, with
-    FP32 masters and their gradients (`grads`, by the parameters' names)."""
+    FP32 masters and their gradients (`grads`, by the parameters' names).  With
+    `score` (nv.SCORE_*) the router chooses by scores: `groups` of experts of which
+    `groups_kept` are kept, weights times `route_scale`, renormalised or not, and a
+    bias (`bias`, zero at first) that `balance` moves."""
 
     def __init__(self, hidden: int, ffn: int, experts: int, top: int, *, seed: int = 0,
                  z_scale: float = 1.0, eps: float = 1e-5, mode: int = nv.ROUTE_CHOSEN,
+                 score: int | None = None, groups: int = 1, groups_kept: int | None = None,
+                 group_top: int = 2, renormalise: bool = True, route_scale: float = 1.0,
                  device: str = "cuda"):
         if hidden % 128 or ffn % 128:
             raise ValueError("hidden and ffn must be multiples of 128")
         self.experts, self.top, self.mode = experts, top, mode
         self.eps, self.z_scale, self.seed = eps, z_scale, seed
+        # how the weights follow from the scores, and what else decides the choice
+        self.weighting = None
+        if score is not None:
+            self.weighting = dict(score=score, renormalise=renormalise, scale=route_scale)
+            self.choice = dict(groups=groups, groups_kept=groups_kept, group_top=group_top)
+            self.bias = torch.zeros(experts, device=device)
         g = torch.Generator(device=device).manual_seed(seed)
 
         def normal(*shape, scale):
@@ -55,6 +73,12 @@ class MoEBlock:
         }
         self.grads = {k: torch.zeros_like(v) for k, v in self.params.items()}
         self.hidden, self.ffn = hidden, ffn
+        self.matrices = {"router": (experts, hidden), "gate_proj": (experts, ffn, hidden),
+                         "up_proj": (experts, ffn, hidden), "down_proj": (experts, hidden, ffn)}
+        # the weights' amaxes as their last step gave them, in buffers that stay (a captured
+        # forward reads what the replay before has written), and of which weight they are
+        self.momentum, self.stepped = {}, {}
+        self.amax = {k: torch.zeros(1, device=device) for k in self.matrices if k != "router"}
         self.operand_ids = torch.arange(6, device=device)
 
     def _both(self, x, flags=0, offsets=(0, 0)):
@@ -70,6 +94,18 @@ class MoEBlock:
         nv.nvfp4_amax(x, row, col, seed=self.seed)
         return row, col
 
+    def _route(self, logits):
+        if self.weighting is None:
+            return nv.nvfp4_route_fwd(logits, self.top, self.mode)
+        return nv.nvfp4_route_scored_fwd(logits, self.top, bias=self.bias, **self.weighting,
+                                         **self.choice)
+
+    def _known_amax(self, name):
+        """The amax that a weight's last step gave, unless the weight was changed since."""
+        w = self.params[name]
+        same, version = self.stepped.get(name, (None, None))
+        return self.amax[name] if same is w and version == w._version else None
+
     def forward(self, x: torch.Tensor):
         """y [tokens, hidden] of x (bf16 or FP32); what the backward reads is
         kept in `self.saved`."""
@@ -78,12 +114,13 @@ class MoEBlock:
         _, s["h"] = nv.nvfp4_residual_norm_fwd(x, w_pre=p["w_in"], eps=self.eps)
         s["router"] = p["router"].bfloat16()
         s["logits"] = torch.mm(s["h"], s["router"].t(), out_dtype=torch.float32)
-        plan = s["plan"] = nv.nvfp4_route_fwd(s["logits"], self.top, self.mode)
+        plan = s["plan"] = self._route(s["logits"])
         groups = (plan.sizes, plan.offsets)
         xe = nv.nvfp4_dispatch(s["h"], plan.row, plan.source)
         qx, s["qx_col"] = self._both(xe)
         for name in ("gate_proj", "up_proj", "down_proj"):
-            s[name] = nv.nvfp4_quantize(p[name], nv.BLOCK_16X16, nv.EMIT_T)
+            s[name] = nv.nvfp4_quantize(p[name], nv.BLOCK_16X16, nv.EMIT_T,
+                                        amax=self._known_amax(name))
         s["G"] = nv.nvfp4_group_gemm(qx, s["gate_proj"], *groups)
         s["U"] = nv.nvfp4_group_gemm(qx, s["up_proj"], *groups)
         H, row, col = nv.nvfp4_swiglu_fwd(s["G"], s["U"], seed=self.seed)
@@ -130,7 +167,11 @@ class MoEBlock:
             nv.nvfp4_group_wgrad(qd_col, s["qx_col"], *groups, out=g[name].view(E, F, D),
                                  d_mode=nv.D_F32_ACCUM)
         dh = nv.nvfp4_combine(dxe, plan.row)
-        dlogits = nv.nvfp4_route_bwd(s["logits"], plan, dweight, self.mode).bfloat16()
+        if self.weighting is None:
+            dlogits = nv.nvfp4_route_bwd(s["logits"], plan, dweight, self.mode).bfloat16()
+        else:
+            dlogits = nv.nvfp4_route_scored_bwd(s["logits"], plan, dweight,
+                                                **self.weighting).bfloat16()
         g["router"] += torch.mm(dlogits.t(), s["h"], out_dtype=torch.float32)
         dh = torch.mm(dlogits, s["router"], out_dtype=torch.float32).add_(dh).bfloat16()
         dx, _, _, _, dw_in = nv.nvfp4_residual_norm_bwd(dx, dh, s["x"], w_pre=p["w_in"],
@@ -140,15 +181,43 @@ class MoEBlock:
 
     def sgd(self, lr: float):
         """One step on every FP32 master; the gradients are cleared."""
+        self.stepped.clear()
         for name, w in self.params.items():
             nv.nvfp4_sgd_step(w, self.grads[name], lr, zero_grad=True)
 
+    def muon(self, lr: float, vector_lr: float, mu: float = 0.95, decay: float = 0.0):
+        """One step: the matrices by their orthogonalised momentum, scaled to a root
+        mean square of about 0.2 an element whatever the shape, the vectors by SGD; the
+        gradients are cleared."""
+        for name, w in self.params.items():
+            shape = self.matrices.get(name)
+            if shape is None:
+                nv.nvfp4_sgd_step(w, self.grads[name], vector_lr, zero_grad=True)
+                continue
+            if name not in self.momentum:
+                self.momentum[name] = torch.zeros_like(w)
+            update = nv.nvfp4_muon_update(self.grads[name].view(shape),
+                                          self.momentum[name].view(shape), mu, zero_grad=True)
+            nv.nvfp4_muon_apply(w.view(shape), update, lr, 0.2 * math.sqrt(max(shape[-2:])), decay,
+                                self.amax.get(name))
+            if name in self.amax:
+                self.stepped[name] = w, w._version
+
+    def balance(self, rate: float):
+        """Moves the bias of a scored router by the last forward's loads."""
+        if self.weighting is None:
+            raise ValueError("the block's router has no bias: give it a score")
+        nv.nvfp4_route_balance(self.saved["plan"].sizes, self.bias, rate)
+
 
 def main(steps: int = 30, tokens: int = 500, hidden: int = 512, ffn: int = 1024, experts: int = 8,
-         top: int = 2, lr: float = 5.0):
-    """Fits a block to a fixed random map and prints the loss as it falls."""
+         top: int = 2, lr: float = 5.0, muon_lr: float | None = None):
+    """Fits a block to a fixed random map and prints the loss as it falls.  With
+    `muon_lr` the router scores by sigmoids with a bias for balance, in two groups, and
+    the matrices take their orthogonalised momentum."""
     torch.manual_seed(0)
-    block = MoEBlock(hidden, ffn, experts, top)
+    how = {} if muon_lr is None else dict(score=nv.SCORE_SIGMOID, groups=2, groups_kept=1)
+    block = MoEBlock(hidden, ffn, experts, top, **how)
     x = torch.randn(tokens, hidden, device="cuda")
     target = x + torch.randn(tokens, hidden, device="cuda")
     losses = []
@@ -156,7 +225,11 @@ def main(steps: int = 30, tokens: int = 500, hidden: int = 512, ffn: int = 1024,
         diff = block.forward(x) - target
         losses.append((diff * diff).mean().item())
         block.backward(diff * (2.0 / diff.numel() * hidden), step)
-        block.sgd(lr / tokens)
+        if muon_lr is None:
+            block.sgd(lr / tokens)
+        else:
+            block.muon(muon_lr, lr / tokens)
+            block.balance(1e-3)
         if step % 5 == 0 or step == steps - 1:
             print(f"step {step}: loss {losses[-1]:.4f}", flush=True)
     nv.check_device_errors()

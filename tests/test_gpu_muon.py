@@ -263,3 +263,47 @@ def test_large_layer():
 def test_many_matrices():
     for shape in itertools.chain([(300, 24, 40)], [(40, 264, 520)]):
         run(*inputs(shape, 22))
+
+
+# one launch a product on pairs; one launch for all; a team of CTAs by counters
+@pytest.mark.parametrize("shape", [(40, 264, 520), (300, 400), (128, 14336)],
+                         ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("quit", [False, True], ids=["stall", "quit"])
+def test_a_kernel_that_gives_up_recovers(shape, quit):
+    """Injected: no loads come (a CTA does not count itself in), or the MMA threads give
+    up with the loads in flight.  The error is reported, and the calls after it give what
+    they gave before."""
+    if quit and shape == (128, 14336):
+        pytest.skip("that kernel has no loads in flight")
+    g, m = inputs(shape, 23)
+    want = nv.nvfp4_muon_update(g, m.clone())
+    nv.check_device_errors()
+    nv.debug_inject(nv.QUIT_GEMM if quit else nv.STALL_GEMM, 1_000_000)
+    try:
+        nv.nvfp4_muon_update(g, m.clone())
+        with pytest.raises(nv.NVFP4Error) as e:
+            nv.check_device_errors()
+        assert e.value.status == nv.ERR_DEVICE_TIMEOUT
+    finally:
+        nv.debug_inject(0, 0)
+    nv.check_device_errors()
+    for _ in range(2):
+        assert torch.equal(nv.nvfp4_muon_update(g, m.clone()), want)
+    nv.check_device_errors()
+
+
+def test_two_streams_at_once():
+    """Calls of every kind side by side, each with its own workspace."""
+    shapes = [(64, 512), (300, 400), (128, 14336), (40, 264, 520)]
+    ins = [inputs(s, 24 + i) for i, s in enumerate(shapes)]
+    want = [nv.nvfp4_muon_update(g, m.clone()) for g, m in ins]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        bufs, got = [m.clone() for _, m in ins], []
+        torch.cuda.synchronize()
+        for (g, _), b, s in zip(ins, bufs, streams):
+            got.append(nv.nvfp4_muon_update(g, b, stream=s))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    nv.check_device_errors()
