@@ -594,16 +594,17 @@ def _on_device(call):
     """As _on_stream, for a call whose first tensor may lie on another device
     than the current one: the call then runs there, on that device's current
     stream."""
-    inner = _on_stream(call)
-
     @functools.wraps(call)
-    def run(first, *args, **kwargs):
+    def run(first, *args, stream=None, **kwargs):
         if not (isinstance(first, torch.Tensor) and first.is_cuda):
             raise ValueError(f"{call.__name__}: the first argument must be a CUDA tensor")
-        if first.get_device() == torch.cuda.current_device():
-            return inner(first, *args, **kwargs)
-        with torch.cuda.device(first.device):
-            return inner(first, *args, **kwargs)
+        if first.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(first.device):
+                return run(first, *args, stream=stream, **kwargs)
+        if stream is None:
+            return call(first, *args, **kwargs)
+        with torch.cuda.stream(stream):
+            return call(first, *args, **kwargs)
     return run
 
 
@@ -678,6 +679,9 @@ def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.
     return out
 
 
+_APPLY_BYTES = quantize_sizes(128, 128, ROW_1X16)[3]
+
+
 @_on_device
 def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: float = 1.0,
                      decay: float = 0.0, amax: torch.Tensor | None = None,
@@ -692,7 +696,7 @@ def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: fl
     else:
         _cuda(amax, _F32, "amax", (1,))
     if workspace is None:
-        workspace = _scratch(4096, W)
+        workspace = _scratch(_APPLY_BYTES, W)
     else:
         _cuda(workspace, _U8, "workspace")
     _together(W, update, amax, workspace)
@@ -779,9 +783,12 @@ def _logits(logits):
     return kind, tokens, experts, logits.stride(0) if tokens > 1 else experts
 
 
+_route_sizes = functools.lru_cache(maxsize=256)(route_sizes)
+
+
 def _plan_buffers(tokens, experts, top, plan, workspace, logits):
     """The plan and the workspace of a routing call, checked or new."""
-    rows, nbytes = route_sizes(tokens, experts, top)
+    rows, nbytes = _route_sizes(tokens, experts, top)
     if plan is None:
         plan = _alloc_plan(tokens, experts, top, rows, logits.device)
     else:
@@ -838,6 +845,11 @@ def nvfp4_route_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor
     return dlogits
 
 
+@functools.lru_cache(maxsize=256)
+def _route_params(*fields):
+    return RouteParams(*fields)
+
+
 @_on_device
 def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SIGMOID,
                            bias: torch.Tensor | None = None, groups: int = 1,
@@ -854,8 +866,8 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
         _cuda(bias, _F32, "bias", (experts,))
     _together(logits, bias, plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row,
               plan.source, workspace)
-    p = RouteParams(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, groups,
-                    groups if groups_kept is None else groups_kept, group_top, scale)
+    p = _route_params(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, groups,
+                      groups if groups_kept is None else groups_kept, group_top, scale)
     st = lib.nvfp4_route_scored_fwd(p, logits.data_ptr(), _ptr(bias), plan.expert.data_ptr(),
                                     plan.weight.data_ptr(), plan.sizes.data_ptr(),
                                     plan.offsets.data_ptr(), plan.row.data_ptr(),
@@ -882,7 +894,8 @@ def nvfp4_route_scored_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch
     else:
         _cuda(dlogits, logits.dtype, "dlogits", (tokens, experts))
     _together(logits, plan.expert, plan.weight, dweight, dlogits)
-    p = RouteParams(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, 1, 1, 1, scale)
+    p = _route_params(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, 1, 1, 1,
+                      scale)
     st = lib.nvfp4_route_scored_bwd(p, logits.data_ptr(), plan.expert.data_ptr(),
                                     plan.weight.data_ptr(), dweight.data_ptr(), dlogits.data_ptr(),
                                     _current(logits))

@@ -83,15 +83,12 @@ NVFP4_DEV float apply1(float w, float u, float keep, float step) {
 }
 
 template <bool AMAX>
-__global__ void __launch_bounds__(kThreads) muon_apply_kernel(float* __restrict__ W,
-                                                              const uint16_t* __restrict__ U,
-                                                              int64_t n, float keep, float step,
-                                                              float* partials) {
-  __shared__ float red[kThreads / 32];
+NVFP4_DEV float apply_share(float* __restrict__ W, const uint16_t* __restrict__ U, int64_t n,
+                            float keep, float step) {
   constexpr int kChunks = 2;
-  const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * kThreads;
+  const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * blockDim.x;
   float m = 0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n8; i += kChunks * stride) {
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += kChunks * stride) {
     float4 w[kChunks][2];
     uint4 u[kChunks];
 #pragma unroll
@@ -128,11 +125,42 @@ __global__ void __launch_bounds__(kThreads) muon_apply_kernel(float* __restrict_
     W[t] = r;
     if (AMAX) m = fmaxf(m, fabsf(r));
   }
+  return m;
+}
+
+template <bool AMAX>
+__global__ void __launch_bounds__(kThreads) muon_apply_kernel(float* __restrict__ W,
+                                                              const uint16_t* __restrict__ U,
+                                                              int64_t n, float keep, float step,
+                                                              float* partials) {
+  __shared__ float red[kThreads / 32];
+  float m = apply_share<AMAX>(W, U, n, keep, step);
   if (AMAX) {
     m = block_max(m, red);
     if (threadIdx.x == 0) partials[blockIdx.x] = m;
   }
 }
+
+// A small weight's step on one cluster, whose first CTA gathers the others' maxima: one
+// launch instead of two.
+constexpr int kClusterCtas = 8, kClusterThreads = 1024;
+__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+    muon_apply_small_kernel(float* __restrict__ W, const uint16_t* __restrict__ U, int64_t n,
+                            float keep, float step, float* amax) {
+  __shared__ float red[kClusterThreads / 32];
+  __shared__ float maxima[kClusterCtas];
+  const float m = block_max(apply_share<true>(W, U, n, keep, step), red);
+  if (threadIdx.x == 0)
+    st_cluster_u32(mapa_shared(smem_u32(&maxima[cluster_ctarank()]), 0), __float_as_uint(m));
+  cluster_sync();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    float most = maxima[0];
+    for (int c = 1; c < kClusterCtas; ++c) most = fmaxf(most, maxima[c]);
+    *amax = most;
+  }
+}
+// Up to here (us, one cluster and two launches, 262144 elements: 4.4, 6.2).
+constexpr int64_t kClusterElements = 1 << 18;
 
 // CTAs of a persistent launch: as many as are resident at once (looked up
 // once per kernel and device), at most one partial slot each, at most one
@@ -221,6 +249,10 @@ extern "C" nvfp4_status nvfp4_muon_apply(float* W, const void* update, int64_t n
   if (!amax) {
     const int grid = sgd_grid<muon_apply_kernel<false>>(n / 8, dev.sm_count);
     muon_apply_kernel<false><<<grid, kThreads, 0, s>>>(W, u, n, keep, step, nullptr);
+    return cuda_status(cudaGetLastError());
+  }
+  if (n <= kClusterElements) {
+    muon_apply_small_kernel<<<kClusterCtas, kClusterThreads, 0, s>>>(W, u, n, keep, step, amax);
     return cuda_status(cudaGetLastError());
   }
   float* partials = static_cast<float*>(workspace);

@@ -25,9 +25,12 @@
 // Scored choice (nvfp4_route_scored_fwd): by s + bias with s the softmax or the
 // sigmoid of the logits, among the best groups of experts, as 64 bits order them.
 // A warp computes the keys in FP32 and looks at the gaps between those that it
-// puts in an order; a token with a gap that the rounding could have turned round
-// (about one in a thousand) is done again in FP64, whose rate here would make it
-// the bound for all of them.  Without a bias the logits' own order decides.
+// puts in an order.  Where the rounding could have turned a gap round (one token in
+// some hundred) the candidates' keys are computed again in FP64, one a lane, and
+// ranked; FP64 for every expert of a token, which its rate here makes 5 us long, is
+// left for close groups and for a softmax's keys, whose sum it needs (all of them done
+// so took 51 us for 16384 tokens of 256 experts).  Without a bias the logits' own order
+// decides.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -42,6 +45,7 @@ constexpr int kWarps = 16;            // that rank a CTA's choices
 constexpr int kThreads = kWarps * 32;
 constexpr int kChooseWarps = 32;      // that make them
 constexpr int kChooseThreads = kChooseWarps * 32;
+constexpr int kScoredThreads = 640;   // that make them by scores: their registers
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 16;
 constexpr int kGroupAlign = 128;
@@ -67,6 +71,7 @@ struct RouteArgs {
   int score, renorm;
   int groups, kept, group_top;
   int group_size, lanes, per;  // of a group: experts, lanes that hold them, experts of a lane
+  int vec;                     // a lane's logits are whole aligned fours
   float scale;
   // backward
   const float* dweight;
@@ -207,11 +212,46 @@ NVFP4_DEV float open_logit(float v) {
   return v > -INFINITY ? fminf(v, WIDE ? 3.402823466e38f : 3.3895314e38f) : -INFINITY;
 }
 
-// Unsigned order of the floats, 0 for -inf and NaN; +-0 are equal.
-NVFP4_DEV uint32_t order_key(float v) {
-  if (!(v > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+// A lane's logits of token t.
+template <int NI, bool WIDE>
+NVFP4_DEV void load_share(const RouteArgs& a, int64_t t, const Share mine, float (&v)[NI]) {
+  const int64_t at = t * a.ld + mine.first;
+  if (NI % 4 == 0 && a.vec) {
+#pragma unroll
+    for (int i = 0; i < NI; i += 4) {
+      float4 u = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < mine.count) {
+        if (WIDE) {
+          u = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + at + i);
+        } else {
+          const uint2 w =
+              *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + at + i);
+          u = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                          __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+        }
+      }
+      v[i] = open_logit<WIDE>(u.x);
+      v[i + 1] = open_logit<WIDE>(u.y);
+      v[i + 2] = open_logit<WIDE>(u.z);
+      v[i + 3] = open_logit<WIDE>(u.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      v[i] = i < mine.count ? open_logit<WIDE>(load_logit<WIDE>(a.logits, at + i)) : -INFINITY;
+  }
+}
+
+// The largest of a warp's floats (NaN left out), and the smallest.
+NVFP4_DEV float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
+}
+NVFP4_DEV float redux_min(float v) {
+  float r;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 NVFP4_DEV double shfl_xor_double(double v, int o) {
@@ -230,12 +270,9 @@ __device__ __noinline__ int choose_exact(const RouteArgs& a, int64_t t) {
   const double none = -__longlong_as_double(0x7FF0000000000000ll);
   const Share mine = lane_share(a, lane);
   float l[NI], most = -INFINITY;
+  load_share<NI, WIDE>(a, t, mine, l);
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    l[i] = i < mine.count ? open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + mine.first + i))
-                          : -INFINITY;
-    most = fmaxf(most, l[i]);
-  }
+  for (int i = 0; i < NI; ++i) most = fmaxf(most, l[i]);
   most = warp_max(most);
   double key[NI], all = 0.0;
 #pragma unroll
@@ -342,23 +379,90 @@ NVFP4_DEV float slot_weight(const RouteArgs& a, float l, float most, float all) 
   return some ? a.scale * (1.0f / (1.0f + expf(-l))) : 0.0f;
 }
 
-// Experts and weights of token t by their scores, one warp.  bias: of this lane's
-// experts.
-template <int NI, bool WIDE>
-NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
-                             const float (&bias)[NI], int* hist) {
+// The first `count` lanes' experts in the order of their sigmoids plus biases in FP64.
+template <bool WIDE>
+__device__ __noinline__ int rank_exact(const RouteArgs& a, int64_t t, int expert, int count) {
   const int lane = threadIdx.x & 31;
-  float v[NI], l_most = -INFINITY;
+  double key = 0.0;
+  if (lane < count) {
+    const float l = open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + expert));
+    key = 1.0 / (1.0 + exp(-(double)l)) + (double)a.bias[expert];
+  }
+  int rank = 0;
+  for (int i = 0; i < count; ++i) {
+    const double k = shfl_double(key, i);
+    const int e = __shfl_sync(0xFFFFFFFFu, expert, i);
+    rank += k > key || (k == key && e < expert);
+  }
+  int sorted = -1;
+  for (int i = 0; i < count; ++i) {
+    const int e = __shfl_sync(0xFFFFFFFFu, expert, i), r = __shfl_sync(0xFFFFFFFFu, rank, i);
+    if (r == lane) sorted = e;
+  }
+  return sorted;
+}
+
+// The experts of the first lanes by their keys, a round for each: at least `top` of them
+// and with a bias on to the first clear gap, `count` in all (33: there is none).  close:
+// a gap before that is not clear.
+template <int NI, bool WIDE>
+__device__ __noinline__ int choose_rounds(const RouteArgs& a, int64_t t, const Share mine,
+                                          const float (&keys)[NI], float near0, int& count,
+                                          bool& close) {
+  const int lane = threadIdx.x & 31;
+  const bool softmax = a.score == NVFP4_SCORE_SOFTMAX;
+  float key[NI], last = INFINITY, best = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
-    v[i] = i < mine.count ? open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + mine.first + i))
-                          : -INFINITY;
-    l_most = fmaxf(l_most, v[i]);
+    key[i] = keys[i];
+    best = fmaxf(best, key[i]);
   }
+  int expert = -1, last_e = -1;
+  close = false;
+  for (count = 0; count <= 32; ++count) {
+    const float m = redux_max(best);
+    const bool near = a.bias && last - m <= near0 * (softmax ? 1.0f : fmaxf(1.0f, fabsf(m))) +
+                                                5e-7f * fabsf(m);
+    if (!(m > -INFINITY) || (count >= a.top && !near)) break;
+    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
+    int at = 0;
+    if (lane == from) {  // takes its first such key out
+#pragma unroll
+      for (int i = NI - 1; i >= 0; --i) at = key[i] == m ? i : at;
+      best = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        key[i] = i == at ? -INFINITY : key[i];
+        best = fmaxf(best, key[i]);
+      }
+    }
+    const int e = __shfl_sync(0xFFFFFFFFu, mine.first + at, from);
+    if (near) {
+      const float p = load_logit<WIDE>(a.logits, t * a.ld + last_e);
+      const float q = load_logit<WIDE>(a.logits, t * a.ld + e);
+      close = close || !(p == q && a.bias[last_e] == a.bias[e]);
+    }
+    last = m;
+    last_e = e;
+    if (lane == count) expert = e;
+  }
+  return expert;
+}
+
+// Experts and weights of token t by their scores, one warp.  v: this lane's logits;
+// bias: of this lane's experts; list: the warp's, in shared memory.
+template <int NI, bool WIDE>
+NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
+                             const float (&v)[NI], const float (&bias)[NI], uint2* list,
+                             int* hist) {
+  const int lane = threadIdx.x & 31;
+  float l_most = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) l_most = fmaxf(l_most, v[i]);
   const bool softmax = a.score == NVFP4_SCORE_SOFTMAX;
   float all = 1.0f, inv = 1.0f;
   if (softmax) {
-    l_most = fmaxf(warp_max(l_most), -3.402823466e38f);
+    l_most = fmaxf(redux_max(l_most), -3.402823466e38f);
     if (a.bias || !a.renorm) {
       all = 0.0f;
 #pragma unroll
@@ -367,101 +471,141 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
       inv = all > 0.0f ? 1.0f / all : 0.0f;
     }
   }
-  // keys, and how near two may be to be told apart: the scores are good to 3e-7
-  // (the softmax's to 2e-6 of the largest), a sum to half a step more
-  uint32_t key[NI];
-  const float near0 = softmax ? 5e-6f * inv : 1e-6f;
+  // keys, -inf for what is never chosen, and how near two may be to be told apart: a
+  // sigmoid is good to 2.5e-7 (its exponential's (2 + 1.2 |l|) 2^-23 of a share
+  // s (1 - s), and two roundings), a softmax's score to 2e-6 of the largest, and a sum
+  // to half a step more
+  float key[NI];
+  const float near0 = softmax ? 5e-6f * inv : 6e-7f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    float k = v[i];
-    if (a.bias) {
+  for (int i = 0; i < NI; ++i) key[i] = v[i];
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
       const float s = softmax ? expf(v[i] - l_most) * inv
                               : __fdividef(1.0f, 1.0f + __expf(fminf(-v[i], 80.0f)));
-      k = v[i] > -INFINITY ? s + bias[i] : -INFINITY;
+      key[i] = v[i] > -INFINITY ? s + bias[i] : -INFINITY;
     }
-    key[i] = order_key(k);
   }
   bool doubt = false;
   if (a.groups > 1) {
-    uint32_t best = 0u, next = 0u;
+    float best = -INFINITY, next = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      next = max(next, min(best, key[i]));
-      best = max(best, key[i]);
+      next = fmaxf(next, fminf(best, key[i]));
+      best = fmaxf(best, key[i]);
     }
     for (int o = 1; o < a.lanes; o <<= 1) {
-      const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
-      const uint32_t n = __shfl_xor_sync(0xFFFFFFFFu, next, o);
-      next = max(max(next, n), min(best, b));
-      best = max(best, b);
+      const float b = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+      const float n = __shfl_xor_sync(0xFFFFFFFFu, next, o);
+      next = fmaxf(fmaxf(next, n), fminf(best, b));
+      best = fmaxf(best, b);
     }
-    float worth = key_value<true>(max(best, 1u)), size = fabsf(worth), near = 0.0f;
+    float worth = best, near = 0.0f;
     if (a.group_top == 2) {
-      const float second = key_value<true>(max(next, 1u));
+      const bool two = next > -INFINITY;
       if (a.bias) {
-        worth = next ? worth + second : worth;
-        size += next ? fabsf(second) : 0.0f;
+        worth = two ? best + next : best;
       } else if (softmax) {
-        worth = expf(worth - l_most) + (next ? expf(second - l_most) : 0.0f);
+        worth = expf(best - l_most) + (two ? expf(next - l_most) : 0.0f);
         near = 1e-5f * worth;
       } else {
-        worth = 1.0f / (1.0f + expf(-worth)) + (next ? 1.0f / (1.0f + expf(-second)) : 0.0f);
+        worth = 1.0f / (1.0f + expf(-best)) + (two ? 1.0f / (1.0f + expf(-next)) : 0.0f);
         near = 2e-6f * worth;
       }
+      worth = best > -INFINITY ? worth : -INFINITY;
     }
-    if (a.bias) near = 2.0f * near0 + 1e-6f * size;
-    const uint32_t w = best ? order_key(worth) : 0u;
+    if (a.bias) near = 2.0f * near0 + 1e-6f * (fabsf(best) + (a.group_top == 2 ? fabsf(next) : 0.0f));
     const int g = lane / a.lanes;
     int rank = 0;
+#pragma unroll 4
     for (int h = 0; h < a.groups; ++h) {
-      const uint32_t u = __shfl_sync(0xFFFFFFFFu, w, h * a.lanes);
-      rank += u > w || (u == w && h < g);
+      const float u = __shfl_sync(0xFFFFFFFFu, worth, h * a.lanes);
+      rank += u > worth || (u == worth && h < g);
     }
     const bool keep = rank < a.kept;
     if (a.bias || a.group_top == 2) {
-      const uint32_t in = __reduce_min_sync(0xFFFFFFFFu, keep ? w : 0xFFFFFFFFu);
-      const uint32_t out = __reduce_max_sync(0xFFFFFFFFu, keep ? 0u : w);
-      const float margin = __uint_as_float(
-          __reduce_max_sync(0xFFFFFFFFu, __float_as_uint((w == in || w == out) ? near : 0.0f)));
-      doubt = out != 0u && key_value<true>(in) - key_value<true>(out) <= margin;
+      const float in = redux_min(keep ? worth : INFINITY);
+      const float out = redux_max(keep ? -INFINITY : worth);
+      if (out > -INFINITY) {
+        const float margin = redux_max(worth == in || worth == out ? near : 0.0f);
+        doubt = !(in - out > margin);
+      }
     }
     if (!keep)
 #pragma unroll
-      for (int i = 0; i < NI; ++i) key[i] = 0u;
+      for (int i = 0; i < NI; ++i) key[i] = -INFINITY;
   }
+  // Candidates: what is not below the `top`-th largest of the lanes' maxima (below which
+  // `top` keys cannot all lie), nor near it.  About a dozen, which take a lane each and
+  // are ranked together; 86 instructions for each of `top` rounds over all keys are 690
+  // of 1300 for a token otherwise.
+  float best = key[0];
+#pragma unroll
+  for (int i = 1; i < NI; ++i) best = fmaxf(best, key[i]);
+  float least = INFINITY;
+  for (int j = 0; j < a.top; ++j) {
+    least = redux_max(best);
+    best = best == least ? -INFINITY : best;
+  }
+  auto margin = [&](float k) {
+    return a.bias ? near0 * (softmax ? 1.0f : fmaxf(1.0f, fabsf(k))) + 5e-7f * fabsf(k) : 0.0f;
+  };
+  least -= least > -INFINITY ? 2.0f * margin(least) : 0.0f;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const bool in = key[i] >= least && key[i] > -INFINITY;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, in);
+    const int at = count + __popc(mask & ((1u << lane) - 1u));
+    if (in && at < 32) list[at] = make_uint2(__float_as_uint(key[i]), (uint32_t)(mine.first + i));
+    count += __popc(mask);
+  }
+  __syncwarp();
   int expert = -1;
-  float last = INFINITY;
-  int last_e = -1;
-  // with a bias one round more, for the gap behind the last slot
-  const int rounds = a.bias ? a.top + 1 : a.top;
-  for (int j = 0; j < rounds && !doubt; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < NI; ++i) best = max(best, key[i]);
-    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, best);
-    if (m == 0u) break;
-    int at = 0;
-#pragma unroll
-    for (int i = NI - 1; i >= 0; --i) at = key[i] == m ? i : at;
-    const int from = __ffs(__ballot_sync(0xFFFFFFFFu, best == m)) - 1;
-    const int e = __shfl_sync(0xFFFFFFFFu, mine.first + at, from);
-    if (a.bias) {
-      const float k = key_value<true>(m);
-      if (last - k <= near0 * (softmax ? 1.0f : fmaxf(1.0f, fabsf(k))) + 5e-7f * fabsf(k)) {
-        // equal logits with equal biases are equal in any arithmetic
-        const float p = load_logit<WIDE>(a.logits, t * a.ld + last_e);
-        const float q = load_logit<WIDE>(a.logits, t * a.ld + e);
-        doubt = !(p == q && a.bias[last_e] == a.bias[e]);
-      }
-      last = k;
-      last_e = e;
+  bool close = false;
+  if (count <= 32) {
+    float k = -INFINITY;
+    if (lane < count) {
+      k = __uint_as_float(list[lane].x);
+      expert = (int)list[lane].y;
     }
-    if (lane == j && j < a.top) expert = e;
-    if (lane == from)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) key[i] = i == at ? 0u : key[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const uint2 u = list[i];
+      const float o = __uint_as_float(u.x);
+      rank += o > k || (o == k && (int)u.y < expert);
+    }
+    __syncwarp();
+    if (lane < count) list[rank] = make_uint2(__float_as_uint(k), (uint32_t)expert);
+    __syncwarp();
+    expert = -1;
+    if (lane < count) {
+      const uint2 u = list[lane];
+      k = __uint_as_float(u.x);
+      expert = (int)u.y;
+      if (a.bias && lane > 0) {
+        const uint2 w = list[lane - 1];
+        if (__uint_as_float(w.x) - k <= margin(k)) {
+          // equal logits with equal biases are equal in any arithmetic
+          const float p = load_logit<WIDE>(a.logits, t * a.ld + w.y);
+          const float q = load_logit<WIDE>(a.logits, t * a.ld + expert);
+          close = !(p == q && a.bias[w.y] == a.bias[expert]);
+        }
+      }
+    }
+    close = __any_sync(0xFFFFFFFFu, close);
+    __syncwarp();
+  } else {
+    // many alike: one after the other, up to the first clear gap behind the last slot
+    expert = choose_rounds<NI, WIDE>(a, t, mine, key, near0, count, close);
   }
-  if (doubt) expert = choose_exact<NI, WIDE>(a, t);
+  if (doubt || (close && (softmax || count > 32)))
+    expert = choose_exact<NI, WIDE>(a, t);
+  else if (close)
+    expert = rank_exact<WIDE>(a, t, expert, count);
+  if (lane >= a.top) expert = -1;
   float l = -INFINITY;
   if (expert >= 0) l = open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + expert));
   const float weight = slot_weight(a, l, l_most, all);
@@ -475,20 +619,31 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
 // Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
 template <int NI, bool WIDE, bool SCORED>
 NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
-  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) hist[e] = 0;
-  for (int64_t r = (int64_t)blockIdx.x * kChooseThreads + threadIdx.x; r < a.rows;
-       r += (int64_t)gridDim.x * kChooseThreads)
+  constexpr int kThr = SCORED ? kScoredThreads : kChooseThreads;
+  for (int e = threadIdx.x; e < a.experts; e += kThr) hist[e] = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kThr + threadIdx.x; r < a.rows;
+       r += (int64_t)gridDim.x * kThr)
     a.source[r] = -1;
   __syncthreads();
   int t, t1;
-  warp_tokens(a, kChooseWarps, t, t1);
+  warp_tokens(a, kThr / 32, t, t1);
   if constexpr (SCORED) {
     const Share mine = lane_share(a, threadIdx.x & 31);
     float bias[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       bias[i] = a.bias && i < mine.count ? a.bias[mine.first + i] : 0.0f;
-    for (; t < t1; ++t) choose_scored<NI, WIDE>(a, t, mine, bias, hist);
+    // a token's logits come in while the one before is chosen for
+    __shared__ uint2 lists[kScoredThreads];
+    float next[NI];
+    if (t < t1) load_share<NI, WIDE>(a, t, mine, next);
+    for (; t < t1; ++t) {
+      float v[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) v[i] = next[i];
+      if (t + 1 < t1) load_share<NI, WIDE>(a, t + 1, mine, next);
+      choose_scored<NI, WIDE>(a, t, mine, v, bias, lists + (threadIdx.x & ~31u), hist);
+    }
   } else {
     if (NI <= 8)  // more would not leave registers for two tokens
       for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
@@ -572,11 +727,11 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
 }
 
 template <int NI, bool WIDE, bool SCORED>
-__global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(SCORED ? kScoredThreads : kChooseThreads) route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
   griddep_wait();
   choose<NI, WIDE, SCORED>(a, hist);
-  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads)
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
     a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
@@ -636,11 +791,11 @@ __global__ void __launch_bounds__(kThreads) route_assign_kernel(const RouteArgs 
 }
 
 template <int NI, bool WIDE, bool SCORED>
-__global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(SCORED ? kScoredThreads : kChooseThreads) route_small_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
   choose<NI, WIDE, SCORED>(a, s.total);
-  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) s.before[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) s.before[e] = 0;
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);
 }
@@ -932,10 +1087,10 @@ nvfp4_status check_route(int64_t tokens, int64_t experts, int32_t top) {
 
 template <int NI, bool WIDE, bool SCORED>
 cudaError_t launch_route(RouteArgs& a, int ctas, cudaStream_t stream) {
-  if (ctas == 1)
-    return launch_pdl(route_small_kernel<NI, WIDE, SCORED>, 1, kChooseThreads, 0, stream, a);
+  constexpr int kThr = SCORED ? kScoredThreads : kChooseThreads;
+  if (ctas == 1) return launch_pdl(route_small_kernel<NI, WIDE, SCORED>, 1, kThr, 0, stream, a);
   const cudaError_t e =
-      launch_pdl(route_choose_kernel<NI, WIDE, SCORED>, ctas, kChooseThreads, 0, stream, a);
+      launch_pdl(route_choose_kernel<NI, WIDE, SCORED>, ctas, kThr, 0, stream, a);
   if (e != cudaSuccess) return e;
   const cudaError_t f = launch_pdl(route_scan_kernel, (a.experts + 31) / 32, 1024, 0, stream, a);
   if (f != cudaSuccess) return f;
@@ -956,7 +1111,8 @@ cudaError_t call_route(int64_t experts, RouteArgs& a, int ctas, cudaStream_t s) 
          : experts <= 64  ? launch_route<2, WIDE, SCORED>(a, ctas, s)
          : experts <= 128 ? launch_route<4, WIDE, SCORED>(a, ctas, s)
          : experts <= 256 ? launch_route<8, WIDE, SCORED>(a, ctas, s)
-                          : launch_route<16, WIDE, SCORED>(a, ctas, s);
+         : SCORED && experts <= 384 ? launch_route<12, WIDE, SCORED>(a, ctas, s)
+                                    : launch_route<16, WIDE, SCORED>(a, ctas, s);
 }
 template <bool WIDE>
 cudaError_t call_route_bwd(int64_t experts, RouteArgs& a, cudaStream_t s) {
@@ -1046,6 +1202,8 @@ static nvfp4_status route_fwd(const void* logits, int32_t in_dtype, int64_t toke
   int ctas = route_ctas(tokens, dev.sm_count);
   a.per_cta = (int)((tokens + ctas - 1) / ctas);
   ctas = a.ctas = (int)((tokens + a.per_cta - 1) / a.per_cta);
+  const uintptr_t vec = reinterpret_cast<uintptr_t>(logits) | (uintptr_t)(ld * (wide ? 4 : 2));
+  a.vec = scored && a.per % 4 == 0 && a.group_size % 4 == 0 && vec % (wide ? 16 : 8) == 0;
   if (!scored)
     return cuda_status(wide ? call_route<true, false>(experts, a, ctas, stream)
                             : call_route<false, false>(experts, a, ctas, stream));
