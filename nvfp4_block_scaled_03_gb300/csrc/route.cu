@@ -624,27 +624,39 @@ NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
   for (int64_t r = (int64_t)blockIdx.x * kThr + threadIdx.x; r < a.rows;
        r += (int64_t)gridDim.x * kThr)
     a.source[r] = -1;
+  __shared__ int taken;
+  if (threadIdx.x == 0) taken = 0;
   __syncthreads();
-  int t, t1;
-  warp_tokens(a, kThr / 32, t, t1);
   if constexpr (SCORED) {
     const Share mine = lane_share(a, threadIdx.x & 31);
     float bias[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       bias[i] = a.bias && i < mine.count ? a.bias[mine.first + i] : 0.0f;
-    // a token's logits come in while the one before is chosen for
+    // The warps take the CTA's tokens one after the other, for some cost more; a token's
+    // logits come in while the one before is chosen for.
     __shared__ uint2 lists[kScoredThreads];
+    const int c0 = blockIdx.x * a.per_cta, n = min(a.per_cta, a.tokens - c0);
+    auto take = [&]() {
+      int k = 0;
+      if ((threadIdx.x & 31) == 0) k = atomicAdd(&taken, 1);
+      return __shfl_sync(0xFFFFFFFFu, k, 0);
+    };
     float next[NI];
-    if (t < t1) load_share<NI, WIDE>(a, t, mine, next);
-    for (; t < t1; ++t) {
+    int k = take();
+    if (k < n) load_share<NI, WIDE>(a, c0 + k, mine, next);
+    while (k < n) {
       float v[NI];
 #pragma unroll
       for (int i = 0; i < NI; ++i) v[i] = next[i];
-      if (t + 1 < t1) load_share<NI, WIDE>(a, t + 1, mine, next);
+      const int t = c0 + k;
+      k = take();
+      if (k < n) load_share<NI, WIDE>(a, c0 + k, mine, next);
       choose_scored<NI, WIDE>(a, t, mine, v, bias, lists + (threadIdx.x & ~31u), hist);
     }
   } else {
+    int t, t1;
+    warp_tokens(a, kThr / 32, t, t1);
     if (NI <= 8)  // more would not leave registers for two tokens
       for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
     for (; t < t1; ++t) choose_tokens<NI, WIDE, 1>(a, t, hist);
