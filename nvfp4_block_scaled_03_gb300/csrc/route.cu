@@ -27,9 +27,9 @@
 // A warp computes the keys in FP32 and looks at the gaps between those that it
 // puts in an order.  Where the rounding could have turned a gap round (one token in
 // some hundred) the candidates' keys are computed again in FP64, one a lane, and
-// ranked; FP64 for every expert of a token, which its rate here makes 5 us long, is
-// left for close groups and for a softmax's keys, whose sum it needs (all of them done
-// so took 51 us for 16384 tokens of 256 experts).  Without a bias the logits' own order
+// ranked, or close groups' worths of their best two; FP64 for every expert of a token,
+// which its rate here makes 7 us long, is left for a softmax's keys, whose sum it needs
+// (16384 tokens of 256 experts: 51 us with it for all of them).  Without a bias the logits' own order
 // decides.
 #include <algorithm>
 #include <climits>
@@ -379,6 +379,58 @@ NVFP4_DEV float slot_weight(const RouteArgs& a, float l, float most, float all) 
   return some ? a.scale * (1.0f / (1.0f + expf(-l))) : 0.0f;
 }
 
+// Whether the group of this lane is kept, by sigmoids plus biases in FP64 of the best
+// experts of each.  False: which those are is not clear either.
+template <int NI, bool WIDE>
+__device__ __noinline__ bool groups_exact(const RouteArgs& a, int64_t t, const Share mine,
+                                          const float (&key)[NI], float near0, bool& keep) {
+  const int lane = threadIdx.x & 31;
+  float k1 = -INFINITY, k2 = -INFINITY, k3 = -INFINITY;
+  int e1 = 0, e2 = 0;
+  auto add = [&](float k, int e) {
+    if (k > k1) {
+      k3 = k2;
+      k2 = k1, e2 = e1;
+      k1 = k, e1 = e;
+    } else if (k > k2) {
+      k3 = k2;
+      k2 = k, e2 = e;
+    } else {
+      k3 = fmaxf(k3, k);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NI; ++i) add(key[i], mine.first + i);
+  for (int o = 1; o < a.lanes; o <<= 1) {
+    const float o1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
+    const float o3 = __shfl_xor_sync(0xFFFFFFFFu, k3, o);
+    const int f1 = __shfl_xor_sync(0xFFFFFFFFu, e1, o), f2 = __shfl_xor_sync(0xFFFFFFFFu, e2, o);
+    add(o1, f1);
+    add(o2, f2);
+    add(o3, 0);  // never above both
+  }
+  const float in = a.group_top == 2 ? k2 : k1, out = a.group_top == 2 ? k3 : k2;
+  const float margin = 2.0f * (near0 * fmaxf(1.0f, fabsf(in)) + 5e-7f * fabsf(in));
+  if (__any_sync(0xFFFFFFFFu, out > -INFINITY && in - out <= margin)) return false;
+  double worth = -__longlong_as_double(0x7FF0000000000000ll);
+  if (k1 > -INFINITY) {
+    auto value = [&](int e) {
+      const float l = open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + e));
+      return 1.0 / (1.0 + exp(-(double)l)) + (double)a.bias[e];
+    };
+    worth = value(e1);
+    if (a.group_top == 2 && k2 > -INFINITY) worth += value(e2);
+  }
+  const int g = lane / a.lanes;
+  int rank = 0;
+  for (int h = 0; h < a.groups; ++h) {
+    const double w = shfl_double(worth, h * a.lanes);
+    rank += w > worth || (w == worth && h < g);
+  }
+  keep = rank < a.kept;
+  return true;
+}
+
 // The first `count` lanes' experts in the order of their sigmoids plus biases in FP64.
 template <bool WIDE>
 __device__ __noinline__ int rank_exact(const RouteArgs& a, int64_t t, int expert, int count) {
@@ -523,13 +575,15 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
       const float u = __shfl_sync(0xFFFFFFFFu, worth, h * a.lanes);
       rank += u > worth || (u == worth && h < g);
     }
-    const bool keep = rank < a.kept;
+    bool keep = rank < a.kept;
     if (a.bias || a.group_top == 2) {
       const float in = redux_min(keep ? worth : INFINITY);
       const float out = redux_max(keep ? -INFINITY : worth);
       if (out > -INFINITY) {
         const float margin = redux_max(worth == in || worth == out ? near : 0.0f);
         doubt = !(in - out > margin);
+        if (doubt && a.bias && !softmax)
+          doubt = !groups_exact<NI, WIDE>(a, t, mine, key, near0, keep);
       }
     }
     if (!keep)
