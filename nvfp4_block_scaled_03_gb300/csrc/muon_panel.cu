@@ -12,8 +12,9 @@
 //   X <- (a + d'_i) X + F X of its own blocks, in place
 // A block, rows of 128 bytes with the 128-byte swizzle, is a K-major operand of the
 // Gram product and an MN-major one of F X: one image serves both.  Rows behind m are
-// zeros up to a multiple of 16; what an operand of 128 rows reads behind those
-// reaches rows of the result that nobody looks at.  For m up to 64 F's rows stand
+// zeros up to a multiple of 16; what an operand of 128 rows reads behind those (E, the
+// blocks' first halves and their second halves follow one another) reaches rows of the
+// result that nobody looks at.  For m up to 64 F's rows stand
 // there again, so that every quarter of tensor memory, and with it every warp, has a
 // share of the columns of F X.
 //
@@ -27,12 +28,8 @@ namespace {
 
 constexpr int kPanelThreads = 512, kColWarps = kPanelThreads / 128;
 constexpr int kMaxM = 128;
-constexpr uint32_t kEBlock = 128 * 128;  // bytes of 64 columns of E or F
-constexpr uint32_t kFixed = 2 * kEBlock;
-constexpr uint32_t kSlack = 128 * 128;   // behind the blocks: an operand's 128 rows
 constexpr uint32_t kMisc = 2048;
 constexpr uint32_t kPanelSmem = 232448;
-constexpr uint32_t kPanelRoom = kPanelSmem - 1024 - kFixed - kSlack - kMisc;
 constexpr int kBarStride = 32;           // words between two teams' counters
 constexpr int kPanelSms = 148;           // a plan has no more CTAs a matrix than this
 // Up to so many values in a team's parts every CTA adds all of them.
@@ -47,6 +44,7 @@ struct PanelArgs {
   float* norm;         // [teams][ctas]
   unsigned int* bars;  // [teams], a counter each, zero at the start
   int m, mp, n;        // mp: m up to a multiple of 16
+  int e_block;         // bytes of 64 columns of E or F
   int blocks;          // of 64 columns, of the matrix
   int room;            // blocks that a CTA has room for
   int ctas, teams, batch;
@@ -95,7 +93,6 @@ NVFP4_DEV bool team_barrier(Panel& s, const PanelArgs& a) {
   if (a.ctas > 1 && threadIdx.x == 0) {
     s.target += a.ctas;
     const bool lost = (injected() & kStall) != 0 && s.rank == 0;
-    __threadfence();
     if (!lost) asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(s.bar) : "memory");
     const uint64_t t0 = globaltimer_ns();
     const uint64_t limit = *reinterpret_cast<volatile unsigned long long*>(&g_gemm_wait_ns);
@@ -109,7 +106,6 @@ NVFP4_DEV bool team_barrier(Panel& s, const PanelArgs& a) {
         break;
       }
     }
-    __threadfence();
   }
   __syncthreads();
   return *s.abort_flag == 0;
@@ -265,7 +261,8 @@ NVFP4_DEV float4 add_parts(const float4* at, int ctas, int stride) {
 }
 
 // 8 columns from j0 on of row i of E, in f16 with 2^12; the diagonal goes to d.
-NVFP4_DEV void put_e(const Panel& s, int i, int j0, const float4 u, const float4 v) {
+NVFP4_DEV void put_e(const Panel& s, const PanelArgs& a, int i, int j0, const float4 u,
+                     const float4 v) {
   float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -275,7 +272,7 @@ NVFP4_DEV void put_e(const Panel& s, int i, int j0, const float4 u, const float4
       x[e] = 0.0f;
     }
   }
-  *reinterpret_cast<uint4*>(s.e + (j0 >> 6) * kEBlock + piece_at(i, (j0 & 63) >> 3)) =
+  *reinterpret_cast<uint4*>(s.e + (j0 >> 6) * a.e_block + piece_at(i, (j0 & 63) >> 3)) =
       make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]),
                  pack_f16x2(x[6], x[7]));
 }
@@ -289,7 +286,7 @@ NVFP4_DEV void make_e(const Panel& s, const PanelArgs& a, const float4* parts, i
     if (x < pieces) {
       const float4* at = parts + p * a.m + x;  // 2 p m + i
       const float4 u = add_parts(at, count, quads), v = add_parts(at + a.m, count, quads);
-      put_e(s, x - p * a.m, 8 * p, u, v);
+      put_e(s, a, x - p * a.m, 8 * p, u, v);
     }
     return;
   }
@@ -317,7 +314,7 @@ NVFP4_DEV void make_e(const Panel& s, const PanelArgs& a, const float4* parts, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int x = x0 + k * kPanelThreads, p = x / a.m;
-      if (x < pieces) put_e(s, x - p * a.m, 8 * p, t[k][0], t[k][1]);
+      if (x < pieces) put_e(s, a, x - p * a.m, 8 * p, t[k][0], t[k][1]);
     }
   }
 }
@@ -330,7 +327,8 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
   const uint32_t block_bytes = (uint32_t)a.mp * 128;
   Panel s;
   s.e = smem;
-  s.hi = smem + kFixed;
+  const uint32_t e_bytes = a.e_block * ((a.mp + 63) / 64);
+  s.hi = smem + e_bytes;
   s.lo = s.hi + a.room * block_bytes;
   uint8_t* misc = smem + kPanelSmem - 1024 - kMisc;
   s.d = reinterpret_cast<float*>(misc);
@@ -358,7 +356,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
-  for (uint32_t i = tid * 16; i < kFixed; i += kPanelThreads * 16)
+  for (uint32_t i = tid * 16; i < e_bytes; i += kPanelThreads * 16)
     *reinterpret_cast<uint4*>(s.e + i) = make_uint4(0u, 0u, 0u, 0u);
   if (tid < kMaxM) s.d[tid] = s.dp[tid] = 0.0f;
   tc_fence_before();
@@ -428,7 +426,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
       if (tid == 0) {
         tc_fence_after();
         for (int k = 0; k < a.mp; k += 16) {
-          const uint64_t d = smem_desc_sw128(e + (k >> 6) * kEBlock + (k & 63) * 2);
+          const uint64_t d = smem_desc_sw128(e + (k >> 6) * a.e_block + (k & 63) * 2);
           tc_mma_f16(tmem, d, d, idesc_mm, k ? 1u : 0u);
         }
         tc_commit(s.mbar);
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
           tmem_ld_wait();
           if (row < a.m) {
             const float di = s.d[row];
-            uint8_t* block = s.e + (c0 >> 6) * kEBlock;
+            uint8_t* block = s.e + (c0 >> 6) * a.e_block;
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
               uint4* at = reinterpret_cast<uint4*>(block + piece_at(row, ((c0 & 63) >> 3) + p));
@@ -480,7 +478,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
         const uint32_t idesc = idesc_f16(128, 64 * nb, false, true);
         for (int k = 0; k < a.mp; k += 16)
           tc_mma_f16(tmem + (c & 1) * 256,
-                     smem_desc_sw128(e + (k >> 6) * kEBlock + (k & 63) * 2),
+                     smem_desc_sw128(e + (k >> 6) * a.e_block + (k & 63) * 2),
                      smem_desc_mn(hi + 4 * c * block_bytes + k * 128, block_bytes), idesc,
                      k ? 1u : 0u);
         tc_commit(s.mbar + 8u * (c & 1));
@@ -568,7 +566,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
 
 // How a call is spread over a device's SMs.
 struct PanelPlan {
-  int m, mp, n, blocks, room, least, ctas, teams;
+  int m, mp, n, e_block, blocks, room, least, ctas, teams;
   bool cluster;
 };
 // wide: how many clusters of 16 a device has room for (0: not known).
@@ -578,7 +576,8 @@ PanelPlan panel_plan(int64_t batch, int64_t rows, int64_t cols, int sms, int wid
   l.n = (int)std::max(rows, cols);
   l.mp = (l.m + 15) / 16 * 16;
   l.blocks = (l.n + 63) / 64;
-  l.room = (int)(kPanelRoom / (uint32_t)(l.mp * 256));
+  l.e_block = 128 * (l.m > 64 ? l.mp : 128);  // with copies 128 rows
+  l.room = (int)((kPanelSmem - 1024 - kMisc - l.e_block * ((l.mp + 63) / 64)) / (l.mp * 256));
   l.least = (l.blocks + l.room - 1) / l.room;
   // Teams that fit a cluster are one, for its barrier (a team of 64 CTAs by counters
   // took 72 us for 64 x 4096, a cluster of 8 63, of 16 52); a matrix is spread over as
@@ -649,6 +648,7 @@ nvfp4_status muon_panel(const MuonCall& c) {
   a.m = l.m;
   a.rows = l.m <= 32 ? 32 : l.m <= 64 ? 64 : 128;
   a.mp = l.mp;
+  a.e_block = l.e_block;
   a.n = l.n;
   a.blocks = l.blocks;
   a.room = l.room;
