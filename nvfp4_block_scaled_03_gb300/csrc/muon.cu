@@ -685,41 +685,64 @@ NVFP4_DEV float4 fma4(float m, const float4 v, const float4 g) {
   return make_float4(fmaf(m, v.x, g.x), fmaf(m, v.y, g.y), fmaf(m, v.z, g.z), fmaf(m, v.w, g.w));
 }
 
-// Part `part` of matrix `mat`.  VEC: a matrix has a multiple of 4 elements.
-template <bool WIDE, bool VEC>
+// Matrix `mat` lies at elements [first, last) of the stack; its quads are the aligned
+// fours that hold them, of which the ends may belong to other matrices in part.
+struct Quads {
+  int64_t first, last, q0, count;
+};
+NVFP4_DEV Quads quads_of(const MomentumArgs& a, int mat) {
+  const int64_t first = (int64_t)mat * a.size, last = first + a.size;
+  return {first, last, first / 4, (last + 3) / 4 - first / 4};
+}
+NVFP4_DEV bool whole_quad(const Quads& q, int64_t at) {
+  return 4 * at >= q.first && 4 * at + 4 <= q.last;
+}
+NVFP4_DEV float* parts_of(float4& v) { return reinterpret_cast<float*>(&v); }
+
+// A quad of the gradient and of the momentum; zeros outside the matrix.
+template <bool WIDE>
+NVFP4_DEV void load_quad(const MomentumArgs& a, const Quads& q, int64_t at, bool grad, float4& g,
+                         float4& v) {
+  if (whole_quad(q, at)) {
+    if (grad) g = grad4_at<WIDE>(a.grad, 4 * at);
+    v = *reinterpret_cast<const float4*>(a.momentum + 4 * at);
+    return;
+  }
+  g = v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int64_t i = 4 * at + e;
+    if (i < q.first || i >= q.last) continue;
+    if (grad) parts_of(g)[e] = grad_at<WIDE>(a.grad, i);
+    parts_of(v)[e] = a.momentum[i];
+  }
+}
+
+// Part `part` of matrix `mat`.
+template <bool WIDE>
 NVFP4_DEV void momentum_part(const MomentumArgs& a, int mat, int part, float* red) {
-  const int64_t base = (int64_t)mat * a.size;
-  const int64_t first = (int64_t)part * blockDim.x + threadIdx.x;
+  const Quads q = quads_of(a, mat);
   const int64_t stride = (int64_t)a.parts * blockDim.x;
   float sum = 0.0f;
-  if (VEC) {
-    const int64_t n4 = a.size / 4;
-    for (int64_t i = first; i < n4; i += kEwUnroll * stride) {
-      float4 g[kEwUnroll], v[kEwUnroll];
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < q.count; i += kEwUnroll * stride) {
+    float4 g[kEwUnroll], v[kEwUnroll];
 #pragma unroll
-      for (int u = 0; u < kEwUnroll; ++u) {
-        const int64_t at = base + 4 * (i + u * stride);
-        if (i + u * stride < n4) {
-          g[u] = grad4_at<WIDE>(a.grad, at);
-          v[u] = *reinterpret_cast<const float4*>(a.momentum + at);
-        }
-      }
+    for (int u = 0; u < kEwUnroll; ++u)
+      if (i + u * stride < q.count) load_quad<WIDE>(a, q, q.q0 + i + u * stride, true, g[u], v[u]);
 #pragma unroll
-      for (int u = 0; u < kEwUnroll; ++u) {
-        if (i + u * stride >= n4) continue;
-        v[u] = fma4(a.mu, v[u], g[u]);
-        *reinterpret_cast<float4*>(a.momentum + base + 4 * (i + u * stride)) = v[u];
-        if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
-        sum += (v[u].x * v[u].x + v[u].y * v[u].y) + (v[u].z * v[u].z + v[u].w * v[u].w);
+    for (int u = 0; u < kEwUnroll; ++u) {
+      if (i + u * stride >= q.count) continue;
+      const int64_t at = q.q0 + i + u * stride;
+      v[u] = fma4(a.mu, v[u], g[u]);
+      if (whole_quad(q, at)) {
+        *reinterpret_cast<float4*>(a.momentum + 4 * at) = v[u];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * at + e >= q.first && 4 * at + e < q.last) a.momentum[4 * at + e] = parts_of(v[u])[e];
       }
-    }
-  } else {
-    for (int64_t i = first; i < a.size; i += stride) {
-      const float g = grad_at<WIDE>(a.grad, base + i);
-      float v = fmaf(a.mu, a.momentum[base + i], g);
-      a.momentum[base + i] = v;
-      if (a.nesterov) v = fmaf(a.mu, v, g);
-      sum = fmaf(v, v, sum);
+      if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
+      sum += (v[u].x * v[u].x + v[u].y * v[u].y) + (v[u].z * v[u].z + v[u].w * v[u].w);
     }
   }
   const float s = block_sum(sum, red);
@@ -727,84 +750,90 @@ NVFP4_DEV void momentum_part(const MomentumArgs& a, int mat, int part, float* re
 }
 
 // From the matrix's end to its beginning: the first pass left the end in L2.
-// VEC: rows of a multiple of 8 elements, so hi and lo are laid out as the matrix.
-template <bool WIDE, bool VEC>
+// FLAT: rows of a multiple of 8 elements, so hi and lo are laid out as the matrix.
+template <bool WIDE, bool FLAT>
 NVFP4_DEV void start_part(const MomentumArgs& a, int mat, int part, float* red) {
   float sum = 0.0f;
   for (int p = threadIdx.x; p < a.parts; p += blockDim.x)
     sum += __ldcg(a.partial + (int64_t)mat * a.parts + p);
   const float scale = kScale / fmaxf(sqrtf(block_sum(sum, red)), a.eps);
-  const int64_t base = (int64_t)mat * a.size, to = (int64_t)mat * a.padded;
-  const int64_t first = (int64_t)part * blockDim.x + threadIdx.x;
-  const int64_t stride = (int64_t)a.parts * blockDim.x;
-  if (VEC) {
-    const int64_t n4 = a.size / 4;
-    for (int64_t i = first; i < n4; i += kEwUnroll * stride) {
-      float4 g[kEwUnroll], v[kEwUnroll];
+  const Quads q = quads_of(a, mat);
+  const int64_t to = (int64_t)mat * a.padded, stride = (int64_t)a.parts * blockDim.x;
+  for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < q.count; i += kEwUnroll * stride) {
+    float4 g[kEwUnroll], v[kEwUnroll];
 #pragma unroll
-      for (int u = 0; u < kEwUnroll; ++u) {
-        const int64_t at = base + 4 * (n4 - 1 - i - u * stride);
-        if (i + u * stride < n4) {
-          if (a.nesterov) g[u] = grad4_at<WIDE>(a.grad, at);
-          v[u] = *reinterpret_cast<const float4*>(a.momentum + at);
+    for (int u = 0; u < kEwUnroll; ++u)
+      if (i + u * stride < q.count)
+        load_quad<WIDE>(a, q, q.q0 + q.count - 1 - i - u * stride, a.nesterov, g[u], v[u]);
+#pragma unroll
+    for (int u = 0; u < kEwUnroll; ++u) {
+      if (i + u * stride >= q.count) continue;
+      const int64_t at = q.q0 + q.count - 1 - i - u * stride;
+      if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
+      float* x = parts_of(v[u]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] *= scale;
+      const uint32_t h[2] = {pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3])};
+      const float2 h0 = unpack_f16x2(h[0]), h1 = unpack_f16x2(h[1]);
+      const uint32_t l[2] = {pack_f16x2(x[0] - h0.x, x[1] - h0.y),
+                             pack_f16x2(x[2] - h1.x, x[3] - h1.y)};
+      const bool whole = FLAT || whole_quad(q, at);
+      if (FLAT) {
+        const int64_t e = to + 4 * at - q.first;
+        *reinterpret_cast<uint2*>(a.hi + e) = make_uint2(h[0], h[1]);
+        *reinterpret_cast<uint2*>(a.lo + e) = make_uint2(l[0], l[1]);
+      } else {
+        // elements before the matrix's first (of a quad shared with the one before) are
+        // skipped; the first that counts gives row and column
+        const int skip = (int)max((int64_t)0, q.first - 4 * at);
+        const uint32_t k = (uint32_t)(4 * at + skip - q.first);
+        uint32_t row = k / (uint32_t)a.cols, col = k - row * (uint32_t)a.cols;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (e < skip || 4 * at + e >= q.last) continue;
+          const int64_t place = to + (int64_t)row * a.ld + col;
+          reinterpret_cast<uint16_t*>(a.hi)[place] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+          reinterpret_cast<uint16_t*>(a.lo)[place] = (uint16_t)(l[e >> 1] >> (16 * (e & 1)));
+          if (++col == (uint32_t)a.cols) {
+            col = 0;
+            ++row;
+          }
         }
       }
-#pragma unroll
-      for (int u = 0; u < kEwUnroll; ++u) {
-        const int64_t e = 4 * (n4 - 1 - i - u * stride);
-        if (i + u * stride >= n4) continue;
-        if (a.nesterov) v[u] = fma4(a.mu, v[u], g[u]);
-        v[u].x *= scale;
-        v[u].y *= scale;
-        v[u].z *= scale;
-        v[u].w *= scale;
-        const uint2 h = make_uint2(pack_f16x2(v[u].x, v[u].y), pack_f16x2(v[u].z, v[u].w));
-        const float2 h0 = unpack_f16x2(h.x), h1 = unpack_f16x2(h.y);
-        *reinterpret_cast<uint2*>(a.hi + to + e) = h;
-        *reinterpret_cast<uint2*>(a.lo + to + e) =
-            make_uint2(pack_f16x2(v[u].x - h0.x, v[u].y - h0.y),
-                       pack_f16x2(v[u].z - h1.x, v[u].w - h1.y));
-        if (a.zero) {
+      if (a.zero) {
+        if (whole) {
           if (WIDE)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.grad) + base + e) =
+            *reinterpret_cast<float4*>(static_cast<float*>(a.grad) + 4 * at) =
                 make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           else
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad) + base + e) =
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.grad) + 4 * at) =
                 make_uint2(0u, 0u);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (4 * at + e >= q.first && 4 * at + e < q.last) {
+              if (WIDE)
+                static_cast<float*>(a.grad)[4 * at + e] = 0.0f;
+              else
+                static_cast<uint16_t*>(a.grad)[4 * at + e] = 0;
+            }
         }
-      }
-    }
-  } else {
-    for (int64_t i = first; i < a.size; i += stride) {
-      float v = a.momentum[base + i];
-      if (a.nesterov) v = fmaf(a.mu, v, grad_at<WIDE>(a.grad, base + i));
-      v *= scale;
-      const uint32_t row = (uint32_t)i / (uint32_t)a.cols, col = (uint32_t)i - row * a.cols;
-      const int64_t at = to + (int64_t)row * a.ld + col;
-      const __half h = __float2half_rn(v);
-      a.hi[at] = h;
-      a.lo[at] = __float2half_rn(v - __half2float(h));
-      if (a.zero) {
-        if (WIDE)
-          static_cast<float*>(a.grad)[base + i] = 0.0f;
-        else
-          static_cast<uint16_t*>(a.grad)[base + i] = 0;
       }
     }
   }
 }
 
-template <bool WIDE, bool VEC>
+template <bool WIDE>
 __global__ void __launch_bounds__(kEwThreads) momentum_kernel(const MomentumArgs a) {
   __shared__ float red[kEwThreads / 32];
   griddep_wait();
-  momentum_part<WIDE, VEC>(a, blockIdx.y, blockIdx.x, red);
+  momentum_part<WIDE>(a, blockIdx.y, blockIdx.x, red);
 }
-template <bool WIDE, bool VEC>
+template <bool WIDE, bool FLAT>
 __global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a) {
   __shared__ float red[kEwThreads / 32];
   griddep_wait();
-  start_part<WIDE, VEC>(a, gridDim.y - 1 - blockIdx.y, blockIdx.x, red);
+  start_part<WIDE, FLAT>(a, gridDim.y - 1 - blockIdx.y, blockIdx.x, red);
 }
 
 // ---- one launch for all of it: matrices of some hundred rows and columns -----------
@@ -818,7 +847,7 @@ struct WholeArgs {
   MomentumArgs e;
   NsArgs gram, poly, update;  // without coefficients
   unsigned int* bars;  // two counters, zero at the start
-  int batch, steps, vec1, vec2;
+  int batch, steps, flat;
   float coefs[3 * NVFP4_MUON_MAX_STEPS];
 };
 struct WholeMaps {
@@ -875,16 +904,13 @@ __global__ void __launch_bounds__(WholeLayout<BN>::kThreads, 1)
   const int items = a.batch * a.e.parts;
   for (int w = blockIdx.x; w < items; w += gridDim.x) {
     const int mat = w / a.e.parts, part = w - mat * a.e.parts;
-    if (a.vec1)
-      momentum_part<WIDE, true>(a.e, mat, part, red);
-    else
-      momentum_part<WIDE, false>(a.e, mat, part, red);
+    momentum_part<WIDE>(a.e, mat, part, red);
   }
   bool ok = whole_barrier(c, a, gridDim.x);
   if (ok) {
     for (int w = blockIdx.x; w < items; w += gridDim.x) {
       const int mat = w / a.e.parts, part = w - mat * a.e.parts;
-      if (a.vec2)
+      if (a.flat)
         start_part<WIDE, true>(a.e, mat, part, red);
       else
         start_part<WIDE, false>(a.e, mat, part, red);
@@ -1171,7 +1197,7 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   const bool tall = p->rows > p->cols, whole = takes_whole(l, p->batch, dev.sm_count);
   const int bn = whole ? whole_width(l, p->batch, dev.sm_count) : 256;
   const int b_rows = whole ? bn : 128;  // rows of B that a CTA loads at a time
-  const bool vec1 = e.size % 4 == 0, vec2 = p->cols % 8 == 0;
+  const bool flat = p->cols % 8 == 0;
   WholeMaps t;
   bool ok = true;
   const int64_t mm = l.m;
@@ -1195,7 +1221,7 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
        make_map(&t.e, E, p->batch, mm, mm, l.ldm, 32, 32) &&
        make_map(&t.f, F, p->batch, mm, mm, l.ldm, 32, 32) &&
        make_map(&t.lo, lo, p->batch, p->rows, p->cols, l.ldx, 32, 32);
-  if (vec2)
+  if (flat)
     ok = ok && make_map(&t.out, update, p->batch, p->rows, p->cols, p->cols, 32, 32, true);
   else
     t.out = t.lo;  // not read
@@ -1223,7 +1249,7 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   upd.by_col = tall;
   upd.din = db;
   upd.out = static_cast<__nv_bfloat16*>(update);
-  upd.out_boxes = vec2;
+  upd.out_boxes = flat;
 
   if (whole) {
     WholeArgs a = {};
@@ -1234,8 +1260,7 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
     a.bars = reinterpret_cast<unsigned int*>(w + l.total - kBarBytes);
     a.batch = (int)p->batch;
     a.steps = p->steps;
-    a.vec1 = vec1;
-    a.vec2 = vec2;
+    a.flat = flat;
     std::copy(p->coefs, p->coefs + 3 * p->steps, a.coefs);
     if (bn == 64)
       return wide ? launch_whole<64, true>(t, a, dev.sm_count, s)
@@ -1248,10 +1273,9 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   const int64_t fit = std::max<int64_t>(1, (int64_t)dev.sm_count * 8 / p->batch);
   e.parts = (int)std::min<int64_t>({want, fit, kMaxParts});
   const dim3 grid((unsigned)e.parts, (unsigned)p->batch);
-  auto k1 = wide ? (vec1 ? momentum_kernel<true, true> : momentum_kernel<true, false>)
-                 : (vec1 ? momentum_kernel<false, true> : momentum_kernel<false, false>);
-  auto k2 = wide ? (vec2 ? start_kernel<true, true> : start_kernel<true, false>)
-                 : (vec2 ? start_kernel<false, true> : start_kernel<false, false>);
+  auto k1 = wide ? momentum_kernel<true> : momentum_kernel<false>;
+  auto k2 = wide ? (flat ? start_kernel<true, true> : start_kernel<true, false>)
+                 : (flat ? start_kernel<false, true> : start_kernel<false, false>);
   if (launch_pdl(k1, grid, kEwThreads, 0, s, e) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (launch_pdl(k2, grid, kEwThreads, 0, s, e) != cudaSuccess) return NVFP4_ERR_CUDA;
   for (int i = 0; i < p->steps; ++i) {
