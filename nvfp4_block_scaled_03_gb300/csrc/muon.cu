@@ -64,7 +64,8 @@ constexpr uint32_t kBoxMN = 64 * kBK * 2;
 struct NsArgs {
   int m, n, k;             // its rows, columns and contraction
   int tiles_m, tiles_n;
-  int tiles_per, tiles;    // of a matrix, of all
+  int tiles_per, tiles;    // of a matrix; of all, each as often as it has splits
+  int splits;              // parts of the contraction, each a CTA's
   int a_mn, b_mn;          // operands whose contraction does not lie along their rows
   int symmetric;
   int loads;               // boxes that a chunk brings in
@@ -74,6 +75,8 @@ struct NsArgs {
   const float* din;
   float* dout;
   int64_t dstride;         // from one matrix's diagonal to the next's
+  float4* part;            // splits: [tile][split][chunk][8][32 lanes], 4 columns each
+  unsigned int* tickets;   // [tile][chunk], zero before and after
   __nv_bfloat16* out;      // final
   int out_boxes;           // final: rows are whole multiples of 16 bytes
 };
@@ -174,6 +177,8 @@ NVFP4_DEV void box_transpose(uint32_t from, uint32_t to, int lane) {
 // diagonal stored twice, the second time transposed (ldmatrix and stmatrix).  Rows,
 // columns and contraction behind a matrix's end are filled with zeros by the loads and
 // left out by the stores.
+// Of a contraction in `splits` parts every CTA writes its sums of a tile to memory;
+// whichever warp comes last to a chunk adds all of them, in their order, and finishes it.
 // =============================================================================
 template <bool PAIR, int BN, int STAGES, int SLOTS>
 struct NsLayout {
@@ -340,17 +345,25 @@ template <class L, class B>
 NVFP4_DEV bool ns_produce(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Pipe& p, B begin) {
   const int num_kb = (a.k + kBK - 1) / kBK;
   int tile = c.unit, z = 0, tm = 0, tn = 0;
+  int kb0 = 0, kb1 = num_kb;
   auto find = [&]() {
     if (tile >= a.tiles) return;
-    z = tile / a.tiles_per;
-    tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
+    int t = tile;
+    if (a.splits > 1) {
+      t = tile / a.splits;
+      const int part = tile - t * a.splits;
+      kb0 = num_kb * part / a.splits;
+      kb1 = num_kb * (part + 1) / a.splits;
+    }
+    z = t / a.tiles_per;
+    tile_of<L>(t - z * a.tiles_per, a, tm, tn);
   };
   find();
   if (!begin()) return false;
   for (; tile < a.tiles; tile += c.units, find()) {
     const int a0 = tm * L::kBM + (int)c.rank * 128;
     const int b0 = tn * L::kBN + (int)c.rank * L::kRowsB;
-    for (int kb = 0; kb < num_kb; ++kb) {
+    for (int kb = kb0; kb < kb1; ++kb) {
       if (!all_waited(c.wait(c.empty_bar(p.s), p.ph ^ 1u, 0x71u))) return false;
       ++p.it;
       if (elect_one()) {
@@ -405,7 +418,13 @@ NVFP4_DEV bool ns_multiply(const Ns<L>& c, const NsArgs& a, Pipe& p) {
     const uint32_t b = p.it & 1u;
     if (!all_waited(c.wait(c.acc_empty(b), ((p.it >> 1) & 1u) ^ 1u, 0x72u))) return false;
     tc_fence_after();
-    for (int kb = 0; kb < num_kb; ++kb) {
+    int kb0 = 0, kb1 = num_kb;
+    if (a.splits > 1) {
+      const int part = tile % a.splits;
+      kb0 = num_kb * part / a.splits;
+      kb1 = num_kb * (part + 1) / a.splits;
+    }
+    for (int kb = kb0; kb < kb1; ++kb) {
       if (!all_waited(c.wait(c.full_bar(p.s), p.ph, 0x74u))) return false;
       tc_fence_after();
       if (elect_one()) {
@@ -417,11 +436,11 @@ NVFP4_DEV bool ns_multiply(const Ns<L>& c, const NsArgs& a, Pipe& p) {
         for (int j = 0; j < kBK / 16; ++j) {
           if (16 * j >= left) break;
           tc_mma_f16(L::kPair, c.tmem + b * L::kBN, ad + j * as, bd + j * bs, idesc,
-                     kb | j ? 1u : 0u);
+                     kb != kb0 || j ? 1u : 0u);
         }
-        if (kb == 0) st_shared_u8(c.inject() + 1, 1u);
+        if (kb == kb0) st_shared_u8(c.inject() + 1, 1u);
         c.commit(c.empty_bar(p.s));
-        if (kb == num_kb - 1) c.commit(c.acc_full(b));
+        if (kb == kb1 - 1) c.commit(c.acc_full(b));
       }
       __syncwarp();
       if (++p.s == L::kStages) {
@@ -430,6 +449,50 @@ NVFP4_DEV bool ns_multiply(const Ns<L>& c, const NsArgs& a, Pipe& p) {
       }
     }
   }
+  return true;
+}
+
+// Leaves a warp's 32 x 32 sums of a split tile in memory; the last of the parts to come
+// gets the sum of all.
+NVFP4_DEV bool last_part(const NsArgs& a, int item, int chunk, int chunks, int lane,
+                         uint32_t (&r)[32]) {
+  const int tile = item / a.splits, part = item - tile * a.splits;
+  float4* first = a.part + ((int64_t)tile * a.splits * chunks + chunk) * 256 + lane;
+  const int64_t step = (int64_t)chunks * 256;  // to the next part
+#pragma unroll
+  for (int x = 0; x < 8; ++x)
+    __stcg(first + part * step + 32 * x,
+           make_float4(__uint_as_float(r[4 * x]), __uint_as_float(r[4 * x + 1]),
+                       __uint_as_float(r[4 * x + 2]), __uint_as_float(r[4 * x + 3])));
+  __threadfence();
+  __syncwarp();
+  unsigned int* ticket = a.tickets + tile * chunks + chunk;
+  unsigned int before = 0;
+  if (lane == 0) before = atomicAdd(ticket, 1u);
+  before = __shfl_sync(0xFFFFFFFFu, before, 0);
+  if (before != (unsigned int)a.splits - 1u) return false;
+  __threadfence();
+  float4 t[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) t[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+  for (int k = 0; k < a.splits; ++k)
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const float4 u = __ldcg(first + k * step + 32 * x);
+      t[x].x += u.x;
+      t[x].y += u.y;
+      t[x].z += u.z;
+      t[x].w += u.w;
+    }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    r[4 * x] = __float_as_uint(t[x].x);
+    r[4 * x + 1] = __float_as_uint(t[x].y);
+    r[4 * x + 2] = __float_as_uint(t[x].z);
+    r[4 * x + 3] = __float_as_uint(t[x].w);
+  }
+  if (lane == 0) *ticket = 0;  // for the next step's
   return true;
 }
 
@@ -445,6 +508,7 @@ NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Ch
   const uint32_t slot_bar = c.bar0 + 8u * (L::kSlotBar + ew * L::kSlots);
   // where this warp's chunks of a tile lie, and how many there are
   auto place = [&](int tile, int& x, int& y, int& z) {
+    if (a.splits > 1) tile /= a.splits;
     z = tile / a.tiles_per;
     int tm, tn;
     tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
@@ -509,6 +573,10 @@ NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Ch
       tmem_ld32(c.tmem + ((uint32_t)(q * 32) << 16) + b * L::kBN +
                     (uint32_t)(h * (L::kBN / 2) + ch * 32),
                 r);
+      if (a.splits > 1) {
+        tmem_ld_wait();
+        if (!last_part(a, tile, ew * L::kChunks + ch, 8 * L::kChunks, lane, r)) continue;
+      }
       uint32_t in0[16] = {}, in1[16] = {};
       if (a.loads) {
         if (!all_waited(c.wait(slot_bar + 8u * s, (p.used / L::kSlots) & 1u, 0x75u))) return false;
@@ -653,7 +721,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout::kThreads
 // its two halves.
 constexpr int kEwThreads = 256, kEwUnroll = 4;
 
-constexpr size_t kBarBytes = 1024;
+constexpr size_t kBarBytes = 16384;  // two counters, then the tickets
+constexpr int kTicketWord = 64;
 constexpr int kMaxParts = 1024;
 constexpr int kWholeTiles = 2;
 
@@ -1018,6 +1087,7 @@ void set_tiles(NsArgs& a, int64_t batch, int bm, int bn) {
   a.tiles_per = a.symmetric  // matrix's end there may be some, which have no chunks
                     ? per * (a.tiles_m * (a.tiles_m + 1) / 2)
                     : a.tiles_m * a.tiles_n;
+  a.splits = 1;
   a.tiles = (int)(a.tiles_per * batch);
 }
 
@@ -1043,12 +1113,20 @@ nvfp4_status launch_whole(const WholeMaps& maps, WholeArgs& a, int sms, cudaStre
   set_tiles(a.gram, a.batch, L::kBM, BN);
   set_tiles(a.poly, a.batch, L::kBM, BN);
   set_tiles(a.update, a.batch, L::kBM, BN);
+  // Long contractions of few tiles are shared by the CTAs that have none, 1024 a part at
+  // least (us, whole and in parts, all steps: 256 x 8192 268, 172; 1024 x 1024 in two
+  // 137, 146).
+  const int parts = std::min({16, sms / a.gram.tiles, a.gram.k / 1024});
+  if (parts > 1) {
+    a.gram.splits = parts;
+    a.gram.tiles *= parts;
+  }
   if (cudaMemsetAsync(a.bars, 0, kBarBytes, stream) != cudaSuccess) return NVFP4_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   // no more CTAs than have a tile, or a share of the momentum
   const int64_t share = (a.e.size * a.batch + 8191) / 8192;
   const int ctas = (int)std::min<int64_t>(
-      sms, std::max<int64_t>({share, a.poly.tiles, a.update.tiles}));
+      sms, std::max<int64_t>({share, a.gram.tiles, a.poly.tiles, a.update.tiles}));
   a.e.parts = (int)std::min<int64_t>(kMaxParts, std::max<int64_t>(1, ctas / a.batch));
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(L::kThreads);
@@ -1072,6 +1150,16 @@ struct Layout {
 };
 constexpr int64_t kMaxSide = 1 << 20;
 
+// Whether one launch does it all: as long as the tiles of 128 x 128 of an update are
+// few.
+bool takes_whole(const Layout& l, int64_t batch, int sms) {
+  return ((l.m + 127) / 128) * ((l.n + 127) / 128) * batch <= kWholeTiles * sms;
+}
+// Its tiles' width.
+int whole_width(const Layout& l, int64_t batch, int sms) {
+  return ((l.m + 127) / 128) * ((l.n + 63) / 64) * batch <= sms ? 64 : 128;
+}
+
 nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
   if (batch <= 0 || rows <= 0 || cols <= 0 || batch > 65535 || rows > kMaxSide || cols > kMaxSide)
     return NVFP4_ERR_SHAPE;
@@ -1089,18 +1177,9 @@ nvfp4_status muon_layout(int64_t batch, int64_t rows, int64_t cols, Layout* l) {
   l->panel = muon_panel_fits(rows, cols);
   l->total = l->panel ? muon_panel_workspace(rows, cols)
                       : 3 * l->x_bytes + 2 * l->g_bytes + 2 * l->d_bytes +
-                            up1k((size_t)batch * kMaxParts * 4) + kBarBytes;
+                            up1k((size_t)batch * kMaxParts * 4) + kBarBytes +
+                            (takes_whole(*l, batch, kMaxSms) ? (size_t)kMaxSms * 128 * 128 * 4 : 0);
   return NVFP4_OK;
-}
-
-// Whether one launch does it all: as long as the tiles of 128 x 128 of an update are
-// few.
-bool takes_whole(const Layout& l, int64_t batch, int sms) {
-  return ((l.m + 127) / 128) * ((l.n + 127) / 128) * batch <= kWholeTiles * sms;
-}
-// Its tiles' width.
-int whole_width(const Layout& l, int64_t batch, int sms) {
-  return ((l.m + 127) / 128) * ((l.n + 63) / 64) * batch <= sms ? 64 : 128;
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -1257,7 +1336,10 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
     a.gram = gram;
     a.poly = poly;
     a.update = upd;
-    a.bars = reinterpret_cast<unsigned int*>(w + l.total - kBarBytes);
+    a.bars = reinterpret_cast<unsigned int*>(reinterpret_cast<uint8_t*>(e.partial) +
+                                             up1k((size_t)p->batch * kMaxParts * 4));
+    a.gram.tickets = a.bars + kTicketWord;
+    a.gram.part = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(a.bars) + kBarBytes);
     a.batch = (int)p->batch;
     a.steps = p->steps;
     a.flat = flat;

@@ -102,6 +102,16 @@ def test_variants(nesterov, mu, steps):
     run(*inputs((200, 328), 7), nesterov=nesterov, mu=mu, steps=steps)
 
 
+@pytest.mark.parametrize("shape", [(200, 5000), (5000, 200), (2, 300, 6001), (140, 20000),
+                                   (1, 129, 2048)], ids=lambda s: "x".join(map(str, s)))
+def test_long_contractions(shape):
+    """Few tiles, whose contraction several CTAs share; twice the same."""
+    g, m = inputs(shape, 6)
+    a = run(g, m)
+    for _ in range(3):
+        assert torch.equal(a, nv.nvfp4_muon_update(g, m.clone()))
+
+
 def test_coefficients_of_each_step():
     coefs = ((3.9, -6.0, 2.9), (3.4445, -4.7750, 2.0315), (2.8, -2.9, 1.1))
     run(*inputs((136, 520), 8), steps=3, coefs=coefs)
