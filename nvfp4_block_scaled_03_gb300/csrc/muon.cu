@@ -66,6 +66,7 @@ struct NsArgs {
   int tiles_m, tiles_n;
   int tiles_per, tiles;    // of a matrix; of all, each as often as it has splits
   int splits;              // parts of the contraction, each a CTA's
+  int last;                // >= 0: matrices from this one down to the first
   int a_mn, b_mn;          // operands whose contraction does not lie along their rows
   int symmetric;
   int loads;               // boxes that a chunk brings in
@@ -357,6 +358,7 @@ NVFP4_DEV bool ns_produce(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, P
     }
     z = t / a.tiles_per;
     tile_of<L>(t - z * a.tiles_per, a, tm, tn);
+    if (a.last >= 0) z = a.last - z;
   };
   find();
   if (!begin()) return false;
@@ -512,6 +514,7 @@ NVFP4_DEV bool ns_finish(const Ns<L>& c, const NsArgs& a, const NsMaps& maps, Ch
     z = tile / a.tiles_per;
     int tm, tn;
     tile_of<L>(tile - z * a.tiles_per, a, tm, tn);
+    if (a.last >= 0) z = a.last - z;
     y = tm * L::kBM + (int)c.rank * 128 + q * 32;
     x = tn * L::kBN + h * (L::kBN / 2);
     if (y >= a.m || x >= a.n) return 0;
@@ -1313,6 +1316,7 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
   gram.symmetric = 1;
   gram.din = gram.dout = d;
   gram.dstride = l.dstride;
+  gram.last = -1;
   poly = gram;
   poly.k = (int)l.m;
   poly.a_mn = poly.b_mn = 0;
@@ -1367,6 +1371,10 @@ extern "C" nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad
     set_coefs(gram, 0, abc, last);
     set_coefs(poly, 1, abc, last);
     set_coefs(upd, 2, abc, last);
+    // every launch goes through the matrices the other way than the one before, whose
+    // last results are in L2 (64 x [1024, 2048]: 2547 us, 2570 without)
+    gram.last = upd.last = i & 1 ? (int)p->batch - 1 : -1;
+    poly.last = i & 1 ? -1 : (int)p->batch - 1;
     st = launch_ns(t.gram_a[x], t.gram_b[x], t.e, t.e, t.e, t.e, gram, p->batch,
                           dev.sm_count, s);
     if (st != NVFP4_OK) return st;
