@@ -667,8 +667,8 @@ def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.
     else:
         _cuda(workspace, _U8, "workspace")
     _together(grad, momentum, out, workspace)
-    if not hasattr(coefs, "__hash__") or coefs.__hash__ is None:
-        coefs = tuple(tuple(c) if hasattr(c, "__len__") else c for c in coefs)
+    if coefs is not MUON_COEFS:  # lists and arrays as well
+        coefs = tuple([tuple(c) if hasattr(c, "__len__") else c for c in coefs])
     p = MuonParams(batch, rows, cols, kind, 1 if nesterov else 0, steps, mu, eps,
                    _coefs(coefs, steps))
     st = lib.nvfp4_muon_update(p, grad.data_ptr(), momentum.data_ptr(), out.data_ptr(),

@@ -86,6 +86,7 @@ struct Panel {
 // its own barrier, which does not wait for CTAs that have left.
 NVFP4_DEV bool team_barrier(Panel& s, const PanelArgs& a) {
   if (a.cluster) {
+    __syncwarp();
     cluster_sync();
     return true;
   }

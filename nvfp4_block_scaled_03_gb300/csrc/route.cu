@@ -380,46 +380,61 @@ NVFP4_DEV float slot_weight(const RouteArgs& a, float l, float most, float all) 
 }
 
 // Whether the group of this lane is kept, by sigmoids plus biases in FP64 of the best
-// experts of each.  False: which those are is not clear either.
+// experts of each.  False: which those are is not clear either, for another expert lies
+// close to the last that counts (one with the same logit and bias is as good).
 template <int NI, bool WIDE>
 __device__ __noinline__ bool groups_exact(const RouteArgs& a, int64_t t, const Share mine,
                                           const float (&key)[NI], float near0, bool& keep) {
   const int lane = threadIdx.x & 31;
-  float k1 = -INFINITY, k2 = -INFINITY, k3 = -INFINITY;
-  int e1 = 0, e2 = 0;
+  float k1 = -INFINITY, k2 = -INFINITY;
+  int e1 = -1, e2 = -1;
   auto add = [&](float k, int e) {
     if (k > k1) {
-      k3 = k2;
       k2 = k1, e2 = e1;
       k1 = k, e1 = e;
     } else if (k > k2) {
-      k3 = k2;
       k2 = k, e2 = e;
-    } else {
-      k3 = fmaxf(k3, k);
     }
   };
 #pragma unroll
   for (int i = 0; i < NI; ++i) add(key[i], mine.first + i);
   for (int o = 1; o < a.lanes; o <<= 1) {
     const float o1 = __shfl_xor_sync(0xFFFFFFFFu, k1, o), o2 = __shfl_xor_sync(0xFFFFFFFFu, k2, o);
-    const float o3 = __shfl_xor_sync(0xFFFFFFFFu, k3, o);
     const int f1 = __shfl_xor_sync(0xFFFFFFFFu, e1, o), f2 = __shfl_xor_sync(0xFFFFFFFFu, e2, o);
-    add(o1, f1);
-    add(o2, f2);
-    add(o3, 0);  // never above both
+    // the lower lane's first, so that both take the same of equals
+    const bool low = (lane & o) == 0;
+    const float a1 = low ? k1 : o1, a2 = low ? k2 : o2, b1 = low ? o1 : k1, b2 = low ? o2 : k2;
+    const int c1 = low ? e1 : f1, c2 = low ? e2 : f2, d1 = low ? f1 : e1, d2 = low ? f2 : e2;
+    k1 = a1, e1 = c1;
+    k2 = a2, e2 = c2;
+    add(b1, d1);
+    add(b2, d2);
   }
-  const float in = a.group_top == 2 ? k2 : k1, out = a.group_top == 2 ? k3 : k2;
-  const float margin = 2.0f * (near0 * fmaxf(1.0f, fabsf(in)) + 5e-7f * fabsf(in));
-  if (__any_sync(0xFFFFFFFFu, out > -INFINITY && in - out <= margin)) return false;
+  auto logit = [&](int e) {
+    return open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + e));
+  };
+  const bool two = a.group_top == 2;
+  const float edge = two ? k2 : k1;
+  const int edge_e = two ? e2 : e1;
+  bool unclear = false;
+  if (edge > -INFINITY) {
+    const float margin = 2.0f * (near0 * fmaxf(1.0f, fabsf(edge)) + 5e-7f * fabsf(edge));
+    const float l = logit(edge_e), b = a.bias[edge_e];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int e = mine.first + i;
+      if (e != e1 && (!two || e != e2) && edge - key[i] <= margin)
+        unclear = unclear || logit(e) != l || a.bias[e] != b;
+    }
+  }
+  if (__any_sync(0xFFFFFFFFu, unclear)) return false;
   double worth = -__longlong_as_double(0x7FF0000000000000ll);
   if (k1 > -INFINITY) {
     auto value = [&](int e) {
-      const float l = open_logit<WIDE>(load_logit<WIDE>(a.logits, t * a.ld + e));
-      return 1.0 / (1.0 + exp(-(double)l)) + (double)a.bias[e];
+      return 1.0 / (1.0 + exp(-(double)logit(e))) + (double)a.bias[e];
     };
     worth = value(e1);
-    if (a.group_top == 2 && k2 > -INFINITY) worth += value(e2);
+    if (two && k2 > -INFINITY) worth += value(e2);
   }
   const int g = lane / a.lanes;
   int rank = 0;

@@ -114,7 +114,9 @@ def test_long_contractions(shape):
 
 def test_coefficients_of_each_step():
     coefs = ((3.9, -6.0, 2.9), (3.4445, -4.7750, 2.0315), (2.8, -2.9, 1.1))
-    run(*inputs((136, 520), 8), steps=3, coefs=coefs)
+    a = run(*inputs((136, 520), 8), steps=3, coefs=coefs)
+    g, m = inputs((136, 520), 8)
+    assert torch.equal(a, nv.nvfp4_muon_update(g, m, steps=3, coefs=[list(c) for c in coefs]))
 
 
 @pytest.mark.parametrize("shape,rank", [((256, 512), 1), ((512, 264), 2), ((300, 300), 8),

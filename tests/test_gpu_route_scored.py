@@ -125,6 +125,27 @@ def test_ties_go_to_the_lowest_index(score):
             check(x2, 6, score, bias, groups=4, kept=2)
 
 
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_groups_closer_than_fp32(group_top):
+    """Groups whose worths FP32 cannot tell apart, some of them with their second and
+    third experts alike or as close."""
+    t, e = 400, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(t, 8, 8, generator=g, device="cuda") - 3
+    # every group's two best: nearly the same two logits, in other places
+    place = torch.argsort(torch.rand(t, 8, 8, generator=g, device="cuda"), dim=2)
+    ulp = (torch.rand(t, 8, 2, generator=g, device="cuda") * 4).floor() * 2.0 ** -22
+    x.scatter_(2, place[:, :, :2], torch.tensor([2.5, 1.5], device="cuda") + ulp)
+    third = x[100:].gather(2, place[100:, :, 1:2]) - (torch.arange(300, device="cuda") % 3).view(
+        -1, 1, 1) * 2.0 ** -23
+    x[100:].scatter_(2, place[100:, :, 2:3], third)  # as good as the second, or just below
+    x = x.view(t, e)
+    for bias in (torch.zeros(e, device="cuda"), torch.full((e,), -0.125, device="cuda")):
+        check(x, 4, 1, bias, 8, 3, group_top)
+        check(torch.zeros_like(x), 4, 1, bias, 8, 3, group_top)
+    check(x, 4, 1, torch.randn(e, generator=g, device="cuda") * 1e-7, 8, 3, group_top)
+
+
 @pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
 def test_masks(score):
     x, bias = make(100, 64, 5, masked=0.0)
