@@ -536,9 +536,10 @@ nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t fl
  * diagonals carried beside them, and FP32 accumulators; the update is within
  * about 1.5e-3 of that of 64 bits (2-norm of the difference) plus its one
  * rounding to bf16.  A matrix of zeros gives zeros.  NaN or infinities in a
- * matrix make its update (and momentum) unspecified, not the others'.  The
- * entries of X, A and B must stay below 16 in magnitude, which they do for every
- * input with coefficients that keep X's singular values below 2 and
+ * matrix make its update (and momentum) unspecified, not the others'; a norm's
+ * squares are summed in FP32, so norms below 1e-18 or above 1e18 count as 0 or
+ * infinity.  The entries of X, A and B must stay below 16 in magnitude, which they
+ * do for every input with coefficients that keep X's singular values below 2 and
  * |b s + c s^2| below 16 on their squares s, as the usual (3.4445, -4.7750,
  * 2.0315) do. */
 enum { NVFP4_MUON_MAX_STEPS = 32 };
@@ -552,8 +553,9 @@ typedef struct nvfp4_muon_params {
   const float* coefs; /* host, [steps][3]; read before the call returns    */
 } nvfp4_muon_params;
 
-/* *workspace_bytes (may be NULL) = what nvfp4_muon_update needs: about 6 bytes
- * an element and 4 min(rows, cols)^2 a matrix.  NVFP4_ERR_SHAPE unless
+/* *workspace_bytes (may be NULL) = what nvfp4_muon_update needs: up to 21 MB where
+ * min(rows, cols) <= 128, else about 6 bytes an element and 4 min(rows, cols)^2 a
+ * matrix, and 11 MB.  NVFP4_ERR_SHAPE unless
  * 1 <= batch <= 65535, rows, cols >= 1, rows cols < 2^31 and
  * min(rows, cols) <= 32768. */
 nvfp4_status nvfp4_muon_sizes(int64_t batch, int64_t rows, int64_t cols,
@@ -564,8 +566,10 @@ nvfp4_status nvfp4_muon_sizes(int64_t batch, int64_t rows, int64_t cols,
  * contiguous, 16-byte aligned, not overlapping.  Any rows and cols; rows of a
  * multiple of 8 elements take the fast loads and stores.  The result is the same
  * on every call.  workspace: device, 16-byte aligned, at least
- * nvfp4_muon_sizes gives; contents on return unspecified.  2 + 3 steps launches
- * on `stream`, nothing allocated.  Returns NVFP4_ERR_INVALID_ARG (NULL pointers,
+ * nvfp4_muon_sizes gives; contents on return unspecified.  On `stream`, with nothing
+ * allocated: one launch for matrices with a side of at most 128 and for a few of some
+ * hundred rows and columns (with it, where CTAs meet by counters, a small memset; such
+ * a launch is cooperative), else 2 + 3 steps.  Returns NVFP4_ERR_INVALID_ARG (NULL pointers,
  * overlaps, unknown flags or types, steps, mu, eps or coefs out of range),
  * _SHAPE, _ALIGN, _WORKSPACE, _ARCH, _CUDA. */
 nvfp4_status nvfp4_muon_update(const nvfp4_muon_params* p, void* grad, float* momentum,

@@ -76,8 +76,10 @@ __global__ void __launch_bounds__(kThreads) sgd_amax_finalize_kernel(const float
   if (threadIdx.x == 0) *amax = m;
 }
 
-// W = keep W - step update (bf16), 8 elements a thread, two chunks in flight (four
-// gain nothing); the elements behind the last chunk are the last CTA's.
+// W = keep W - step update (bf16), four chunks of 4 elements a thread in flight, 512
+// contiguous bytes of W a warp (14336 x 4096: 98 us, floor 86; chunks of 8 elements, with
+// whole 16-byte loads of the update, 106); the elements behind the last chunk are the
+// last CTA's.
 NVFP4_DEV float apply1(float w, float u, float keep, float step) {
   return fmaf(-step, u, __fmul_rn(keep, w));
 }
@@ -85,41 +87,34 @@ NVFP4_DEV float apply1(float w, float u, float keep, float step) {
 template <bool AMAX>
 NVFP4_DEV float apply_share(float* __restrict__ W, const uint16_t* __restrict__ U, int64_t n,
                             float keep, float step) {
-  constexpr int kChunks = 2;
-  const int64_t n8 = n / 8, stride = (int64_t)gridDim.x * blockDim.x;
+  constexpr int kChunks = 4;
+  const int64_t n4 = n / 4, stride = (int64_t)gridDim.x * blockDim.x;
   float m = 0.0f;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n8; i += kChunks * stride) {
-    float4 w[kChunks][2];
-    uint4 u[kChunks];
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += kChunks * stride) {
+    float4 w[kChunks];
+    uint2 u[kChunks];
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int64_t q = i + c * stride;
-      if (q < n8) {
-        w[c][0] = reinterpret_cast<const float4*>(W)[2 * q];
-        w[c][1] = reinterpret_cast<const float4*>(W)[2 * q + 1];
-        u[c] = reinterpret_cast<const uint4*>(U)[q];
+      if (q < n4) {
+        w[c] = reinterpret_cast<const float4*>(W)[q];
+        u[c] = reinterpret_cast<const uint2*>(U)[q];
       }
     }
 #pragma unroll
     for (int c = 0; c < kChunks; ++c) {
       const int64_t q = i + c * stride;
-      if (q >= n8) continue;
-      const uint32_t b[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t lo = b[2 * k], hi = b[2 * k + 1];
-        const float4 v = w[c][k];
-        const float4 r = make_float4(apply1(v.x, __uint_as_float(lo << 16), keep, step),
-                                     apply1(v.y, __uint_as_float(lo & 0xFFFF0000u), keep, step),
-                                     apply1(v.z, __uint_as_float(hi << 16), keep, step),
-                                     apply1(v.w, __uint_as_float(hi & 0xFFFF0000u), keep, step));
-        reinterpret_cast<float4*>(W)[2 * q + k] = r;
-        if (AMAX)
-          m = fmaxf(m, fmaxf(fmaxf(fabsf(r.x), fabsf(r.y)), fmaxf(fabsf(r.z), fabsf(r.w))));
-      }
+      if (q >= n4) continue;
+      const float4 v = w[c];
+      const float4 r = make_float4(apply1(v.x, __uint_as_float(u[c].x << 16), keep, step),
+                                   apply1(v.y, __uint_as_float(u[c].x & 0xFFFF0000u), keep, step),
+                                   apply1(v.z, __uint_as_float(u[c].y << 16), keep, step),
+                                   apply1(v.w, __uint_as_float(u[c].y & 0xFFFF0000u), keep, step));
+      reinterpret_cast<float4*>(W)[q] = r;
+      if (AMAX) m = fmaxf(m, fmaxf(fmaxf(fabsf(r.x), fabsf(r.y)), fmaxf(fabsf(r.z), fabsf(r.w))));
     }
   }
-  const int64_t t = n8 * 8 + threadIdx.x;
+  const int64_t t = n4 * 4 + threadIdx.x;
   if (blockIdx.x == gridDim.x - 1 && t < n) {
     const float r = apply1(W[t], __uint_as_float((uint32_t)U[t] << 16), keep, step);
     W[t] = r;
@@ -143,8 +138,8 @@ __global__ void __launch_bounds__(kThreads) muon_apply_kernel(float* __restrict_
 
 // A small weight's step on one cluster, whose first CTA gathers the others' maxima: one
 // launch instead of two.
-constexpr int kClusterCtas = 8, kClusterThreads = 1024;
-__global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterThreads)
+constexpr int kClusterCtas = 16, kClusterThreads = 1024;
+__global__ void __launch_bounds__(kClusterThreads)
     muon_apply_small_kernel(float* __restrict__ W, const uint16_t* __restrict__ U, int64_t n,
                             float keep, float step, float* amax) {
   __shared__ float red[kClusterThreads / 32];
@@ -152,15 +147,49 @@ __global__ void __cluster_dims__(kClusterCtas, 1, 1) __launch_bounds__(kClusterT
   const float m = block_max(apply_share<true>(W, U, n, keep, step), red);
   if (threadIdx.x == 0)
     st_cluster_u32(mapa_shared(smem_u32(&maxima[cluster_ctarank()]), 0), __float_as_uint(m));
+  __syncwarp();
   cluster_sync();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     float most = maxima[0];
-    for (int c = 1; c < kClusterCtas; ++c) most = fmaxf(most, maxima[c]);
+    for (int c = 1; c < (int)gridDim.x; ++c) most = fmaxf(most, maxima[c]);
     *amax = most;
   }
 }
-// Up to here (us, one cluster and two launches, 262144 elements: 4.4, 6.2).
 constexpr int64_t kClusterElements = 1 << 18;
+
+// Launches it; false: the device has no room for such a cluster.
+bool launch_small(float* W, const uint16_t* U, int64_t n, float keep, float step, float* amax,
+                  cudaStream_t s, cudaError_t* err) {
+  static std::atomic<int> fits[64];  // 1: yes, -1: no
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kClusterCtas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kClusterCtas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int known = fits[dev].load(std::memory_order_relaxed);
+  if (known == 0) {
+    int count = 0;
+    known = cudaFuncSetAttribute(muon_apply_small_kernel,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&count, muon_apply_small_kernel, &cfg) ==
+                        cudaSuccess &&
+                    count > 0
+                ? 1
+                : -1;
+    if (known < 0) cudaGetLastError();
+    fits[dev].store(known, std::memory_order_relaxed);
+  }
+  if (known < 0) return false;
+  *err = cudaLaunchKernelEx(&cfg, muon_apply_small_kernel, W, U, n, keep, step, amax);
+  return true;
+}
 
 // CTAs of a persistent launch: as many as are resident at once (looked up
 // once per kernel and device), at most one partial slot each, at most one
@@ -247,16 +276,15 @@ extern "C" nvfp4_status nvfp4_muon_apply(float* W, const void* update, int64_t n
   const float keep = (float)(1.0 - (double)lr * decay), step = (float)((double)lr * scale);
   const uint16_t* u = static_cast<const uint16_t*>(update);
   if (!amax) {
-    const int grid = sgd_grid<muon_apply_kernel<false>>(n / 8, dev.sm_count);
+    const int grid = sgd_grid<muon_apply_kernel<false>>(n / 4, dev.sm_count);
     muon_apply_kernel<false><<<grid, kThreads, 0, s>>>(W, u, n, keep, step, nullptr);
     return cuda_status(cudaGetLastError());
   }
-  if (n <= kClusterElements) {
-    muon_apply_small_kernel<<<kClusterCtas, kClusterThreads, 0, s>>>(W, u, n, keep, step, amax);
-    return cuda_status(cudaGetLastError());
-  }
+  cudaError_t err;
+  if (n <= kClusterElements && launch_small(W, u, n, keep, step, amax, s, &err))
+    return cuda_status(err);
   float* partials = static_cast<float*>(workspace);
-  const int grid = sgd_grid<muon_apply_kernel<true>>(n / 8, dev.sm_count);
+  const int grid = sgd_grid<muon_apply_kernel<true>>(n / 4, dev.sm_count);
   muon_apply_kernel<true><<<grid, kThreads, 0, s>>>(W, u, n, keep, step, partials);
   if (cudaGetLastError() != cudaSuccess) return NVFP4_ERR_CUDA;
   sgd_amax_finalize_kernel<<<1, kThreads, 0, s>>>(partials, grid, amax);

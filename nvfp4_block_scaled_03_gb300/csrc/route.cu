@@ -45,7 +45,6 @@ constexpr int kWarps = 16;            // that rank a CTA's choices
 constexpr int kThreads = kWarps * 32;
 constexpr int kChooseWarps = 32;      // that make them
 constexpr int kChooseThreads = kChooseWarps * 32;
-constexpr int kScoredThreads = 640;   // that make them by scores: their registers
 constexpr int kMaxExperts = 512;
 constexpr int kMaxTop = 16;
 constexpr int kGroupAlign = 128;
@@ -516,14 +515,14 @@ __device__ __noinline__ int choose_rounds(const RouteArgs& a, int64_t t, const S
   return expert;
 }
 
-// Experts and weights of token t by their scores, one warp.  v: this lane's logits;
-// bias: of this lane's experts; list: the warp's, in shared memory.
+// Experts and weights of token t by their scores, one warp.  bias: of this lane's
+// experts, and list, the warp's, in shared memory.
 template <int NI, bool WIDE>
-NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
-                             const float (&v)[NI], const float (&bias)[NI], uint2* list,
-                             int* hist) {
+NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine, const float* bias,
+                             uint2* list, int* hist) {
   const int lane = threadIdx.x & 31;
-  float l_most = -INFINITY;
+  float v[NI], l_most = -INFINITY;
+  load_share<NI, WIDE>(a, t, mine, v);
 #pragma unroll
   for (int i = 0; i < NI; ++i) l_most = fmaxf(l_most, v[i]);
   const bool softmax = a.score == NVFP4_SCORE_SOFTMAX;
@@ -688,44 +687,36 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine,
 // Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
 template <int NI, bool WIDE, bool SCORED>
 NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
-  constexpr int kThr = SCORED ? kScoredThreads : kChooseThreads;
-  for (int e = threadIdx.x; e < a.experts; e += kThr) hist[e] = 0;
-  for (int64_t r = (int64_t)blockIdx.x * kThr + threadIdx.x; r < a.rows;
-       r += (int64_t)gridDim.x * kThr)
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) hist[e] = 0;
+  for (int64_t r = (int64_t)blockIdx.x * kChooseThreads + threadIdx.x; r < a.rows;
+       r += (int64_t)gridDim.x * kChooseThreads)
     a.source[r] = -1;
   __shared__ int taken;
   if (threadIdx.x == 0) taken = 0;
   __syncthreads();
   if constexpr (SCORED) {
+    // The warps take the CTA's tokens one after the other, for some cost more.  32 warps
+    // leave 64 registers, so the lanes' biases lie in shared memory (40000 tokens, 384
+    // experts, all launches of a training step: 83 us; 104 with 20 warps and the biases and
+    // the next token's logits in registers).
     const Share mine = lane_share(a, threadIdx.x & 31);
-    float bias[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-      bias[i] = a.bias && i < mine.count ? a.bias[mine.first + i] : 0.0f;
-    // The warps take the CTA's tokens one after the other, for some cost more; a token's
-    // logits come in while the one before is chosen for.
-    __shared__ uint2 lists[kScoredThreads];
+    __shared__ __align__(16) float biases[NI * 32];
+    if (a.bias && threadIdx.x < 32)
+      for (int i = 0; i < mine.count; ++i) biases[threadIdx.x * NI + i] = a.bias[mine.first + i];
+    __shared__ uint2 lists[kChooseThreads];
     const int c0 = blockIdx.x * a.per_cta, n = min(a.per_cta, a.tokens - c0);
     auto take = [&]() {
       int k = 0;
       if ((threadIdx.x & 31) == 0) k = atomicAdd(&taken, 1);
       return __shfl_sync(0xFFFFFFFFu, k, 0);
     };
-    float next[NI];
-    int k = take();
-    if (k < n) load_share<NI, WIDE>(a, c0 + k, mine, next);
-    while (k < n) {
-      float v[NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i) v[i] = next[i];
-      const int t = c0 + k;
-      k = take();
-      if (k < n) load_share<NI, WIDE>(a, c0 + k, mine, next);
-      choose_scored<NI, WIDE>(a, t, mine, v, bias, lists + (threadIdx.x & ~31u), hist);
-    }
+    __syncthreads();
+    for (int k = take(); k < n; k = take())
+      choose_scored<NI, WIDE>(a, c0 + k, mine, biases + (threadIdx.x & 31) * NI,
+                              lists + (threadIdx.x & ~31u), hist);
   } else {
     int t, t1;
-    warp_tokens(a, kThr / 32, t, t1);
+    warp_tokens(a, kChooseWarps, t, t1);
     if (NI <= 8)  // more would not leave registers for two tokens
       for (; t + 1 < t1; t += 2) choose_tokens<NI, WIDE, 2>(a, t, hist);
     for (; t < t1; ++t) choose_tokens<NI, WIDE, 1>(a, t, hist);
@@ -808,11 +799,11 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
 }
 
 template <int NI, bool WIDE, bool SCORED>
-__global__ void __launch_bounds__(SCORED ? kScoredThreads : kChooseThreads) route_choose_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
   griddep_wait();
   choose<NI, WIDE, SCORED>(a, hist);
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x)
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads)
     a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
@@ -872,11 +863,11 @@ __global__ void __launch_bounds__(kThreads) route_assign_kernel(const RouteArgs 
 }
 
 template <int NI, bool WIDE, bool SCORED>
-__global__ void __launch_bounds__(SCORED ? kScoredThreads : kChooseThreads) route_small_kernel(const RouteArgs a) {
+__global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
   choose<NI, WIDE, SCORED>(a, s.total);
-  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) s.before[e] = 0;
+  for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) s.before[e] = 0;
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);
 }
@@ -1168,10 +1159,10 @@ nvfp4_status check_route(int64_t tokens, int64_t experts, int32_t top) {
 
 template <int NI, bool WIDE, bool SCORED>
 cudaError_t launch_route(RouteArgs& a, int ctas, cudaStream_t stream) {
-  constexpr int kThr = SCORED ? kScoredThreads : kChooseThreads;
-  if (ctas == 1) return launch_pdl(route_small_kernel<NI, WIDE, SCORED>, 1, kThr, 0, stream, a);
+  if (ctas == 1)
+    return launch_pdl(route_small_kernel<NI, WIDE, SCORED>, 1, kChooseThreads, 0, stream, a);
   const cudaError_t e =
-      launch_pdl(route_choose_kernel<NI, WIDE, SCORED>, ctas, kThr, 0, stream, a);
+      launch_pdl(route_choose_kernel<NI, WIDE, SCORED>, ctas, kChooseThreads, 0, stream, a);
   if (e != cudaSuccess) return e;
   const cudaError_t f = launch_pdl(route_scan_kernel, (a.experts + 31) / 32, 1024, 0, stream, a);
   if (f != cudaSuccess) return f;
