@@ -526,6 +526,13 @@ def mlp_operand(M, D, F, saved, workspace, which) -> QTensor:
 ZERO_GRAD = 16
 
 
+def _changed(t):
+    """Tells torch that a call wrote to a tensor in place, as its own operations do
+    (a weight's known amax goes by it, and autograd's check of what it saved)."""
+    if not t.is_inference():
+        torch.autograd.graph.increment_version(t)
+
+
 def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool = False,
                    amax: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                    stream=None):
@@ -545,6 +552,7 @@ def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool 
                               ZERO_GRAD if zero_grad else 0, _ptr(amax), _ptr(workspace),
                               workspace.numel() if workspace is not None else 0,
                               _stream(stream)), "nvfp4_sgd_step")
+    _changed(W)
     return W
 
 
@@ -594,17 +602,20 @@ def _on_device(call):
     """As _on_stream, for a call whose first tensor may lie on another device
     than the current one: the call then runs there, on that device's current
     stream."""
+    name = call.__code__.co_varnames[0]
+
     @functools.wraps(call)
-    def run(first, *args, stream=None, **kwargs):
+    def run(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs.get(name)
         if not (isinstance(first, torch.Tensor) and first.is_cuda):
-            raise ValueError(f"{call.__name__}: the first argument must be a CUDA tensor")
+            raise ValueError(f"{call.__name__}: {name} must be a CUDA tensor")
         if first.get_device() != torch._C._cuda_getDevice():
             with torch.cuda.device(first.device):
-                return run(first, *args, stream=stream, **kwargs)
+                return run(*args, stream=stream, **kwargs)
         if stream is None:
-            return call(first, *args, **kwargs)
+            return call(*args, **kwargs)
         with torch.cuda.stream(stream):
-            return call(first, *args, **kwargs)
+            return call(*args, **kwargs)
     return run
 
 
@@ -705,6 +716,7 @@ def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: fl
                               _current(W))
     if st:
         raise NVFP4Error(st, "nvfp4_muon_apply")
+    _changed(W)
     return amax
 
 

@@ -195,12 +195,14 @@ class MoEBlock:
                 nv.nvfp4_sgd_step(w, self.grads[name], vector_lr, zero_grad=True)
                 continue
             if name not in self.momentum:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the first step makes the momenta: it cannot be captured")
                 self.momentum[name] = torch.zeros_like(w)
             update = nv.nvfp4_muon_update(self.grads[name].view(shape),
                                           self.momentum[name].view(shape), mu, zero_grad=True)
             nv.nvfp4_muon_apply(w.view(shape), update, lr, 0.2 * math.sqrt(max(shape[-2:])), decay,
                                 self.amax.get(name))
-            if name in self.amax:
+            if name in self.amax and not w.is_inference():
                 self.stepped[name] = w, w._version
 
     def balance(self, rate: float):

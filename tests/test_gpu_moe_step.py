@@ -114,6 +114,12 @@ def test_given_amax_and_its_end():
         b.params["up_proj"].mul_(0.5)
     assert block._known_amax("up_proj") is None and block._known_amax("down_proj") is not None
     assert torch.equal(block.forward(x), plain.forward(x))
+    # a step past the block, and another tensor in the weight's place
+    for b in (block, plain):
+        nv.nvfp4_sgd_step(b.params["down_proj"], torch.ones_like(b.params["down_proj"]), 0.5)
+        b.params["gate_proj"] = b.params["gate_proj"] * 2
+    assert block._known_amax("down_proj") is None and block._known_amax("gate_proj") is None
+    assert torch.equal(block.forward(x), plain.forward(x))
 
 
 def test_balance():
@@ -154,6 +160,21 @@ def test_captured_step():
         for name in block.params:
             assert torch.equal(block.params[name], eager.params[name]), name
         assert torch.equal(block.bias, eager.bias)
+    nv.check_device_errors()
+
+
+def test_the_first_step_is_not_captured():
+    """A graph would make the momenta anew in every replay."""
+    block = make()
+    x, dy = data(7)
+    block.forward(x)
+    block.backward(dy)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="momenta"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            block.muon(0.02, 0.01)
+    torch.cuda.synchronize()
+    block.muon(0.02, 0.01)
     nv.check_device_errors()
 
 

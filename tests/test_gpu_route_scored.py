@@ -310,8 +310,12 @@ def test_given_plan_and_refusals():
     for error, kw in bad:
         with pytest.raises(error):
             nv.nvfp4_route_scored_fwd(x, 4, **kw)
+    by_name = nv.nvfp4_route_scored_fwd(logits=x, top=4, bias=bias)
+    assert torch.equal(by_name.expert, plan.expert)
     with pytest.raises(TypeError):
         nv.nvfp4_route_scored_fwd(x.half(), 4)
+    with pytest.raises(ValueError):
+        nv.nvfp4_route_scored_fwd(x.cpu(), 4)
     with pytest.raises(ValueError):
         nv.nvfp4_route_scored_bwd(x, plan, torch.zeros(50, 3, device="cuda"))
     with pytest.raises(nv.NVFP4Error):
