@@ -630,8 +630,8 @@ nvfp4_status nvfp4_route_sizes(int64_t tokens, int64_t experts, int32_t top, int
  *   row [tokens, top] int32     the row of each slot among the groups, -1 for -1
  *   source [rows] int32         the slot (token top + j) of each row, -1: padding
  * A group's rows are in the order of the slots.  The result is the same on
- * every call.  workspace: device, 4-byte aligned, >= nvfp4_route_sizes gives.
- * One launch up to 64 tokens, else three.  Returns NVFP4_ERR_INVALID_ARG,
+ * every call.  workspace: device, 4-byte aligned, >= nvfp4_route_sizes gives, not
+ * touched up to 64 tokens.  One launch up to 64 tokens, else three.  Returns NVFP4_ERR_INVALID_ARG,
  * _SHAPE, _ALIGN, _WORKSPACE, _ARCH, _CUDA. */
 nvfp4_status nvfp4_route_fwd(const void* logits, int32_t in_dtype, int64_t tokens,
                              int64_t experts, int64_t ld, int32_t top, int32_t mode,

@@ -857,6 +857,19 @@ def nvfp4_route_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch.Tensor
     return dlogits
 
 
+_small_workspace: dict = {}
+
+
+def _untouched(t):
+    """The workspace of a device's routing calls of up to 64 tokens, whose kernel does
+    not touch it: one for all of them, on any stream and in any graph."""
+    device = t.get_device()
+    if device not in _small_workspace:
+        _small_workspace[device] = torch.empty(route_sizes(1, 512, 1)[1], dtype=_U8,
+                                               device=t.device)
+    return _small_workspace[device]
+
+
 @functools.lru_cache(maxsize=256)
 def _route_params(*fields):
     return RouteParams(*fields)
@@ -873,11 +886,15 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
     groups of experts, and order the rows by expert (see nvfp4_route_scored_fwd in
     nvfp4.h).  groups_kept None: all of them."""
     kind, tokens, experts, ld = _logits(logits)
+    if workspace is None and tokens <= 64:
+        workspace = _untouched(logits)
+    if plan is not None:
+        _together(logits, plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row,
+                  plan.source)
     plan, workspace = _plan_buffers(tokens, experts, top, plan, workspace, logits)
     if bias is not None:
         _cuda(bias, _F32, "bias", (experts,))
-    _together(logits, bias, plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row,
-              plan.source, workspace)
+    _together(logits, bias, workspace)
     p = _route_params(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, groups,
                       groups if groups_kept is None else groups_kept, group_top, scale)
     st = lib.nvfp4_route_scored_fwd(p, logits.data_ptr(), _ptr(bias), plan.expert.data_ptr(),

@@ -684,9 +684,10 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine, co
   }
 }
 
-// Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.
+// Step 1 for the tokens of this CTA; this CTA's part of `source` is cleared.  lists:
+// scratch of the scored choice in shared memory, an entry a thread.
 template <int NI, bool WIDE, bool SCORED>
-NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
+NVFP4_DEV void choose(const RouteArgs& a, int* hist, uint2* lists) {
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) hist[e] = 0;
   for (int64_t r = (int64_t)blockIdx.x * kChooseThreads + threadIdx.x; r < a.rows;
        r += (int64_t)gridDim.x * kChooseThreads)
@@ -703,7 +704,6 @@ NVFP4_DEV void choose(const RouteArgs& a, int* hist) {
     __shared__ __align__(16) float biases[NI * 32];
     if (a.bias && threadIdx.x < 32)
       for (int i = 0; i < mine.count; ++i) biases[threadIdx.x * NI + i] = a.bias[mine.first + i];
-    __shared__ uint2 lists[kChooseThreads];
     const int c0 = blockIdx.x * a.per_cta, n = min(a.per_cta, a.tokens - c0);
     auto take = [&]() {
       int k = 0;
@@ -801,16 +801,18 @@ NVFP4_DEV void assign(const RouteArgs& a, const int* before, const int* total, i
 template <int NI, bool WIDE, bool SCORED>
 __global__ void __launch_bounds__(kChooseThreads) route_choose_kernel(const RouteArgs a) {
   __shared__ int hist[kMaxExperts];
+  __shared__ uint2 lists[SCORED ? kChooseThreads : 1];
   griddep_wait();
-  choose<NI, WIDE, SCORED>(a, hist);
+  choose<NI, WIDE, SCORED>(a, hist, lists);
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads)
     a.counts[(int64_t)blockIdx.x * a.experts + e] = hist[e];
 }
 
-struct AssignSmem {
+struct alignas(16) AssignSmem {
   int before[kMaxExperts], total[kMaxExperts], offset[kMaxExperts];
   int base[kWarps * kMaxExperts];
 };
+static_assert(sizeof(int) * kWarps * kMaxExperts >= sizeof(uint2) * kChooseThreads, "lists");
 
 // counts [CTAs][experts] becomes its running sums over the CTAs, without the
 // CTA's own, and the totals behind them.  A CTA takes 32 experts (lanes), its
@@ -866,7 +868,7 @@ template <int NI, bool WIDE, bool SCORED>
 __global__ void __launch_bounds__(kChooseThreads) route_small_kernel(const RouteArgs a) {
   __shared__ AssignSmem s;
   griddep_wait();
-  choose<NI, WIDE, SCORED>(a, s.total);
+  choose<NI, WIDE, SCORED>(a, s.total, reinterpret_cast<uint2*>(s.base));  // not in use yet
   for (int e = threadIdx.x; e < a.experts; e += kChooseThreads) s.before[e] = 0;
   __syncthreads();
   assign(a, s.before, s.total, s.offset, s.base);

@@ -158,6 +158,19 @@ def test_nan_stays_in_its_matrix():
     assert torch.equal(got[0], clean[0]) and torch.equal(got[2], clean[2])
 
 
+@pytest.mark.parametrize("shape", [(400, 40, 72), (200, 130, 33), (90, 300, 264)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_nan_does_not_reach_what_follows_on_the_same_unit(shape):
+    """More matrices than there are units: those behind one with NaN take its place."""
+    g, m = inputs(shape, 33)
+    clean = nv.nvfp4_muon_update(g, m.clone())
+    g[0, 3, 5] = float("nan")
+    g[1, 0, 0] = float("inf")
+    got = nv.nvfp4_muon_update(g, m.clone())
+    nv.check_device_errors()
+    assert torch.equal(got[2:], clean[2:])
+
+
 def test_zero_grad_and_repeats():
     g, m = inputs((2, 300, 520), 14)
     a = nv.nvfp4_muon_update(g.clone(), m.clone())

@@ -78,7 +78,7 @@ CASES = [  # tokens, experts, top, groups, kept, group_top
     (1, 256, 8, 8, 4, 2), (1, 1, 1, 1, 1, 1), (3, 8, 2, 1, 1, 2), (64, 60, 4, 1, 1, 1),
     (65, 160, 6, 8, 3, 1), (500, 96, 16, 16, 4, 2), (777, 384, 8, 1, 1, 2), (300, 512, 8, 32, 5, 2),
     (129, 40, 3, 4, 1, 2), (200, 64, 5, 32, 31, 2), (1000, 33, 7, 1, 1, 2), (90, 24, 2, 8, 2, 2),
-    (2000, 128, 8, 2, 1, 1), (31, 510, 10, 2, 2, 2)]
+    (2000, 128, 8, 2, 1, 1), (31, 510, 10, 2, 2, 2), (64, 512, 16, 1, 1, 2)]
 
 
 @pytest.mark.parametrize("tokens,experts,top,groups,kept,group_top", CASES)
@@ -320,6 +320,17 @@ def test_given_plan_and_refusals():
         nv.nvfp4_route_scored_bwd(x, plan, torch.zeros(50, 3, device="cuda"))
     with pytest.raises(nv.NVFP4Error):
         nv.nvfp4_route_balance(plan.sizes, bias, INF)
+
+
+def test_a_small_call_leaves_its_workspace_alone():
+    """Up to 64 tokens: the binding lets all such calls share one."""
+    for tokens, experts in ((1, 512), (64, 512), (64, 7)):
+        x, bias = make(tokens, experts, 16)
+        ws = torch.full((nv.route_sizes(tokens, experts, 4)[1],), 0xAB, dtype=torch.uint8,
+                        device="cuda")
+        p = nv.nvfp4_route_scored_fwd(x, 4, 1, bias, workspace=ws)
+        assert (ws == 0xAB).all()
+        assert torch.equal(p.source, nv.nvfp4_route_scored_fwd(x, 4, 1, bias).source)
 
 
 def test_many_tokens():
