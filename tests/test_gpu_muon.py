@@ -112,6 +112,18 @@ def test_long_contractions(shape):
         assert torch.equal(a, nv.nvfp4_muon_update(g, m.clone()))
 
 
+@pytest.mark.parametrize("shape", [(2, 78, 8723), (1, 37, 11654), (5, 101, 2137), (300, 20, 35),
+                                   (2, 128, 4001)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+def test_ragged_widths(shape, dtype):
+    """Small rows whose width eight does not divide, over several CTAs and rounds."""
+    g, m = inputs(shape, 17, dtype)
+    want = run(g, m)
+    grad, buf = g.clone(), m.clone()
+    assert torch.equal(nv.nvfp4_muon_update(grad, buf, zero_grad=True), want)
+    assert not grad.any()
+
+
 def test_coefficients_of_each_step():
     coefs = ((3.9, -6.0, 2.9), (3.4445, -4.7750, 2.0315), (2.8, -2.9, 1.1))
     a = run(*inputs((136, 520), 8), steps=3, coefs=coefs)
