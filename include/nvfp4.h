@@ -568,7 +568,7 @@ nvfp4_status nvfp4_muon_sizes(int64_t batch, int64_t rows, int64_t cols,
  * on every call.  workspace: device, 16-byte aligned, at least
  * nvfp4_muon_sizes gives; contents on return unspecified.  On `stream`, with nothing
  * allocated: one launch for matrices with a side of at most 128 and for a few of some
- * hundred rows and columns (with it, where CTAs meet by counters, a small memset; such
+ * hundred rows or columns (with it, where CTAs meet by counters, a small memset; such
  * a launch is cooperative), else 2 + 3 steps.  Returns NVFP4_ERR_INVALID_ARG (NULL pointers,
  * overlaps, unknown flags or types, steps, mu, eps or coefs out of range),
  * _SHAPE, _ALIGN, _WORKSPACE, _ARCH, _CUDA. */

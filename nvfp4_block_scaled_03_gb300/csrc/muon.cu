@@ -917,7 +917,7 @@ __global__ void __launch_bounds__(kEwThreads) start_kernel(const MomentumArgs a)
   start_part<WIDE, FLAT>(a, gridDim.y - 1 - blockIdx.y, blockIdx.x, red);
 }
 
-// ---- one launch for all of it: matrices of some hundred rows and columns -----------
+// ---- one launch for all of it: matrices of some hundred rows or columns -----------
 // The CTAs, one an SM, go through momentum, start and the products of every step
 // together; between two products they meet at a counter: a CTA's epilogue warps tell
 // its producer that their stores have been written, which counts up for all of them,
@@ -1163,10 +1163,16 @@ struct Layout {
 constexpr int64_t kMaxSide = 1 << 20;
 
 // Whether one launch does it all: as long as an update has no more than two rounds of
-// 128 x 128 tiles.  Measured (us, one launch and a launch each): 200 x 328 90, 140; 1024 x
-// 1024 141, 195; 2048 x 2048 285, 277; 2 x [2048, 2048] 489, 355; 2048 x 4096 438, 379.
+// 128 x 128 tiles, or X X^T in tiles of 256 x 256 would leave three quarters of the SMs
+// idle through a long contraction, which the one launch splits.  Measured (us, one launch
+// and a launch each): 200 x 328 90, 140; 1024 x 1024 141, 195; 2048 x 2048 285, 277; 2 x
+// [2048, 2048] 489, 355; 2048 x 4096 438, 379; by tiles of X X^T: 3, 512 x 16384 300, 541;
+// 9, 3 x [348, 14268] 409, 652; 10, 1024 x 8192 331, 401; 16, 16 x [256, 8192] 600, 622; 20,
+// 2 x [1024, 4096] 327, 321; 32, 32 x [256, 8192] 1113, 994.
 bool takes_whole(const Layout& l, int64_t batch, int sms) {
-  return ((l.m + 127) / 128) * ((l.n + 127) / 128) * batch <= kWholeTiles * sms;
+  const int64_t t = (l.m + 255) / 256;
+  return ((l.m + 127) / 128) * ((l.n + 127) / 128) * batch <= kWholeTiles * sms ||
+         t * (t + 1) / 2 * batch * 8 <= sms;
 }
 // Its tiles' width: 64 while every CTA has one of an update (us, 64 and 128 wide: 1024 x
 // 1024 142, 168; 3 x [777, 1290] 242, 211; 2048 x 2048 432, 293).

@@ -112,6 +112,16 @@ def test_long_contractions(shape):
         assert torch.equal(a, nv.nvfp4_muon_update(g, m.clone()))
 
 
+@pytest.mark.parametrize("shape", [(3, 348, 14268), (8192, 512), (12, 200, 4001), (18, 256, 2312),
+                                   (20, 256, 2312)], ids=lambda s: "x".join(map(str, s)))
+def test_few_products_of_many_rounds(shape):
+    """One launch whose updates have more rounds of tiles than two, and the first that has not."""
+    g, m = inputs(shape, 16)
+    a = run(g, m)
+    for _ in range(3):
+        assert torch.equal(a, nv.nvfp4_muon_update(g, m.clone()))
+
+
 @pytest.mark.parametrize("shape", [(2, 78, 8723), (1, 37, 11654), (5, 101, 2137), (300, 20, 35),
                                    (2, 128, 4001)], ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
