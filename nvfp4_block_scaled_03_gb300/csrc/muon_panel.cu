@@ -6,8 +6,9 @@
 // blocks each, held in shared memory as two f16 halves from the momentum's first
 // read to the update's write.  A step is, for every CTA:
 //   G = its blocks' part of X X^T  (tensor cores, FP32 in tensor memory)
-//   the team's parts are added in a fixed order, a share of the rows by each CTA
-//     (two team barriers, through L2)
+//   the team's parts are added in a fixed order, through L2: all of them by every CTA
+//     for itself where they are few (one team barrier), else a share by each CTA, whose
+//     sums the others read (two)
 //   E E, then F and the diagonals as in muon.cu, by every CTA for itself
 //   X <- (a + d'_i) X + F X of its own blocks, in place
 // A block, rows of 128 bytes with the 128-byte swizzle, is a K-major operand of the
@@ -35,7 +36,10 @@ constexpr uint32_t kMisc = 2048;
 constexpr uint32_t kPanelSmem = 232448;
 constexpr int kBarStride = 32;           // words between two teams' counters
 constexpr int kPanelSms = 148;           // a plan has no more CTAs a matrix than this
-// Up to so many values in a team's parts every CTA adds all of them.
+// Up to so many values in a team's parts every CTA adds all of them.  A step has one
+// barrier then, in front of the reads, and nothing keeps the next step's parts of a fast
+// CTA from being stored while a slow one still reads: they go to a second set of places,
+// whose readers, a step before, are behind that barrier.
 constexpr int64_t kOwnSum = 65536;
 
 struct PanelArgs {
@@ -43,7 +47,7 @@ struct PanelArgs {
   float* momentum;
   __nv_bfloat16* update;
   float4* part;        // [teams][ctas][mp / 4][m]: a CTA's part of X X^T, 4 columns each
-  float4* sum;         // [teams][mp / 4][m]
+  float4* sum;         // [teams][mp / 4][m], or the second set of parts
   float* norm;         // [teams][ctas]
   unsigned int* bars;  // [teams], a counter each, zero at the start
   int m, mp, n;        // mp: m up to a multiple of 16
@@ -424,10 +428,11 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
   const uint32_t idesc_mm = idesc_f16(128, a.mp, false, false);
   const int chunks = (s.nb + 3) / 4;
   bool ok = true;
+  int turn = 0;  // steps done, over all matrices
 
   for (int mat = s.team; ok && mat < a.batch; mat += a.teams) {
     ok = WIDE ? load_matrix<true>(s, a, mat, first) : load_matrix<false>(s, a, mat, first);
-    for (int step = 0; ok && step < a.steps; ++step) {
+    for (int step = 0; ok && step < a.steps; ++step, ++turn) {
       const float ca = a.coefs[3 * step], cb = a.coefs[3 * step + 1], cc = a.coefs[3 * step + 2];
       // ---- X X^T of the own blocks
       fence_proxy_async_smem();
@@ -447,7 +452,8 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
       if (!ok) break;
       // this warp's columns of the part, 4 of 32 rows at a time
       const int quads = a.m * a.mp / 4;
-      float4* parts = a.part + (int64_t)s.team * a.ctas * quads;
+      float4* parts = (!a.shared_sum && (turn & 1) ? a.sum : a.part) +
+                      (int64_t)s.team * a.ctas * quads;
       if (q * 32 < a.m && 32 * h < a.mp) {
         uint32_t r[32];
         tmem_ld32(rows + 32 * h, r);
@@ -639,7 +645,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
 // How a call is spread over a device's SMs.
 struct PanelPlan {
   int m, mp, n, e_block, blocks, room, least, ctas, teams;
-  bool cluster;
+  bool cluster, shared_sum;
 };
 // wide: how many clusters of 16 a device has room for (0: not known).
 PanelPlan panel_plan(int64_t batch, int64_t rows, int64_t cols, int sms, int wide) {
@@ -665,13 +671,14 @@ PanelPlan panel_plan(int64_t batch, int64_t rows, int64_t cols, int sms, int wid
     l.ctas = std::max(l.least, spread);
   }
   l.teams = (int)std::min<int64_t>(batch, std::max(1, sms / l.ctas));
+  l.shared_sum = (int64_t)l.ctas * l.m * l.mp > kOwnSum;
   return l;
 }
 
 size_t panel_bytes(const PanelPlan& l, size_t* sum, size_t* norm, size_t* bars) {
   const size_t square = (size_t)l.m * l.mp * 4;
-  *sum = up1k(l.teams * l.ctas * square);
-  *norm = *sum + up1k(l.teams * square);
+  *sum = up1k((size_t)l.teams * l.ctas * square);
+  *norm = *sum + up1k((size_t)l.teams * (l.shared_sum ? 1 : l.ctas) * square);
   *bars = *norm + up1k((size_t)l.teams * l.ctas * 4);
   return *bars + up1k((size_t)l.teams * kBarStride * 4);
 }
@@ -683,7 +690,8 @@ bool muon_panel_fits(int64_t rows, int64_t cols) {
   return panel_plan(1, rows, cols, kPanelSms, 0).least <= kPanelSms;
 }
 
-// Enough for any plan: at most kMaxSms CTAs, so as many parts, sums and counters.
+// Enough for any plan: at most kMaxSms CTAs, so as many parts, sums (or second parts) and
+// counters.
 size_t muon_panel_workspace(int64_t rows, int64_t cols) {
   const int64_t m = std::min(rows, cols);
   const size_t square = (size_t)m * ((m + 15) / 16 * 16) * 4;
@@ -727,7 +735,7 @@ nvfp4_status muon_panel(const MuonCall& c) {
   a.ctas = l.ctas;
   a.teams = l.teams;
   a.cluster = l.cluster;
-  a.shared_sum = (int64_t)l.ctas * l.m * l.mp > kOwnSum;
+  a.shared_sum = l.shared_sum;
   a.batch = (int)c.p->batch;
   a.tall = c.p->rows > c.p->cols;
   a.nesterov = c.p->nesterov;
