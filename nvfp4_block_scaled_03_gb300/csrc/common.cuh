@@ -440,6 +440,9 @@ NVFP4_DEV void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" :::
                    "memory");
 }
+// The two halves of it, for work in between.
+NVFP4_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+NVFP4_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Address of the same shared-memory location in cluster CTA `rank`.
 NVFP4_DEV uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
   uint32_t r;

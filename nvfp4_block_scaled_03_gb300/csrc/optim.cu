@@ -144,7 +144,12 @@ __global__ void __launch_bounds__(kClusterThreads)
                             float keep, float step, float* amax) {
   __shared__ float red[kClusterThreads / 32];
   __shared__ float maxima[kClusterCtas];
+  // another CTA's shared memory is only there once that CTA runs: this one says so here
+  // and looks for the others under the loads' time, before it stores
+  cluster_arrive();
   const float m = block_max(apply_share<true>(W, U, n, keep, step), red);
+  __syncwarp();
+  cluster_wait();
   if (threadIdx.x == 0)
     st_cluster_u32(mapa_shared(smem_u32(&maxima[cluster_ctarank()]), 0), __float_as_uint(m));
   __syncwarp();
