@@ -569,15 +569,18 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine, co
     }
     float worth = best, near = 0.0f;
     if (a.group_top == 2) {
+      // without a bias the sums are good to a part of themselves, as long as their terms
+      // are: one below FP32's normal range (1.2e-38) has fewer bits or, where e^-l is
+      // infinite, counts as 0
       const bool two = next > -INFINITY;
       if (a.bias) {
         worth = two ? best + next : best;
       } else if (softmax) {
         worth = expf(best - l_most) + (two ? expf(next - l_most) : 0.0f);
-        near = 1e-5f * worth;
+        near = 1e-5f * worth + 1e-36f;
       } else {
         worth = 1.0f / (1.0f + expf(-best)) + (two ? 1.0f / (1.0f + expf(-next)) : 0.0f);
-        near = 2e-6f * worth;
+        near = 2e-6f * worth + 1e-36f;
       }
       worth = best > -INFINITY ? worth : -INFINITY;
     }

@@ -1,0 +1,57 @@
+"""The choice of groups by worths that FP32 does not order: far below a token's largest
+logit, where exponentials lose their bits, and beside biases that swallow a score's."""
+import math
+
+import pytest
+import torch
+
+import route_reference as R
+
+pytestmark = pytest.mark.gpu
+nv = None
+INF = math.inf
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _binding():
+    global nv
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from nvfp4_block_scaled_03_gb300 import binding
+    nv = binding
+
+
+def same(x, top, score, bias, groups, kept, group_top=2):
+    p = nv.nvfp4_route_scored_fwd(x, top, score, bias, groups, kept, group_top)
+    want = R.choose(x, top, score, bias, groups, kept, group_top)
+    wrong = (p.expert.long() != want).any(1)
+    assert not wrong.any(), f"{int(wrong.sum())} of {x.shape[0]} tokens"
+    return p
+
+
+def close_pairs(tokens, groups, size, centre, spread, seed):
+    """Logits of groups whose two best have nearly the same sum of exponentials."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    c = centre + spread * torch.rand(tokens, 1, 1, generator=g, device="cuda").double()
+    share = 0.1 + 0.8 * torch.rand(tokens, groups, 1, generator=g, device="cuda").double()
+    sure = 1e-3 * torch.randn(tokens, groups, 1, generator=g, device="cuda").double()
+    x = (c - 8).repeat(1, groups, size)
+    x[:, :, :1] = c + torch.log(share) + sure
+    x[:, :, 1:2] = c + torch.log1p(-share) + sure
+    return x.reshape(tokens, groups * size).float()
+
+
+@pytest.mark.parametrize("centre", [-103.0, -98.0, -90.0, -60.0, -10.0])
+def test_softmax_groups_far_below_the_maximum(centre):
+    """One group near the maximum, three kept: the others' order is by sums of
+    exponentials that FP32 holds in a few bits or not at all."""
+    x = close_pairs(20000, 8, 4, centre, 5.0, 1)
+    x[:, 4:8] = torch.tensor([0.0, -1.0, -3.0, -2.0], device="cuda")
+    same(x, 10, 0, None, 8, 3)
+
+
+@pytest.mark.parametrize("centre", [-88.9, -88.0, -60.0, -10.0])
+def test_sigmoid_groups_at_the_end_of_the_range(centre):
+    """e^-l is infinite in FP32 from 88.73 on: the sum of a group's two scores is one
+    score then, whatever the other."""
+    same(close_pairs(20000, 8, 4, centre, 1.0, 2), 10, 1, None, 8, 3)
