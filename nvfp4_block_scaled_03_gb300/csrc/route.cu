@@ -584,7 +584,9 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine, co
       }
       worth = best > -INFINITY ? worth : -INFINITY;
     }
-    if (a.bias) near = 2.0f * near0 + 1e-6f * (fabsf(best) + (a.group_top == 2 ? fabsf(next) : 0.0f));
+    if (a.bias)
+      near = 2.0f * near0 + 1e-6f * ((best > -INFINITY ? fabsf(best) : 0.0f) +
+                                     (a.group_top == 2 && next > -INFINITY ? fabsf(next) : 0.0f));
     const int g = lane / a.lanes;
     int rank = 0;
 #pragma unroll 4

@@ -55,3 +55,42 @@ def test_sigmoid_groups_at_the_end_of_the_range(centre):
     """e^-l is infinite in FP32 from 88.73 on: the sum of a group's two scores is one
     score then, whatever the other."""
     same(close_pairs(20000, 8, 4, centre, 1.0, 2), 10, 1, None, 8, 3)
+
+
+def test_groups_by_one_or_by_two_and_none_open():
+    """Groups of a single open expert, of none and of several side by side, each with
+    and without a bias."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(3000, 64, generator=g, device="cuda") * 2
+    x[torch.rand(3000, 64, generator=g, device="cuda") < 0.75] = -INF
+    bias = torch.randn(64, generator=g, device="cuda") * 0.1
+    for score in (0, 1):
+        for b in (None, bias * (1.0 if score else 0.1)):
+            for group_top in (1, 2):
+                same(x, 5, score, b, 16, 4, group_top)
+                same(x, 5, score, b, 32, 7, group_top)
+
+
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+def test_groups_of_one_expert_are_as_clear_as_by_one(score):
+    """The same choice whether one or two experts count where a group has one, and not
+    token by token in 64 bits (eight times as long): at most three times the time."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(65536, 32, generator=g, device="cuda") * 1.5
+    bias = torch.randn(32, generator=g, device="cuda") * (0.05 if score else 0.01)
+
+    def call(group_top):
+        p = nv.nvfp4_route_scored_fwd(x, 4, score, bias, 32, 8, group_top)
+        best = INF
+        for _ in range(20):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            nv.nvfp4_route_scored_fwd(x, 4, score, bias, 32, 8, group_top, plan=p)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return p, best
+
+    (p, one), (q, two) = call(1), call(2)
+    assert torch.equal(p.expert, q.expert) and torch.equal(p.weight, q.weight)
+    assert two <= 3 * one, (two, one)
