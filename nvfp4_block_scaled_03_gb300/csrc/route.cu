@@ -596,11 +596,12 @@ NVFP4_DEV void choose_scored(const RouteArgs& a, int64_t t, const Share mine, co
     }
     bool keep = rank < a.kept;
     if (a.bias || a.group_top == 2) {
-      const float in = redux_min(keep ? worth : INFINITY);
-      const float out = redux_max(keep ? -INFINITY : worth);
+      // clear: every kept group lies above every other, each at its own margin's end (one
+      // with large biases that cancel is known less well than the groups next to it)
+      const float in = redux_min(keep ? worth - 0.5f * near : INFINITY);
+      const float out = redux_max(keep ? -INFINITY : worth + 0.5f * near);
       if (out > -INFINITY) {
-        const float margin = redux_max(worth == in || worth == out ? near : 0.0f);
-        doubt = !(in - out > margin);
+        doubt = !(in > out);
         if (doubt && a.bias && !softmax)
           doubt = !groups_exact<NI, WIDE>(a, t, mine, key, near0, keep);
       }

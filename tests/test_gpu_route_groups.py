@@ -94,3 +94,15 @@ def test_groups_of_one_expert_are_as_clear_as_by_one(score):
     (p, one), (q, two) = call(1), call(2)
     assert torch.equal(p.expert, q.expert) and torch.equal(p.weight, q.weight)
     assert two <= 3 * one, (two, one)
+
+
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+def test_a_large_bias_beside_its_opposite(score):
+    """Groups whose two best have biases that cancel: their worth is known less well than
+    that of the groups next to the last kept, and can lie behind theirs."""
+    t, groups = 40000, 8
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(t, 2 * groups, generator=g, device="cuda") * 1e-4
+    bias = torch.zeros(2 * groups, device="cuda")
+    bias[::4], bias[1::4] = 1000.0, -1000.0  # every other group
+    same(x, 2, score, bias, groups, 4)
