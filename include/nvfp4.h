@@ -526,7 +526,7 @@ nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t fl
  * iteration of products (Newton-Schulz).  For each of `batch` matrices
  * [rows, cols]:
  *   V <- mu V + G,   U = G + mu V (nesterov) or V
- *   X <- U / max(||U||_F, eps)
+ *   X <- U / max(||U||_F, eps, 1e-18)
  *   `steps` times, with the step's (a, b, c):
  *     A = X X^T,  B = b A + c A A,  X <- a X + B X
  *     (rows > cols: A = X^T X,  X <- a X + X B, the same polynomial)
@@ -537,7 +537,7 @@ nvfp4_status nvfp4_sgd_step(float* W, float* G, int64_t n, float lr, uint32_t fl
  * about 1.5e-3 of that of 64 bits (2-norm of the difference) plus its one
  * rounding to bf16.  A matrix of zeros gives zeros.  NaN or infinities in a
  * matrix make its update (and momentum) unspecified, not the others'; a norm's
- * squares are summed in FP32, so norms below 1e-18 or above 1e18 count as 0 or
+ * squares are summed in FP32, so norms below 1e-18 count as that, and above 1e18 as
  * infinity.  The entries of X, A and B must stay below 16 in magnitude, which they
  * do for every input with coefficients that keep X's singular values below 2 and
  * |b s + c s^2| below 16 on their squares s, as the usual (3.4445, -4.7750,

@@ -837,7 +837,7 @@ NVFP4_DEV void start_part(const MomentumArgs& a, int mat, int part, float* red) 
   float sum = 0.0f;
   for (int p = threadIdx.x; p < a.parts; p += blockDim.x)
     sum += __ldcg(a.partial + (int64_t)mat * a.parts + p);
-  const float scale = kScale / fmaxf(sqrtf(block_sum(sum, red)), a.eps);
+  const float scale = start_scale(block_sum(sum, red), a.eps);
   const Quads q = quads_of(a, mat);
   const int64_t to = (int64_t)mat * a.padded, stride = (int64_t)a.parts * blockDim.x;
   for (int64_t i = (int64_t)part * blockDim.x + threadIdx.x; i < q.count; i += kEwUnroll * stride) {

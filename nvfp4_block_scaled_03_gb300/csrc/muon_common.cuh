@@ -32,6 +32,13 @@ namespace {
 
 constexpr float kScale = 4096.0f, kUnscale = 1.0f / 4096.0f;
 
+// What U is multiplied by to give X with the operands' scale.  Squares in FP32 lose a norm
+// below 1e-18, which counts as that: U's entries are smaller then, X's at most about 1, and
+// the factor is finite for any eps.
+NVFP4_DEV float start_scale(float squares, float eps) {
+  return kScale / fmaxf(fmaxf(sqrtf(squares), eps), 1e-18f);
+}
+
 // MN-major operand tile: rows of 128 bytes (64 along M or N) for each k with the
 // 128-byte swizzle, 8 rows (1024 bytes) a swizzle atom; the next 64 of M or N lie
 // `next` bytes further.

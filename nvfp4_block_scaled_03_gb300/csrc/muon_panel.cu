@@ -285,7 +285,7 @@ NVFP4_DEV bool load_matrix(Panel& s, const PanelArgs& a, int mat, int first) {
     for (int c = threadIdx.x; c < a.ctas; c += kPanelThreads) t += __ldcg(norm + c);
     total = block_total(t, s.red);
   }
-  const float scale = kScale / fmaxf(sqrtf(total), a.eps);
+  const float scale = start_scale(total, a.eps);
   for_pieces(s, a, first, [&](int, int, uint32_t at) {
     const uint4 h = *reinterpret_cast<const uint4*>(s.hi + at);
     const uint4 l = *reinterpret_cast<const uint4*>(s.lo + at);
