@@ -21,7 +21,7 @@ rounding's random words, would be the same in every replay.
 
 The masters take plain SGD (`sgd`), or the matrices, each expert's by itself, the
 orthogonalised momentum and the vectors SGD (`muon`), whose last pass gives the
-weights' amaxes to the next forward's quantisation.
+weights' amaxes to the next forward's quantisation where that forward is told so.
 
 ``python -m nvfp4_block_scaled_03_gb300.moe`` trains a small block for a few
 steps on a GB300 and prints the loss.
@@ -76,7 +76,7 @@ class MoEBlock:
         self.matrices = {"router": (experts, hidden), "gate_proj": (experts, ffn, hidden),
                          "up_proj": (experts, ffn, hidden), "down_proj": (experts, hidden, ffn)}
         # the weights' amaxes as their last step gave them, in buffers that stay (a captured
-        # forward reads what the replay before has written), and of which weight they are
+        # step reads what the replay before has written), and of which weight they are
         self.momentum, self.stepped = {}, {}
         self.amax = {k: torch.zeros(1, device=device) for k in self.matrices if k != "router"}
         self.operand_ids = torch.arange(6, device=device)
@@ -101,14 +101,22 @@ class MoEBlock:
                                          **self.choice)
 
     def _known_amax(self, name):
-        """The amax that a weight's last step gave, unless the weight was changed since."""
+        """The amax that a weight's last step gave, unless torch knows of a change since."""
         w = self.params[name]
         same, version = self.stepped.get(name, (None, None))
         return self.amax[name] if same is w and version == w._version else None
 
-    def forward(self, x: torch.Tensor):
+    def forward(self, x: torch.Tensor, after_muon: bool = False):
         """y [tokens, hidden] of x (bf16 or FP32); what the backward reads is
-        kept in `self.saved`."""
+        kept in `self.saved`.
+
+        after_muon: the experts' weights are as the block's own last `muon` left them, and
+        their quantisation takes the amaxes of that step instead of reading them once more.
+        That is the caller's word: a change in place that torch sees, `sgd` or another tensor
+        end it by themselves, but not a change through `.data`, nor a graph's replay that
+        changes the weights in any other way than by `muon`.  A graph captured with it takes
+        the amaxes in every replay, so it has to hold the whole step, and nothing else may
+        change the weights between its replays."""
         p, s = self.params, {}
         s["x"] = x
         _, s["h"] = nv.nvfp4_residual_norm_fwd(x, w_pre=p["w_in"], eps=self.eps)
@@ -120,7 +128,7 @@ class MoEBlock:
         qx, s["qx_col"] = self._both(xe)
         for name in ("gate_proj", "up_proj", "down_proj"):
             s[name] = nv.nvfp4_quantize(p[name], nv.BLOCK_16X16, nv.EMIT_T,
-                                        amax=self._known_amax(name))
+                                        amax=self._known_amax(name) if after_muon else None)
         s["G"] = nv.nvfp4_group_gemm(qx, s["gate_proj"], *groups)
         s["U"] = nv.nvfp4_group_gemm(qx, s["up_proj"], *groups)
         H, row, col = nv.nvfp4_swiglu_fwd(s["G"], s["U"], seed=self.seed)
@@ -224,7 +232,7 @@ def main(steps: int = 30, tokens: int = 500, hidden: int = 512, ffn: int = 1024,
     target = x + torch.randn(tokens, hidden, device="cuda")
     losses = []
     for step in range(steps):
-        diff = block.forward(x) - target
+        diff = block.forward(x, after_muon=muon_lr is not None) - target
         losses.append((diff * diff).mean().item())
         block.backward(diff * (2.0 / diff.numel() * hidden), step)
         if muon_lr is None:
