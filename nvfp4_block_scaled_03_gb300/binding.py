@@ -526,11 +526,12 @@ def mlp_operand(M, D, F, saved, workspace, which) -> QTensor:
 ZERO_GRAD = 16
 
 
-def _changed(t):
-    """Tells torch that a call wrote to a tensor in place, as its own operations do
+def _changed(*tensors):
+    """Tells torch that a call wrote to tensors in place, as its own operations do
     (a weight's known amax goes by it, and autograd's check of what it saved)."""
-    if not t.is_inference():
-        torch.autograd.graph.increment_version(t)
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
 
 
 def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool = False,
@@ -552,7 +553,7 @@ def nvfp4_sgd_step(W: torch.Tensor, G: torch.Tensor, lr: float, zero_grad: bool 
                               ZERO_GRAD if zero_grad else 0, _ptr(amax), _ptr(workspace),
                               workspace.numel() if workspace is not None else 0,
                               _stream(stream)), "nvfp4_sgd_step")
-    _changed(W)
+    _changed(W, G if zero_grad else None, amax)
     return W
 
 
@@ -662,6 +663,7 @@ def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.
     kind = _DTYPES.get(grad.dtype)
     if kind is None:
         raise TypeError(f"grad must be bf16 or fp32, got {grad.dtype}")
+    given = out
     shape = grad.shape
     if len(shape) < 2 or grad.numel() == 0:
         raise ValueError("grad must be a matrix or a stack of matrices, not empty")
@@ -687,6 +689,7 @@ def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.
                                workspace.numel(), _current(grad))
     if st:
         raise NVFP4Error(st, "nvfp4_muon_update")
+    _changed(momentum, grad if zero_grad else None, given)
     return out
 
 
@@ -702,6 +705,7 @@ def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: fl
     tensor that its quantisation takes."""
     _cuda(W, _F32, "W")
     _cuda(update, _BF16, "update", W.shape)
+    given = amax
     if amax is None:
         amax = torch.empty(1, dtype=_F32, device=W.device)
     else:
@@ -716,7 +720,7 @@ def nvfp4_muon_apply(W: torch.Tensor, update: torch.Tensor, lr: float, scale: fl
                               _current(W))
     if st:
         raise NVFP4Error(st, "nvfp4_muon_apply")
-    _changed(W)
+    _changed(W, given)
     return amax
 
 
@@ -888,6 +892,7 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
     kind, tokens, experts, ld = _logits(logits)
     if workspace is None and tokens <= 64:
         workspace = _untouched(logits)
+    given = plan
     if plan is not None:
         _together(logits, plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row,
                   plan.source)
@@ -904,6 +909,8 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
                                     workspace.numel(), _current(logits))
     if st:
         raise NVFP4Error(st, "nvfp4_route_scored_fwd")
+    if given is not None:
+        _changed(plan.expert, plan.weight, plan.sizes, plan.offsets, plan.row, plan.source)
     return plan
 
 
@@ -918,6 +925,7 @@ def nvfp4_route_scored_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch
     _cuda(plan.expert, _I32, "expert", (tokens, top))
     _cuda(plan.weight, _F32, "weight", (tokens, top))
     _cuda(dweight, _F32, "dweight", (tokens, top))
+    given = dlogits
     if dlogits is None:
         dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
     else:
@@ -930,6 +938,7 @@ def nvfp4_route_scored_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch
                                     _current(logits))
     if st:
         raise NVFP4Error(st, "nvfp4_route_scored_bwd")
+    _changed(given)
     return dlogits
 
 
@@ -945,6 +954,7 @@ def nvfp4_route_balance(sizes: torch.Tensor, bias: torch.Tensor, rate: float) ->
                                  _current(sizes))
     if st:
         raise NVFP4Error(st, "nvfp4_route_balance")
+    _changed(bias)
     return bias
 
 
