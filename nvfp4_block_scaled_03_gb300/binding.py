@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import operator
 import os
 from dataclasses import dataclass, field
 
@@ -639,15 +640,28 @@ def muon_sizes(batch, rows, cols) -> int:
     return w.value
 
 
+def _floats(v):
+    """A number, or the numbers of a sequence, as floats."""
+    if isinstance(v, (list, tuple)) or getattr(v, "ndim", 0):
+        return tuple([_floats(x) for x in v])
+    return float(v)
+
+
+# What is kept goes by the arguments' values: plain numbers alone, for a tensor stays the
+# same object when its value changes.
 @functools.lru_cache(maxsize=64)
 def _coefs(coefs, steps):
     """[steps][3] for the library: one triple for every step, or one for each."""
     if not 1 <= steps <= MUON_MAX_STEPS:
         raise ValueError(f"steps must be 1 to {MUON_MAX_STEPS}")
-    rows = [coefs] * steps if len(coefs) == 3 and not hasattr(coefs[0], "__len__") else coefs
-    if len(rows) != steps or any(len(r) != 3 for r in rows):
+
+    def triple(r):
+        return isinstance(r, tuple) and len(r) == 3 and all(isinstance(v, float) for v in r)
+
+    rows = (coefs,) * steps if triple(coefs) else coefs
+    if not (isinstance(rows, tuple) and len(rows) == steps and all(map(triple, rows))):
         raise ValueError("coefs must be one triple, or one for each step")
-    flat = [float(v) for r in rows for v in r]
+    flat = [v for r in rows for v in r]
     return (C.c_float * len(flat))(*flat)
 
 
@@ -680,8 +694,9 @@ def nvfp4_muon_update(grad: torch.Tensor, momentum: torch.Tensor, mu: float = 0.
     else:
         _cuda(workspace, _U8, "workspace")
     _together(grad, momentum, out, workspace)
+    steps = operator.index(steps)
     if coefs is not MUON_COEFS:  # lists and arrays as well
-        coefs = tuple([tuple(c) if hasattr(c, "__len__") else c for c in coefs])
+        coefs = _floats(coefs)
     p = MuonParams(batch, rows, cols, kind, 1 if nesterov else 0, steps, mu, eps,
                    _coefs(coefs, steps))
     st = lib.nvfp4_muon_update(p, grad.data_ptr(), momentum.data_ptr(), out.data_ptr(),
@@ -828,6 +843,7 @@ def nvfp4_route_fwd(logits: torch.Tensor, top: int, mode: int = ROUTE_CHOSEN,
     """Choose each token's `top` experts and order the rows by expert (see
     nvfp4_route_fwd in nvfp4.h)."""
     kind, tokens, experts, ld = _logits(logits)
+    top = operator.index(top)
     plan, workspace = _plan_buffers(tokens, experts, top, plan, workspace, logits)
     st = lib.nvfp4_route_fwd(logits.data_ptr(), kind, tokens, experts, ld, top, mode,
                              plan.expert.data_ptr(), plan.weight.data_ptr(),
@@ -874,9 +890,16 @@ def _untouched(t):
     return _small_workspace[device]
 
 
-@functools.lru_cache(maxsize=256)
-def _route_params(*fields):
-    return RouteParams(*fields)
+_route_params = functools.lru_cache(maxsize=256)(RouteParams)
+
+
+def _scored(tokens, experts, ld, kind, top, score, renormalise, groups, kept, group_top, scale):
+    """The parameters of a scored routing, kept by their values: plain numbers alone, for
+    a tensor stays the same object when its value changes."""
+    index = operator.index
+    return _route_params(tokens, experts, ld, kind, top, index(score), 1 if renormalise else 0,
+                         index(groups), index(groups if kept is None else kept),
+                         index(group_top), float(scale))
 
 
 @_on_device
@@ -890,6 +913,7 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
     groups of experts, and order the rows by expert (see nvfp4_route_scored_fwd in
     nvfp4.h).  groups_kept None: all of them."""
     kind, tokens, experts, ld = _logits(logits)
+    top = operator.index(top)
     if workspace is None and tokens <= 64:
         workspace = _untouched(logits)
     given = plan
@@ -900,8 +924,8 @@ def nvfp4_route_scored_fwd(logits: torch.Tensor, top: int, score: int = SCORE_SI
     if bias is not None:
         _cuda(bias, _F32, "bias", (experts,))
     _together(logits, bias, workspace)
-    p = _route_params(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, groups,
-                      groups if groups_kept is None else groups_kept, group_top, scale)
+    p = _scored(tokens, experts, ld, kind, top, score, renormalise, groups, groups_kept, group_top,
+                scale)
     st = lib.nvfp4_route_scored_fwd(p, logits.data_ptr(), _ptr(bias), plan.expert.data_ptr(),
                                     plan.weight.data_ptr(), plan.sizes.data_ptr(),
                                     plan.offsets.data_ptr(), plan.row.data_ptr(),
@@ -931,8 +955,7 @@ def nvfp4_route_scored_bwd(logits: torch.Tensor, plan: RoutePlan, dweight: torch
     else:
         _cuda(dlogits, logits.dtype, "dlogits", (tokens, experts))
     _together(logits, plan.expert, plan.weight, dweight, dlogits)
-    p = _route_params(tokens, experts, ld, kind, top, score, 1 if renormalise else 0, 1, 1, 1,
-                      scale)
+    p = _scored(tokens, experts, ld, kind, top, score, renormalise, 1, 1, 1, scale)
     st = lib.nvfp4_route_scored_bwd(p, logits.data_ptr(), plan.expert.data_ptr(),
                                     plan.weight.data_ptr(), dweight.data_ptr(), dlogits.data_ptr(),
                                     _current(logits))
