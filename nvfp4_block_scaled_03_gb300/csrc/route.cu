@@ -75,7 +75,6 @@ struct RouteArgs {
   // backward
   const float* dweight;
   void* dlogits;
-  float inv_scale;
 };
 
 template <bool WIDE>
@@ -909,10 +908,10 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) 
     }
   }
   float apart = 0.0f;
+  const float share = w / a.scale;  // not times 1 / c, which the least c make infinite
   if (a.renorm || a.score == NVFP4_SCORE_SOFTMAX)
     for (int j = 0; j < a.top; ++j)
-      apart += (__shfl_sync(0xFFFFFFFFu, w, j) * a.inv_scale) *
-               (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
+      apart += __shfl_sync(0xFFFFFFFFu, share, j) * (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
   else
     apart = dw;
   if (a.score == NVFP4_SCORE_SIGMOID && e >= 0)
@@ -1327,7 +1326,7 @@ static RouteArgs plain_route(int32_t mode) {
   a.mode = mode;
   a.score = NVFP4_SCORE_SOFTMAX;
   a.renorm = mode == NVFP4_ROUTE_CHOSEN;
-  a.inv_scale = 1.0f;
+  a.scale = 1.0f;
   return a;
 }
 
@@ -1373,7 +1372,6 @@ static nvfp4_status scored_args(const nvfp4_route_params* p, const float* bias, 
   a->lanes = 32 / p->groups;
   a->per = (a->group_size + a->lanes - 1) / a->lanes;
   a->scale = p->scale;
-  a->inv_scale = 1.0f / p->scale;
   return NVFP4_OK;
 }
 
