@@ -30,3 +30,18 @@ def test_every_maximum_arrives(n):
     got = [nv.nvfp4_muon_apply(w, u, 0.1) for w in weights]  # one launch right behind another
     assert torch.cat(got).tolist() == [2.0 + k for k in range(len(weights))]
     nv.check_device_errors()
+
+
+def test_without_a_maximum():
+    """The same step through the library's entry without an amax, at both sizes of it."""
+    for n in (1, 5, 65541, 1000003):
+        g = torch.Generator(device="cuda").manual_seed(n)
+        w = torch.randn(n, generator=g, device="cuda")
+        u = torch.randn(n, generator=g, device="cuda").bfloat16()
+        a, b = w.clone(), w.clone()
+        nv.nvfp4_muon_apply(a, u, 0.02, 3.0, 0.1)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert nv.lib.nvfp4_muon_apply(b.data_ptr(), u.data_ptr(), n, 0.02, 3.0, 0.1, None, None, 0,
+                                       stream) == 0
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
