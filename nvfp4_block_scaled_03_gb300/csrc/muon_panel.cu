@@ -38,16 +38,17 @@ constexpr int kBarStride = 32;           // words between two teams' counters
 constexpr int kPanelSms = 148;           // a plan has no more CTAs a matrix than this
 // Up to so many values in a team's parts every CTA adds all of them.  A step has one
 // barrier then, in front of the reads, and nothing keeps the next step's parts of a fast
-// CTA from being stored while a slow one still reads: they go to a second set of places,
-// whose readers, a step before, are behind that barrier.
+// CTA from being stored while a slow one still reads: every other step's go to a second
+// set of places, whose readers, a step before, are behind that barrier.  (Two matrices'
+// steps have the barrier of the norm between them.)
 constexpr int64_t kOwnSum = 65536;
 
 struct PanelArgs {
   void* grad;
   float* momentum;
   __nv_bfloat16* update;
-  float4* part;        // [teams][ctas][mp / 4][m]: a CTA's part of X X^T, 4 columns each
-  float4* sum;         // [teams][mp / 4][m], or the second set of parts
+  float4* part[2];     // [teams][ctas][mp / 4][m]: a CTA's part of X X^T, 4 columns each
+  float4* sum;         // [teams][mp / 4][m]
   float* norm;         // [teams][ctas]
   unsigned int* bars;  // [teams], a counter each, zero at the start
   int m, mp, n;        // mp: m up to a multiple of 16
@@ -428,11 +429,10 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
   const uint32_t idesc_mm = idesc_f16(128, a.mp, false, false);
   const int chunks = (s.nb + 3) / 4;
   bool ok = true;
-  int turn = 0;  // steps done, over all matrices
 
   for (int mat = s.team; ok && mat < a.batch; mat += a.teams) {
     ok = WIDE ? load_matrix<true>(s, a, mat, first) : load_matrix<false>(s, a, mat, first);
-    for (int step = 0; ok && step < a.steps; ++step, ++turn) {
+    for (int step = 0; ok && step < a.steps; ++step) {
       const float ca = a.coefs[3 * step], cb = a.coefs[3 * step + 1], cc = a.coefs[3 * step + 2];
       // ---- X X^T of the own blocks
       fence_proxy_async_smem();
@@ -452,8 +452,7 @@ __global__ void __launch_bounds__(kPanelThreads, 1) panel_kernel(const PanelArgs
       if (!ok) break;
       // this warp's columns of the part, 4 of 32 rows at a time
       const int quads = a.m * a.mp / 4;
-      float4* parts = (!a.shared_sum && (turn & 1) ? a.sum : a.part) +
-                      (int64_t)s.team * a.ctas * quads;
+      float4* parts = a.part[step & 1] + (int64_t)s.team * a.ctas * quads;
       if (q * 32 < a.m && 32 * h < a.mp) {
         uint32_t r[32];
         tmem_ld32(rows + 32 * h, r);
@@ -721,7 +720,8 @@ nvfp4_status muon_panel(const MuonCall& c) {
   a.grad = c.grad;
   a.momentum = c.momentum;
   a.update = c.update;
-  a.part = reinterpret_cast<float4*>(w);
+  a.part[0] = reinterpret_cast<float4*>(w);
+  a.part[1] = reinterpret_cast<float4*>(l.shared_sum ? w : w + sum);
   a.sum = reinterpret_cast<float4*>(w + sum);
   a.norm = reinterpret_cast<float*>(w + norm);
   a.bars = reinterpret_cast<unsigned int*>(w + bars);
