@@ -75,6 +75,7 @@ struct RouteArgs {
   // backward
   const float* dweight;
   void* dlogits;
+  float lift, inv_scale;  // 1 / scale as a product: a power of two that keeps it in range
 };
 
 template <bool WIDE>
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(kThreads) route_bwd_kernel(const RouteArgs a) 
     }
   }
   float apart = 0.0f;
-  const float share = w / a.scale;  // not times 1 / c, which the least c make infinite
+  const float share = (w * a.lift) * a.inv_scale;
   if (a.renorm || a.score == NVFP4_SCORE_SOFTMAX)
     for (int j = 0; j < a.top; ++j)
       apart += __shfl_sync(0xFFFFFFFFu, share, j) * (dw - __shfl_sync(0xFFFFFFFFu, dw, j));
@@ -1326,7 +1327,7 @@ static RouteArgs plain_route(int32_t mode) {
   a.mode = mode;
   a.score = NVFP4_SCORE_SOFTMAX;
   a.renorm = mode == NVFP4_ROUTE_CHOSEN;
-  a.scale = 1.0f;
+  a.lift = a.inv_scale = 1.0f;
   return a;
 }
 
@@ -1372,6 +1373,8 @@ static nvfp4_status scored_args(const nvfp4_route_params* p, const float* bias, 
   a->lanes = 32 / p->groups;
   a->per = (a->group_size + a->lanes - 1) / a->lanes;
   a->scale = p->scale;
+  a->lift = p->scale < 0x1p-64f ? 0x1p64f : p->scale > 0x1p64f ? 0x1p-64f : 1.0f;
+  a->inv_scale = 1.0f / (p->scale * a->lift);
   return NVFP4_OK;
 }
 
