@@ -28,13 +28,15 @@
 // in bf16 3e-1); rounding it to bf16 costs 1.7e-3.
 //
 // What bounds it, and measured.  Large matrices: the tensor cores under the power cap
-// (14336 x 4096, 3.95 TFLOP: 2615 to 2930 us with the card, 1.35 to 1.5 PF/s; cuBLAS holds
-// 1.72 in a loop of seconds): X X^T 145 us (2 rounds of tiles where 1.8 would do), E E 50,
-// an update 285, momentum and start 185 at 7.2 TB/s.  Stacks of smaller ones: what an SM
-// takes in of operands and of X's halves (64 x [1024, 2048]: 2550 us, an update's tensor
-// cores 52 % busy, DRAM 4.5 TB/s), 450 of it momentum and start.  One
-// matrix of 1024 x 1024: 137 us, 15 products of 8: 3.4 us for 16 stages at what an SM takes
-// in (24 KB each), 2.5 for the meeting and the stores before it, 1.5 for the epilogue.
+// (14336 x 4096, 3.95 TFLOP: 2615 to 2985 us by card and by how long the cap has held, the
+// last at a median of 1511 MHz in a loop of seconds, 1.32 to 1.5 PF/s; cuBLAS holds 1.72 in
+// such a loop): X X^T 145 us (2 rounds of tiles where 1.8 would do), E E 50, an update 285,
+// momentum and start 185 at 7.2 TB/s.  Stacks of smaller ones: what an SM takes in of
+// operands and of X's halves (64 x [1024, 2048]: 2510 to 2855 us, the last at a median of
+// 1616 MHz in a loop of seconds; an update's tensor cores 52 % busy, DRAM 4.5 TB/s), 450 of
+// it momentum and start.  One matrix of 1024 x 1024: 137 us, 15 products of 8: 3.4 us for 16
+// stages at what an SM takes in (24 KB each), 2.5 for the meeting and the stores before it,
+// 1.5 for the epilogue.
 #include <cmath>
 
 #include "muon_common.cuh"

@@ -19,10 +19,10 @@
 // quarter of tensor memory, and with it every warp, has a share of the columns of F X.
 //
 // What bounds it, and measured: a step's chain of waits.  64 x 4096 on a cluster of 16
-// takes 50 us (146 by the kernels of muon.cu, floor 0.5): 6 to load, then five steps of 8:
-// 1.0 for X X^T, 3.4 until all CTAs have E (two meetings, parts and sums through L2), 0.5
-// for E E, 0.9 for F, 2.0 for F X.  Stacks go through it in rounds of what fits the SMs:
-// 57 x [102, 1136] 142 us (199), 64 x [100, 9000] 965 (1143; floor 118).
+// takes 49 us (146 by the kernels of muon.cu, floor 0.5): 6 to load, then five steps of 8:
+// 1.0 for X X^T, 3.4 until all CTAs have E (one meeting, 16 parts through L2), 0.5 for
+// E E, 0.9 for F, 2.0 for F X.  Stacks go through it in rounds of what fits the SMs:
+// 57 x [102, 1136] 146 us (199), 64 x [100, 9000] 965 to 1030 (1143; floor 118).
 #include <algorithm>
 
 #include "muon_common.cuh"
@@ -41,6 +41,10 @@ constexpr int kPanelSms = 148;           // a plan has no more CTAs a matrix tha
 // CTA from being stored while a slow one still reads: every other step's go to a second
 // set of places, whose readers, a step before, are behind that barrier.  (Two matrices'
 // steps have the barrier of the norm between them.)
+// Measured (us; all of them by every CTA, a share each): clusters below the limit
+// 16 x 2000 33, 37; 128 x 256 on 4 CTAs 53, 60; at it 64 x 4096 on 16 48.8, 49.5; beyond
+// 128 x 512 on 8 60.4, 59.4; 80 x 4096 on 16 76, 58.  Teams of many CTAs would have the
+// shares from less on: 16 x 60000 on 152 107, 85.
 constexpr int64_t kOwnSum = 65536;
 
 struct PanelArgs {

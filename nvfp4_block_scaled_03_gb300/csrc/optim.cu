@@ -160,6 +160,10 @@ __global__ void __launch_bounds__(kClusterThreads)
     *amax = most;
   }
 }
+// Measured (us, one launch on a cluster and two on all SMs): calls one behind another 7.7
+// and 10.0 for 4096 to 2^18 elements, 8.2 and 10.0 for 2^19; a call waited for 17.5 and
+// 19.5, at 2^18 19.0 and 19.8, at 2^19 20.7 and 19.9.  In a replayed graph, where a launch
+// costs less, the two are the quicker from 4096 on: 3.3 and 3.1, at 2^18 4.4 and 3.4.
 constexpr int64_t kClusterElements = 1 << 18;
 
 // Launches it; false: the device has no room for such a cluster.
