@@ -210,8 +210,9 @@ class MoEBlock:
                                           self.momentum[name].view(shape), mu, zero_grad=True)
             nv.nvfp4_muon_apply(w.view(shape), update, lr, 0.2 * math.sqrt(max(shape[-2:])), decay,
                                 self.amax.get(name))
-            if name in self.amax and not w.is_inference():
-                self.stepped[name] = w, w._version
+            if name in self.amax and not (w.is_inference()
+                                          or torch.cuda.is_current_stream_capturing()):
+                self.stepped[name] = w, w._version  # a step that is captured has not run
 
     def balance(self, rate: float):
         """Moves the bias of a scored router by the last forward's loads."""

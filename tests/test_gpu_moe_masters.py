@@ -126,3 +126,14 @@ def test_a_whole_step_captured_with_its_amaxes():
         for name, w in block.params.items():
             assert torch.equal(w, eager.params[name]), name
     nv.check_device_errors()
+
+
+def test_a_step_that_was_only_captured():
+    """It has not run: a change of the weights before it has still ended their amaxes."""
+    block, x = stepped_block()
+    for k in WEIGHTS:
+        block.params[k].mul_(3)
+    graph, _ = captured(lambda: block.muon(0.02, 0.01))
+    assert torch.equal(block.forward(x, after_muon=True), fresh(block, x))
+    graph.replay()
+    assert torch.equal(block.forward(x, after_muon=True), fresh(block, x))
