@@ -48,8 +48,8 @@ def test_a_step_leaves_the_parts_of_the_one_before(shape):
                                          ((200, 20, 7000), 2), ((16, 60000), 5)],
                          ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else str(s))
 def test_repeats_beside_a_busy_memory(shape, steps):
-    """The same bits alone and while another stream moves memory, over stacks whose rounds
-    go on with either set of parts."""
+    """The same bits alone and while another stream moves memory, over stacks whose teams
+    take several matrices with odd and even numbers of steps."""
     grad, momentum = inputs(shape, 2)
     want_buf = momentum.clone()
     want = nv.nvfp4_muon_update(grad, want_buf, steps=steps)
